@@ -18,6 +18,8 @@ if the library is not built, every call raises.
 
     fa = FaPlan(max_B_u, max_B_c, H, L_q, L_kv, head_dim)   # IKBO target attention
     O = fa.forward(Q, K, V, map)
+
+    from broadcast_gemm_amd.history import UserHistories    # target attention over cached 4-bit histories
 """
 from __future__ import annotations
 
@@ -36,6 +38,9 @@ IKBO_ERR_HIP = -3
 IKBO_ERR_ALIGNMENT = -4
 IKBO_ERR_TIMEOUT = -5
 IKBO_ERR_MAP_RANGE = -6
+IKBO_ERR_PAGE_RANGE = -7
+IKBO_ERR_NO_PAGES = -8
+IKBO_ERR_NONFINITE = -9
 
 DTYPES = {"bf16": 0, "f32": 1}
 VARIANTS = {"auto": 0, "S0": 1, "S1": 2, "S2": 3, "S3": 4, "S4": 5}
@@ -48,7 +53,8 @@ FLAG_BACKWARD = 8
 EXPORTED = ("ikbo_lce_plan", "ikbo_lce_forward", "ikbo_lce_forward_noalloc", "ikbo_lce_backward", "ikbo_lce_check",
             "ikbo_fa_plan", "ikbo_fa_forward", "ikbo_fa_forward_fused", "ikbo_fa_check", "ikbo_fa_plan_destroy", "ikbo_lce_plan_info",
             "ikbo_lce_plan_set_spin_limit", "ikbo_lce_plan_destroy", "ikbo_status_str",
-            "ikbo_last_error_message")
+            "ikbo_last_error_message", "ikbo_kv_status", "ikbo_kv_tables", "ikbo_rope", "ikbo_kv4_write", "ikbo_kv4_read",
+            "ikbo_kv4_attention_workspace", "ikbo_kv4_attention")
 
 
 class IkboError(RuntimeError):
@@ -102,6 +108,11 @@ def lib() -> ctypes.CDLL:
         L.ikbo_status_str.restype = ctypes.c_char_p
         L.ikbo_last_error_message.argtypes = []
         L.ikbo_last_error_message.restype = ctypes.c_char_p
+        for name in ("ikbo_kv_status", "ikbo_kv_tables", "ikbo_rope", "ikbo_kv4_write", "ikbo_kv4_read", "ikbo_kv4_attention"):
+            getattr(L, name).argtypes = [vp, vp]     # a structure (or the status word) and a stream
+            getattr(L, name).restype = ip
+        L.ikbo_kv4_attention_workspace.argtypes = [i] * 7
+        L.ikbo_kv4_attention_workspace.restype = ctypes.c_int64
         _lib = L
     return _lib
 

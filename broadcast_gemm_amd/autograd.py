@@ -15,6 +15,12 @@ step outside the library, a dtype conversion).
     lce = IkboLce(K_u, K_c, M, D).cuda()           # W_u, W_c: bf16 parameters
     Y = lce(U, C, map)                               # U, C may require grad
     Y.backward(dY)                                   # lce.W_u.grad, lce.W_c.grad, U.grad, C.grad
+
+Rotary positions train through ``IkboRope``: the gradient of a rotation is the rotation by the opposite
+angle with the same factor, the same kernel.
+
+    rope = IkboRope(head_dim).cuda()
+    q, k = rope(q, k, positions)                     # [T, H, head_dim] each
 """
 from __future__ import annotations
 
@@ -23,6 +29,7 @@ from typing import Dict, Tuple
 import torch
 
 from . import FLAG_BACKWARD, LcePlan
+from . import history
 from .rewrite import bucket_b_c, bucket_b_u
 
 
@@ -93,3 +100,39 @@ class IkboLce(torch.nn.Module):
 
     def forward(self, U, C, mp):
         return LceFunction.apply(U, C, mp, self.W_u, self.W_c, self._plans)
+
+
+class RopeFunction(torch.autograd.Function):
+    """(q, k) turned by their positions, both directions in the library."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, freq, layout, factor):
+        q_out, k_out = history.rope(q, k, positions, freq, layout=layout, factor=factor)
+        ctx.save_for_backward(positions, freq)
+        ctx.how = (layout, factor)
+        return q_out, k_out
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        positions, freq = ctx.saved_tensors
+        layout, factor = ctx.how
+        dq, dk = (None if d is None or not need else d if d.stride(-1) == 1 else d.contiguous()
+                  for d, need in zip((dq, dk), ctx.needs_input_grad))
+        if dq is not None or dk is not None:
+            dq, dk = history.rope(dq, dk, positions, freq, layout=layout, factor=factor, inverse=True)
+        return dq, dk, None, None, None, None
+
+
+class IkboRope(torch.nn.Module):
+    """Rotary positions of q and k [T, H, head_dim] (k may be None), with gradients.
+
+    ``rot_dim``, ``theta`` and ``scaling`` as in ``history.rope_frequencies``; the frequencies are a buffer."""
+
+    def __init__(self, head_dim: int, rot_dim: int = 0, theta: float = 10000.0, scaling=None, layout: str = "half"):
+        super().__init__()
+        self.layout = layout
+        freq, self.factor = history.rope_frequencies(rot_dim or head_dim, theta, scaling, device="cpu")
+        self.register_buffer("freq", freq, persistent=False)
+
+    def forward(self, q, k, positions):
+        return RopeFunction.apply(q, k, positions, self.freq, self.layout, self.factor)

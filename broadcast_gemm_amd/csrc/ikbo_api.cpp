@@ -175,6 +175,9 @@ const char *ikbo_status_str(int status) {
         case IKBO_ERR_ALIGNMENT: return "tensor base address not 16-byte aligned";
         case IKBO_ERR_TIMEOUT: return "candidate tile timed out waiting for its user partial";
         case IKBO_ERR_MAP_RANGE: return "map entry outside [0, B_u)";
+        case IKBO_ERR_PAGE_RANGE: return "page, slot, length or position outside its range";
+        case IKBO_ERR_NO_PAGES: return "not enough pages, table columns or rows for the step";
+        case IKBO_ERR_NONFINITE: return "infinity or NaN handed to the 4-bit cache";
     }
     return "unknown status";
 }

@@ -46,7 +46,10 @@ enum {
     IKBO_ERR_HIP = -3,          /* a HIP runtime call failed; see ikbo_last_error_message() */
     IKBO_ERR_ALIGNMENT = -4,    /* a tensor base address is not 16-byte aligned */
     IKBO_ERR_TIMEOUT = -5,      /* device: a candidate tile gave up waiting for its user partial */
-    IKBO_ERR_MAP_RANGE = -6     /* device: some map[b] lies outside [0, B_u) */
+    IKBO_ERR_MAP_RANGE = -6,    /* device: some map[b] lies outside [0, B_u) */
+    IKBO_ERR_PAGE_RANGE = -7,   /* device: a page, slot, length or position outside its range */
+    IKBO_ERR_NO_PAGES = -8,     /* device: a batch needs more pages, table columns or rows than there are */
+    IKBO_ERR_NONFINITE = -9     /* device: an infinity or NaN was handed to the 4-bit cache */
 };
 
 /* Element type of U, C, W_u, W_c and Y. */
@@ -252,6 +255,157 @@ int ikbo_fa_check(ikbo_fa_plan_t plan, void *stream);
 
 /* Free the plan and its workspace (synchronises the device first).  NULL is a no-op. */
 int ikbo_fa_plan_destroy(ikbo_fa_plan_t plan);
+
+/*
+ * ---- Cached user histories -------------------------------------------------------------
+ *
+ * Target attention for users whose histories are kept between requests: K and V of user u
+ * are cached in 4 bits in pages of IKBO_KV4_PAGE tokens that a block table names, grow by
+ * tokens and have a length of their own.  The calls below hold no plan: every buffer is
+ * the caller's, so calls on different streams, devices or captured graphs are independent
+ * as long as their buffers are.  All are asynchronous on `stream` and may be captured.
+ * Arguments that the host can see are checked before anything is enqueued; conditions in
+ * device data set bits of the caller's status word (one uint32 that the caller zeroes
+ * once; may not be NULL), which ikbo_kv_status reads.  Strides count elements.  The device
+ * that owns the buffers must be current.
+ */
+#define IKBO_KV4_PAGE 64
+#define IKBO_KV_MAX_USERS 4096
+
+/* Wait for `stream`, then return and clear the condition recorded in *status (device memory):
+ * IKBO_OK, IKBO_ERR_MAP_RANGE, IKBO_ERR_PAGE_RANGE, IKBO_ERR_NO_PAGES or IKBO_ERR_NONFINITE
+ * (the first of these that was set). */
+int ikbo_kv_status(uint32_t *status, void *stream);
+
+/*
+ * Page tables of one step, from the requests' lengths.  Request i holds lens[i] cached tokens
+ * and brings counts[i] >= 0 new ones (counts[i] = -1: it leaves, and its pages return).  With
+ * have = ceil(lens[i] / page_size), its tokens take the pages
+ *     block_table[i][have .. ceil((lens[i] + counts[i]) / page_size))
+ * off the head of the ring of free pages, in request order; the pages of leaving requests join
+ * the ring's tail in request order and are not handed out by the same call.  state[0] is the
+ * ring's head, state[1] the number of free pages behind it (state[2], state[3] belong to the
+ * library and start as 0).  Token t of request i gets row  starts[i] + t  of
+ *     slots = block_table[i][pos / page_size] * page_size + pos % page_size,
+ *     positions = pos = lens[i] + t,  rows = i;
+ * the rows from starts[B_u] to capacity are filled with -1.  lens_out[i] = lens[i] + counts[i]
+ * (0 for a leaving request); lens_out may be lens and state_out may be state (updated in
+ * place: one step after the other, also on replays of a captured graph).
+ * A step that does not fit (free pages, table columns or capacity: IKBO_ERR_NO_PAGES; a
+ * negative or overlong length, a count below -1, a ring state out of range:
+ * IKBO_ERR_PAGE_RANGE) is refused as a whole: slots, positions and rows become -1, starts 0,
+ * lens_out = lens, state_out = state, and the table and the ring keep their contents.  A page
+ * number outside [0, num_pages) that the table or the ring holds is recorded as PAGE_RANGE and
+ * gives slot -1.
+ * 1 <= B_u <= IKBO_KV_MAX_USERS, num_pages * page_size < 2^31.
+ */
+typedef struct ikbo_kv_tables_args {
+    const int32_t *counts;      /* [B_u] */
+    const int32_t *lens;        /* [B_u] */
+    int32_t *lens_out;          /* [B_u] */
+    int32_t *block_table;       /* [B_u][table_stride], max_pages columns used */
+    int32_t *ring;              /* [num_pages] */
+    int32_t *state;             /* [4]: head, free pages, two words of the library's */
+    int32_t *state_out;         /* [4]; may be state */
+    int32_t *slots, *positions, *rows;   /* [capacity] */
+    int32_t *starts;            /* [B_u + 1] */
+    uint32_t *status;
+    int64_t table_stride;
+    int32_t B_u, max_pages, num_pages, page_size, capacity;
+} ikbo_kv_tables_args;
+int ikbo_kv_tables(const ikbo_kv_tables_args *args, void *stream);
+
+/*
+ * Rotary positions of queries and keys.  Pair i < rot_dim/2 of each head at position p turns by
+ * the angle p * freq[i]:
+ *     (a, b) -> factor * (a cos - b sin,  a sin + b cos)
+ * with (a, b) = elements (i, i + rot_dim/2) (IKBO_ROPE_HALF) or (2i, 2i + 1)
+ * (IKBO_ROPE_INTERLEAVED); elements from rot_dim on are copied.  inverse = 1 turns by the
+ * opposite angle with the same factor: the gradient of the forward rotation.  The angle is
+ * formed in 64 bits and reduced to one turn before sine and cosine, so positions may be any
+ * int32; the rotation is in float32 and rounds once to the tensors' type (IKBO_DTYPE_*).
+ * q, q_out [T][H_q][head_dim] and k, k_out [T][H_k][head_dim] with token and head strides and
+ * contiguous heads; an output may be its input (same strides), and may not overlap it
+ * otherwise.  H_k = 0 leaves k out.  rot_dim even, 2 <= rot_dim <= head_dim <= 1024.
+ */
+enum { IKBO_ROPE_HALF = 0, IKBO_ROPE_INTERLEAVED = 1 };
+typedef struct ikbo_rope_args {
+    const void *q, *k;
+    void *q_out, *k_out;
+    const int32_t *positions;   /* [T] */
+    const double *freq;         /* [rot_dim / 2], radians per position */
+    int64_t q_token, q_head, k_token, k_head;                   /* strides of the inputs */
+    int64_t q_out_token, q_out_head, k_out_token, k_out_head;   /* strides of the outputs */
+    int32_t T, H_q, H_k, head_dim, rot_dim, layout, dtype, inverse;
+    float factor;
+} ikbo_rope_args;
+int ikbo_rope(const ikbo_rope_args *args, void *stream);
+
+/*
+ * The 4-bit cache.  tiles [num_pages][H_kv][68 * head_dim bytes], 16-byte aligned; head_dim 64
+ * or 128.  The tile of a page and head holds its 64 tokens' keys and values as
+ *     K codes [64 tokens][head_dim/2]      byte c: element 2c in the low 4 bits, 2c + 1 in the high
+ *     V codes [head_dim/2][64 tokens]      byte (c, t): elements 2c and 2c + 1 of token t
+ *     K scales [head_dim/32][64]           token t at 16 (t / 16) + 4 (t % 4) + (t / 4) % 4
+ *     V scales [head_dim/32][64]           token t at t
+ * (the orders in which the attention's matrix operands read them).  A code is a sign and one of
+ * 0, .5, 1, 1.5, 2, 3, 4, 6; 32 consecutive elements x of a token share the scale 2^e, stored as
+ * e + 127, with e the smallest in [-125, 125] for which max|x| <= 6 * 2^e; x / 2^e is rounded to
+ * the nearest code, ties to the even one, and never beyond +-6.  All values are exact in bf16.
+ *
+ * ikbo_kv4_write puts k, v [T][H_kv][head_dim] (bf16 or float32, token and head strides) at the
+ * slots (page * 64 + offset) of their tokens; a slot of -1 is skipped, others outside the pages
+ * are recorded as PAGE_RANGE and skipped.  Slots of one call are distinct (a slot named twice is
+ * left with either token's parts).  NaN is stored as 0 and infinity as the largest value; both
+ * are recorded as NONFINITE.
+ * ikbo_kv4_read gathers the values at the slots into k, v [T][H_kv][head_dim] (bf16 or float32;
+ * a float32 value is exact, bf16 likewise); rows of a slot of -1 are left as they were.
+ */
+typedef struct ikbo_kv4_rows_args {
+    void *k, *v;                /* read by the write, written by the read; either may be NULL in a read */
+    const int32_t *slots;       /* [T] */
+    void *tiles;
+    uint32_t *status;
+    int64_t k_token, k_head, v_token, v_head;
+    int32_t T, H_kv, head_dim, num_pages, dtype;
+} ikbo_kv4_rows_args;
+int ikbo_kv4_write(const ikbo_kv4_rows_args *args, void *stream);
+int ikbo_kv4_read(const ikbo_kv4_rows_args *args, void *stream);
+
+/*
+ * Target attention over the cache.  Query l of head h of candidate b, with u = map[b] and the
+ * key/value head h / (H_q / H_kv), sees the tokens t of user u with
+ *     t < lens[u]   and, if positions are given,   t <= positions[b][l],
+ *     O[b,h,l] = sum_t softmax_t(scale * Q[b,h,l] . K[u,t]) V[u,t],
+ * and is 0 where it sees none.  Q, O bf16 with candidate, head and query strides and contiguous
+ * heads (16-byte aligned rows); map NULL means candidate b belongs to user b (B_c <= B_u).
+ * Candidates with map -1 are padding: their O is left as it was; other entries outside [0, B_u)
+ * are recorded as MAP_RANGE and left likewise.  Lengths outside [0, 64 * max_pages] are recorded
+ * as PAGE_RANGE and clamped, as are page numbers outside [0, num_pages) (page 0 is read then).
+ * Scores, softmax and sums are float32 (the weights reach the matrix cores as bf16); O is rounded
+ * once.  scale = 0 means 1/sqrt(head_dim); negative, NaN and infinite scales are INVALID_ARG.
+ * head_dim 64 or 128, H_q a multiple of H_kv, 1 <= B_u <= IKBO_KV_MAX_USERS, L_q >= 1.
+ * workspace: ikbo_kv4_attention_workspace bytes, 16-byte aligned, not shared with a call that may
+ * overlap; nothing in it has to be kept between calls.
+ */
+typedef struct ikbo_kv4_attention_args {
+    const void *Q;
+    void *O;
+    const void *tiles;
+    const int32_t *block_table; /* [B_u][table_stride], max_pages columns used */
+    const int32_t *lens;        /* [B_u] */
+    const int32_t *map;         /* [B_c] or NULL */
+    const int32_t *positions;   /* [B_c][L_q] or NULL */
+    uint32_t *status;
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t q_cand, q_head, q_query, o_cand, o_head, o_query, table_stride;
+    int32_t B_u, B_c, H_q, H_kv, L_q, head_dim, max_pages, num_pages;
+    float scale;
+} ikbo_kv4_attention_args;
+/* Bytes of workspace for these dimensions, or a negative status. */
+int64_t ikbo_kv4_attention_workspace(int B_u, int B_c, int H_q, int H_kv, int L_q, int head_dim, int max_pages);
+int ikbo_kv4_attention(const ikbo_kv4_attention_args *args, void *stream);
 
 /* Static text for a status code. */
 const char *ikbo_status_str(int status);

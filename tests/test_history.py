@@ -1,0 +1,224 @@
+"""The cached-history operators on the CPU: refusals at the C ABI before any HIP call, refusals of the binding, the
+frequency tables, and the plain forms that the GPU tests compare with (against independent small cases)."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import broadcast_gemm_amd as bga
+from broadcast_gemm_amd import history
+from history_ref import LEVELS, decode, encode, tables, turn
+
+P = 1 << 20   # a stand-in address: every check below returns before any HIP call
+INVALID, UNSUPPORTED, ALIGNMENT = bga.IKBO_ERR_INVALID_ARG, bga.IKBO_ERR_UNSUPPORTED, bga.IKBO_ERR_ALIGNMENT
+
+
+@pytest.fixture(scope="module")
+def L():
+    import os
+    if not os.path.exists(bga.LIB_PATH):
+        from broadcast_gemm_amd import build
+        build.build()
+    return bga.lib()
+
+
+def call(f, args):
+    return f(ctypes.byref(args), None)
+
+
+def fill(cls, **kw):
+    a = cls()
+    for name, kind in cls._fields_:
+        setattr(a, name, kw.pop(name, P if kind is ctypes.c_void_p else 0))
+    assert not kw
+    return a
+
+
+TABLES = dict(table_stride=9, B_u=3, max_pages=9, num_pages=40, page_size=64, capacity=10)
+
+
+@pytest.mark.parametrize("change, want", [
+    (dict(B_u=0), INVALID), (dict(B_u=4097), UNSUPPORTED), (dict(max_pages=0), INVALID), (dict(num_pages=0), INVALID),
+    (dict(page_size=0), INVALID), (dict(capacity=-1), INVALID), (dict(table_stride=8), INVALID), (dict(counts=0), INVALID),
+    (dict(status=0), INVALID), (dict(slots=0), INVALID), (dict(lens=P + 2), ALIGNMENT), (dict(rows=P + 1), ALIGNMENT),
+    (dict(num_pages=1 << 25), UNSUPPORTED), (dict(max_pages=1 << 25, table_stride=1 << 25), UNSUPPORTED)])
+def test_tables_refusals(L, change, want):
+    assert call(L.ikbo_kv_tables, fill(history._TablesArgs, **{**TABLES, **change})) == want
+    assert L.ikbo_kv_tables(None, None) == INVALID
+
+
+ROPE = dict(q_token=512, q_head=128, k_token=256, k_head=128, q_out_token=512, q_out_head=128, k_out_token=256, k_out_head=128,
+            q_out=2 * P, k_out=2 * P, T=5, H_q=4, H_k=2, head_dim=128, rot_dim=128, layout=0, dtype=0, inverse=0, factor=1.0)
+
+
+@pytest.mark.parametrize("change, want", [
+    (dict(T=-1), INVALID), (dict(T=0), bga.IKBO_OK), (dict(H_q=0, H_k=0), INVALID), (dict(H_q=-1), INVALID), (dict(rot_dim=7), INVALID),
+    (dict(rot_dim=0), INVALID), (dict(rot_dim=130), INVALID), (dict(head_dim=1026), UNSUPPORTED), (dict(layout=2), INVALID),
+    (dict(dtype=2), INVALID), (dict(inverse=2), INVALID), (dict(factor=math.inf), INVALID), (dict(factor=math.nan), INVALID),
+    (dict(q=0), INVALID), (dict(k_out=0), INVALID), (dict(positions=0), INVALID), (dict(freq=P + 4), ALIGNMENT),
+    (dict(q=P + 1), ALIGNMENT), (dict(dtype=1, k=P + 2), ALIGNMENT), (dict(q_out=P, q_out_token=640), INVALID), (dict(H_q=5000), UNSUPPORTED)])
+def test_rope_refusals(L, change, want):
+    assert call(L.ikbo_rope, fill(history._RopeArgs, **{**ROPE, **change})) == want
+    assert L.ikbo_rope(None, None) == INVALID
+
+
+ROWS = dict(k_token=256, k_head=128, v_token=256, v_head=128, T=5, H_kv=2, head_dim=128, num_pages=7, dtype=0)
+
+
+@pytest.mark.parametrize("change, want", [
+    (dict(T=-1), INVALID), (dict(T=0), bga.IKBO_OK), (dict(H_kv=0), INVALID), (dict(num_pages=0), INVALID), (dict(dtype=3), INVALID),
+    (dict(head_dim=96), UNSUPPORTED), (dict(num_pages=1 << 25), UNSUPPORTED), (dict(H_kv=5000), UNSUPPORTED), (dict(slots=0), INVALID),
+    (dict(tiles=0), INVALID), (dict(status=0), INVALID), (dict(k=P + 8), ALIGNMENT), (dict(tiles=P + 4), ALIGNMENT),
+    (dict(k_token=260), ALIGNMENT), (dict(v_head=132), ALIGNMENT)])
+def test_rows_refusals(L, change, want):
+    args = {**ROWS, **change}
+    assert call(L.ikbo_kv4_write, fill(history._RowsArgs, **args)) == want
+    assert call(L.ikbo_kv4_read, fill(history._RowsArgs, **args)) == want
+    assert L.ikbo_kv4_write(None, None) == INVALID and L.ikbo_kv4_read(None, None) == INVALID
+
+
+def test_write_needs_both_tensors(L):
+    assert call(L.ikbo_kv4_write, fill(history._RowsArgs, **ROWS, v=0)) == INVALID
+    assert call(L.ikbo_kv4_read, fill(history._RowsArgs, **ROWS, k=0, v=0)) == bga.IKBO_OK
+
+
+ATTEND = dict(workspace_bytes=1 << 40, q_cand=512, q_head=128, q_query=128, o_cand=512, o_head=128, o_query=128, table_stride=9, B_u=3,
+              B_c=6, H_q=4, H_kv=2, L_q=1, head_dim=128, max_pages=9, num_pages=40, scale=0.0)
+
+
+@pytest.mark.parametrize("change, want", [
+    (dict(B_u=0), INVALID), (dict(B_u=4097), UNSUPPORTED), (dict(B_c=-1), INVALID), (dict(B_c=0), bga.IKBO_OK), (dict(H_kv=0), INVALID),
+    (dict(H_q=5), INVALID), (dict(H_q=1), INVALID), (dict(L_q=0), INVALID), (dict(head_dim=96), UNSUPPORTED), (dict(max_pages=0), INVALID),
+    (dict(num_pages=0), INVALID), (dict(num_pages=1 << 25), UNSUPPORTED), (dict(table_stride=8), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID), (dict(Q=0), INVALID), (dict(O=0), INVALID), (dict(lens=0), INVALID),
+    (dict(workspace=0), INVALID), (dict(workspace_bytes=100), INVALID), (dict(map=0), INVALID), (dict(Q=P + 8), ALIGNMENT),
+    (dict(q_head=132), ALIGNMENT), (dict(o_query=4), ALIGNMENT), (dict(map=P + 2), ALIGNMENT), (dict(positions=P + 1), ALIGNMENT),
+    (dict(B_c=1 << 28, L_q=64), UNSUPPORTED)])
+def test_attention_refusals(L, change, want):
+    assert call(L.ikbo_kv4_attention, fill(history._AttentionArgs, **{**ATTEND, **change})) == want
+    assert L.ikbo_kv4_attention(None, None) == INVALID
+
+
+def test_attention_workspace(L):
+    f = L.ikbo_kv4_attention_workspace
+    assert f(15, 15, 4, 4, 1, 128, 16) > 0
+    assert f(0, 15, 4, 4, 1, 128, 16) == INVALID and f(15, 15, 5, 4, 1, 128, 16) == INVALID
+    assert f(15, 15, 4, 4, 1, 80, 16) == UNSUPPORTED
+
+
+def test_status_word_refusal(L):
+    assert L.ikbo_kv_status(None, None) == INVALID
+    for code in (bga.IKBO_ERR_PAGE_RANGE, bga.IKBO_ERR_NO_PAGES, bga.IKBO_ERR_NONFINITE):
+        assert bga.status_str(code) != "unknown status"
+
+
+def test_binding_refuses_host_tensors():
+    i = torch.zeros(4, dtype=torch.int32)
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    t = torch.zeros(3, 2, 68 * 64, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        history.kv_tables(i, i, torch.zeros(4, 2, dtype=torch.int32), i, i, 4, i[:1])
+    with pytest.raises(ValueError):
+        history.rope(x, x, i, torch.ones(32, dtype=torch.float64))
+    with pytest.raises(ValueError):
+        history.kv4_write(x, x, i, t, i[:1])
+    with pytest.raises(ValueError):
+        history.kv4_read(i, t, i[:1])
+    with pytest.raises(ValueError):
+        history.kv4_attention(x, t, torch.zeros(4, 2, dtype=torch.int32), i, None, i[:1])
+    with pytest.raises(ValueError):
+        history.kv_status(i[:1])
+    with pytest.raises(ValueError):
+        history.rope(None, None, i, torch.ones(32, dtype=torch.float64))
+
+
+def test_heads_of_one_tensor_are_told_from_overlap():
+    qkv = torch.zeros(6, 8, 64)
+    assert history._interleaved(qkv[:, :4], qkv[:, 4:6]) and history._interleaved(qkv[:, 6:], qkv[:, :4])
+    assert not history._interleaved(qkv[:, :4], qkv[:, 3:6])
+    assert not history._interleaved(qkv[:5], qkv[1:])
+    with pytest.raises(ValueError):
+        history._distinct("out", torch.zeros(1, 4, 64).expand(6, 4, 64))
+    with pytest.raises(ValueError):
+        history._distinct("out", torch.zeros(100).as_strided((3, 4, 8), (8, 8, 1)))
+    history._distinct("out", qkv.transpose(0, 1))
+
+
+# ---- frequencies ---------------------------------------------------------------------------
+
+
+def test_frequencies_plain_linear_theta():
+    f, a = history.rope_frequencies(64, 500.0, device="cpu")
+    assert a == 1.0 and f.dtype == torch.float64
+    for i in range(32):
+        assert float(f[i]) == pytest.approx(500.0 ** (-2 * i / 64), rel=1e-14)
+    g, _ = history.rope_frequencies(64, 500.0, {"kind": "linear", "factor": 4}, device="cpu")
+    assert torch.allclose(g * 4, f, rtol=1e-15)
+    g, _ = history.rope_frequencies(64, 500.0, {"kind": "theta", "factor": 4}, device="cpu")
+    assert float(g[0]) == 1.0 and float(g[31]) == pytest.approx(float(f[31]) / 4, rel=1e-12)
+
+
+def test_frequencies_ramps():
+    how = dict(factor=8, context=8192, low=1, high=4)
+    f, _ = history.rope_frequencies(128, 1e4, device="cpu")
+    g, a = history.rope_frequencies(128, 1e4, {"kind": "turns", **how}, device="cpu")
+    assert a == 1.0
+    for x, y in zip(f.tolist(), g.tolist()):
+        turns = 8192 * x / (2 * math.pi)
+        keep = min(1.0, max(0.0, (turns - 1) / 3))
+        assert y == pytest.approx(x * keep + x / 8 * (1 - keep), rel=1e-13)
+    how.update(low=1, high=32)
+    g, a = history.rope_frequencies(128, 1e4, {"kind": "pairs", **how}, device="cpu")
+    assert a == pytest.approx(0.1 * math.log(8) + 1)
+    ratio = (g / f).tolist()
+    assert ratio[0] == 1.0 and ratio[-1] == pytest.approx(1 / 8) and all(x >= y - 1e-12 for x, y in zip(ratio, ratio[1:]))
+    turns = [8192 * x / (2 * math.pi) for x in f.tolist()]
+    assert all(r == pytest.approx(1.0) for r, t in zip(ratio, turns) if t > 40) and all(r == pytest.approx(1 / 8) for r, t in zip(ratio, turns) if t < 0.8)
+    assert history.rope_frequencies(128, 1e4, {"kind": "pairs", "attention": 1.5, **how}, device="cpu")[1] == 1.5
+
+
+@pytest.mark.parametrize("rot, scaling", [(7, None), (0, None), (64, {"kind": "linear", "factor": 0}), (64, {"kind": "other", "factor": 2}),
+                                          (2, {"kind": "theta", "factor": 2}), (64, {"kind": "turns", "factor": 2, "context": 8, "low": 4, "high": 1})])
+def test_frequencies_refusals(rot, scaling):
+    with pytest.raises(ValueError):
+        history.rope_frequencies(rot, 1e4, scaling, device="cpu")
+
+
+# ---- the plain forms -----------------------------------------------------------------------
+
+
+def test_plain_codes():
+    x = np.zeros((1, 32))
+    x[0, :10] = [6, 5, -5, 0.25, -0.75, 1.25, 1.75, 2.5, 3.5, 0.26]
+    c, s = encode(x)
+    assert s[0, 0] == 127
+    assert decode(c, s)[0, :10].tolist() == [6, 4, -4, 0, -1, 1, 2, 2, 4, 0.5]
+    assert encode(x * 1.0001)[1][0, 0] == 128                       # 6.0006 no longer fits the scale 1
+    assert encode(np.zeros((1, 32)))[1][0, 0] == 2
+    rng = np.random.default_rng(0)
+    y = rng.standard_normal((50, 64)) * np.exp(3 * rng.standard_normal((50, 1)))
+    z = decode(*encode(y))
+    # Levels are at most 2 apart at the scale, and the largest magnitude is over 3: within half a gap of 1.
+    top = np.abs(y.reshape(50, 2, 32)).max(-1, keepdims=True)
+    assert (np.abs(z - y).reshape(50, 2, 32) <= top / 3 * 1.0000001).all()
+    assert len(LEVELS) == 8
+
+
+def test_plain_turn_keeps_lengths_and_inverts():
+    rng = np.random.default_rng(1)
+    x, pos, f = rng.standard_normal((5, 2, 10)), np.array([0, 1, 7, 100, 10 ** 6]), np.array([1.0, 0.3, 0.01])
+    for layout in ("half", "interleaved"):
+        y, _ = turn(x, pos, f, layout)
+        assert np.allclose((y ** 2).sum(-1), (x ** 2).sum(-1)) and np.array_equal(y[0], x[0]) and np.array_equal(y[..., 6:], x[..., 6:])
+        assert np.allclose(turn(y, pos, f, layout, inverse=True)[0], x)
+
+
+def test_plain_tables():
+    table, ring = np.full((3, 4), -1, np.int32), np.arange(10, 18, dtype=np.int32)
+    got = tables([3, 0, 5], [0, 0, 0], table, ring, 6, 8, 10, P=4)
+    assert got[0].tolist() == [64, 65, 66, 68, 69, 70, 71, 40, -1, -1] and got[5:] == (1, 5)
+    got = tables([-1, 1, 1], got[4], table, ring, got[5], got[6], 2, P=4)
+    assert got[0].tolist() == [44, 41] and got[4].tolist() == [0, 1, 6] and got[5:] == (2, 5) and ring[6] == 16
+    assert tables([1, 1, 1], got[4], table, ring, got[5], got[6], 2, P=4) is None
