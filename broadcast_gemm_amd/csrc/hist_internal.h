@@ -25,7 +25,7 @@ hipError_t launch_kv4_read(const ikbo_kv4_rows_args &a, hipStream_t s);
 
 // Workspace of the attention: byte offsets of its parts.
 struct Kv4AttnLayout {
-    int rows_per_unit;                 // query rows of one unit (16 times the tiles a wave holds)
+    int rows_per_unit, units;          // query rows of one unit, and about how many units are made
     int64_t o_hdr, o_perm, o_off, o_ubase, o_pbase, o_tbase, o_ml, o_part, total;
     int64_t part_units;                // units that may leave a partial result
 };
