@@ -1,4 +1,5 @@
-"""Build libikbo.so (HIP C++ for gfx950) in-tree with hipcc.
+"""Build libikbo.so (HIP C++ for gfx950) in-tree with hipcc, and _ikbo_torch.so, the host-side binding
+of the cached user histories to torch tensors, with the host compiler.
 
     python -m broadcast_gemm_amd.build
 """
@@ -13,6 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libikbo.so")
+TORCH_LIB = os.path.join(HERE, "_ikbo_torch.so")
 SOURCES = ["ikbo_api.cpp", "lce_kernels.hip", "lce_fused.hip", "lce_rows.hip", "lce_stream.hip", "lce_noalloc.hip", "lce_backward.hip", "ikbo_fa.cpp",
            "fa_kernels.hip", "ikbo_history.cpp", "hist_tables.hip", "hist_rope.hip", "hist_cache.hip", "hist_attention.hip"]
 ARCH = os.environ.get("IKBO_OFFLOAD_ARCH", "gfx950")
@@ -23,6 +25,23 @@ def hipcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("hipcc not found")
+
+
+def torch_command(out: str) -> list:
+    """The host compiler's command for the torch binding."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no host C++ compiler")
+    include = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+            + [x for i in include for x in ("-isystem", i)] + [os.path.join(CSRC, "torch_history.cpp"), "-o", out, "-L" + lib]
+            + ["-Wl,-rpath," + lib, "-ltorch", "-ltorch_cpu", "-lc10", "-ltorch_python"])
 
 
 def build(verbose: bool = False) -> str:
@@ -40,6 +59,11 @@ def build(verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         jobs.append((src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
+    torch_tmp = TORCH_LIB + ".tmp"
+    cmd = torch_command(torch_tmp)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    torch_proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
     objs = []
     for src, obj, proc in jobs:
         _, err = proc.communicate()
@@ -49,6 +73,10 @@ def build(verbose: bool = False) -> str:
         if verbose and msgs.strip():
             print(msgs)
         objs.append(obj)
+    _, err = torch_proc.communicate()
+    if torch_proc.returncode != 0:
+        raise RuntimeError(f"the host compiler failed on torch_history.cpp:\n{err}")
+    os.replace(torch_tmp, TORCH_LIB)
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp] + objs
     if verbose:

@@ -5,83 +5,54 @@
 // matrix operands, 16 to a tile, and the cache is read once for all of them, never per candidate.
 //
 // Per page of 64 tokens a wave forms S^T = K Q^T and O^T += V^T P^T with v_mfma_f32_16x16x32_bf16.
-// Codes go from memory to registers and through the hardware's 4-bit conversion (which applies the
-// block's scale) straight into operand registers; nothing passes through LDS.  With lane = 16 g + j:
+// The hardware's 4-bit conversion applies a block's scale as it converts, and all its results are
+// exact in bf16.  With lane = 16 g + j:
 //   S^T tile t (A: keys, B: queries): row j of the tile is token 16 (j / 4) + 4 t + j % 4, so lane
 //   (g, j) ends up with query j against tokens 16 g + 4 t + i, i < 4: over the four tiles 16
 //   consecutive tokens, 16 g .. 16 g + 15.  Those are the k slots that it must supply as B operand
 //   P^T, and the tokens of its A operand V^T: 16 consecutive bytes of a row of the tile's V codes.
-//   The d order of the S^T product is free as long as K and Q agree: lane group g takes the g-th
-//   quarter of a head, a 16- or 8-byte piece of a K row.
+//   The d order of the S^T product is free as long as K and Q agree.
 //   A byte of V codes holds elements 2c, 2c + 1 of one token: the low halves of the converted pairs
-//   are the operand of the even elements' O^T tile, the high halves that of the odd ones'.
+//   belong to the even element's row of V^T, the high halves to the odd one's.
 // The running maximum is kept per query; it moves (and O^T is rescaled) only when a page's maximum
-// exceeds it by more than 8 (in base 2), so weights stay below 2^8.
+// exceeds it by more than 8 (in base 2), so weights stay below 2^8.  Weights are rounded to bf16 for
+// the product, and their sums are sums of the rounded ones (an all-ones A operand): half a step of
+// bf16 on a weight, as in the dense attention.
 //
-// Work split: a unit is (user, head, row tile, range of pages).  A grouping launch sorts the
-// candidates by user and cuts the histories into about as many units as the chip holds at once
-// (twice as many blocks in the wide kernel), whatever the lengths; a unit that covers all pages of
-// its rows stores O, the others leave float32 partial results and their maxima and sums, which a
-// last launch joins.
+// Two kernels.  Up to 32 rows per user and head on average, a block is one wave, which converts the
+// codes it reads for itself, registers to registers: the cache's bytes are what counts.  With more
+// rows the conversion would be repeated by every wave: a block of 4 waves, 32 rows each, converts a
+// page once into LDS (bf16, two pages deep) and each wave reads its operands there.
 //
-// Two kernels.  Up to 32 rows per user and head on average, a unit is one wave, which converts the
-// codes it reads for itself: the cache's bytes are what counts.  With more rows the conversion would
-// be repeated by every wave: a block of 4 waves, 32 rows each, converts a page once into LDS (bf16,
-// two pages deep) and each wave reads its operands there.
-#include "hist_internal.h"
-
+// How the work is dealt to the blocks, and what joins their partial results: hist_plan.h.
 #include <algorithm>
 
+#include "hist_plan.h"
 #include "lce_device.h"
+#include "lce_sync.h"
 
 namespace ikbo {
 namespace {
 
-constexpr int kPage = IKBO_KV4_PAGE;
-constexpr int kPrep = 1024;           // threads of the grouping block
-constexpr int kNarrowUnits = 4096;    // units aimed at: 16 waves for each of 256 CUs
-constexpr int kWideUnits = 1024;      // blocks of 4 waves, two at a time on each CU
-constexpr int kWideWaves = 4, kWideRows = 32 * kWideWaves;
-constexpr int kPer = IKBO_KV_MAX_USERS / kPrep;   // users per thread of the grouping block
+constexpr int kLogNarrow = 11;        // one wave each, 8 at a time on each of 256 CUs
+constexpr int kLogWide = 9;           // 4 waves each, two at a time on each CU
+constexpr int kWideRows = 128;        // 4 waves of 32 rows
 constexpr float kSlack = 8.0f;
 
-struct AttnArgs {
-    const uint16_t *Q;
-    uint16_t *O;
-    const char *tiles;
-    const int32_t *table, *lens, *map, *positions;
-    uint32_t *status;
-    int32_t *hdr, *perm, *off, *ubase, *pbase, *tbase;
-    float2 *ml;
-    float *part;
-    int64_t q_cand, q_head, q_query, o_cand, o_head, o_query, table_stride;
-    int B_u, B_c, H_kv, G, L_q, max_pages, num_pages;
-    int rows_per_unit, units;         // rows and number of units aimed at
-    float scale_log2;
-};
-
-// Pieces that a history of `pages` is cut into for about `chunk` pages each (hdr[0]): at most 1.5 chunk.
-// Piece s is pages [cut(s), cut(s + 1)).
-__device__ __forceinline__ int pieces(int pages, int chunk) { return max(1, (int)((2u * pages + chunk) / (2u * chunk))); }
-__device__ __forceinline__ int cut(int pages, int n, int s) { return (int)((int64_t)pages * s / n); }
-
-__device__ __forceinline__ int clamp_len(int len, int max_pages) { return min(max(len, 0), max_pages * kPage); }
-
 // One block.  Groups the candidates by user (perm, off: a stable counting sort, one run of
-// candidates per wave), then the prefix sums over the users of units (ubase), of units that leave
-// partial results (pbase) and of row tiles that those join (tbase).
+// candidates per wave) and forms the prefix sums of the plan.
 __global__ void __launch_bounds__(kPrep) kv4_prep_kernel(AttnArgs a, int waves) {
     extern __shared__ int sh[];       // counts [waves][B_u], offsets [B_u + 1]
-    __shared__ long long s_w[kPrep / 64];
-    __shared__ int s_scan[3][kPrep / 64];
+    __shared__ int64_t s_w[kPrep / 64];
+    __shared__ int s_n[kPrep / 64];
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = tid >> 6;
     const int B = a.B_u;
     int *cnt = sh, *offs = sh + waves * B;
     uint32_t err = 0;
     const int per = (B + kPrep - 1) / kPrep;   // consecutive users per thread
-    int len_in[kPer];
+    int len[kPer];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) len_in[e] = e < per && tid * per + e < B ? a.lens[tid * per + e] : 0;
+    for (int e = 0; e < kPer; ++e) len[e] = e < per && tid * per + e < B ? a.lens[tid * per + e] : 0;
 
     if (a.map) {
         for (int i = tid; i < waves * B; i += kPrep) cnt[i] = 0;
@@ -109,10 +80,11 @@ __global__ void __launch_bounds__(kPrep) kv4_prep_kernel(AttnArgs a, int waves) 
             if (lane == 0) cnt[wv * B + u] += __popcll(m);
         });
         __syncthreads();
-        int sum = 0;
-        for (int e = 0; e < per; ++e) {
+        int sum = 0, all;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
             const int u = tid * per + e;
-            if (u < B) {
+            if (e < per && u < B) {
                 int run = 0;
                 for (int w = 0; w < waves; ++w) {
                     const int c = cnt[w * B + u];
@@ -123,112 +95,67 @@ __global__ void __launch_bounds__(kPrep) kv4_prep_kernel(AttnArgs a, int waves) 
                 sum += run;
             }
         }
-        int inc = sum;
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(inc, d);
-            if (lane >= d) inc += o;
-        }
-        if (lane == 63) s_scan[0][wv] = inc;
+        int at = wave_before(sum, &all);
+        if (lane == 0) s_n[wv] = all;
         __syncthreads();
-        int base = inc - sum;
-        for (int w = 0; w < wv; ++w) base += s_scan[0][w];
-        for (int e = 0; e < per; ++e) {
+        for (int w = 0; w < wv; ++w) at += s_n[w];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
             const int u = tid * per + e;
-            if (u < B) {
+            if (e < per && u < B) {
                 const int c = offs[u];
-                offs[u] = base;
-                base += c;
-                if (u == B - 1) offs[B] = base;
+                offs[u] = at;
+                at += c;
+                if (u == B - 1) offs[B] = at;
             }
         }
         __syncthreads();
         walk([&](int b, int u, bool mine, uint64_t m) {
-            int at = 0;
+            int first = 0;
             if (lane == 0) {
-                at = cnt[wv * B + u];
-                cnt[wv * B + u] = at + __popcll(m);
+                first = cnt[wv * B + u];
+                cnt[wv * B + u] = first + __popcll(m);
             }
-            at = __shfl(at, 0);
-            if (mine) a.perm[offs[u] + at + __popcll(m & ((1ull << lane) - 1))] = b;
+            first = __shfl(first, 0);
+            if (mine) a.perm[offs[u] + first + __popcll(m & ((1ull << lane) - 1))] = b;
         });
-        for (int u = tid; u <= B; u += kPrep) a.off[u] = offs[u];
     } else {
         for (int b = tid; b < a.B_c; b += kPrep) a.perm[b] = b;
-        for (int u = tid; u <= B; u += kPrep) a.off[u] = offs[u] = min(u, a.B_c);
+        for (int u = tid; u <= B; u += kPrep) offs[u] = min(u, a.B_c);
+        __syncthreads();
     }
-    __syncthreads();
+    for (int u = tid; u <= B; u += kPrep) a.off[u] = offs[u];
 
-    // Row tiles and pages of this thread's users, then the pages per unit.
-    int tiles[kPer], pages[kPer];
-    long long work = 0;
+    int64_t w[kPer], sum_w = 0, all_w;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
         const int u = tid * per + e;
-        const bool mine = e < per && u < B;
-        const long long rows = mine ? (long long)(offs[u + 1] - offs[u]) * a.L_q * a.G : 0;
-        tiles[e] = (int)((rows + a.rows_per_unit - 1) / a.rows_per_unit);
-        if (mine && (len_in[e] < 0 || len_in[e] > a.max_pages * kPage)) err |= kStPage;
-        pages[e] = (clamp_len(len_in[e], a.max_pages) + kPage - 1) / kPage;
-        work += (long long)tiles[e] * pages[e] * a.H_kv;
+        const int rows = e < per && u < B ? (offs[u + 1] - offs[u]) * a.L_q * a.G : 0;
+        if (len[e] < 0 || len[e] > a.max_pages * kPage) err |= kStPage;
+        w[e] = (int64_t)((rows + a.R - 1) / a.R) * a.H_kv * max(1, pages_of(clamp_len(len[e], a.max_pages)));
+        sum_w += w[e];
     }
-    for (int d = 32; d; d >>= 1) work += __shfl_xor(work, d);
-    if (lane == 0) s_w[wv] = work;
+    int64_t at_w = wave_before(sum_w, &all_w);
+    if (lane == 0) s_w[wv] = all_w;
     __syncthreads();
-    work = 0;
-    for (int w = 0; w < kPrep / 64; ++w) work += s_w[w];
-    const int chunk = (int)min(max(1ll, (work + a.units - 1) / a.units), 1ll << 28);
-
-    int v[3] = {0, 0, 0}, inc[3];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        const int n = pieces(pages[e], chunk);
-        v[0] += tiles[e] * n;
-        if (n > 1) { v[1] += tiles[e] * n; v[2] += tiles[e]; }
-    }
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        inc[k] = v[k];
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(inc[k], d);
-            if (lane >= d) inc[k] += o;
-        }
-        if (lane == 63) s_scan[k][wv] = inc[k];
-    }
-    __syncthreads();
-    int base[3], *const out[3] = {a.ubase, a.pbase, a.tbase};
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        base[k] = inc[k] - v[k];
-        for (int w = 0; w < wv; ++w) base[k] += s_scan[k][w];
+    all_w = 0;
+    for (int v = 0; v < kPrep / 64; ++v) {
+        if (v == wv) at_w += all_w;
+        all_w += s_w[v];
     }
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
         const int u = tid * per + e;
         if (e < per && u < B) {
-            const int n = pieces(pages[e], chunk);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) out[k][u] = base[k];
-            base[0] += tiles[e] * n;
-            if (n > 1) { base[1] += tiles[e] * n; base[2] += tiles[e]; }
-            if (u == B - 1)
-#pragma unroll
-                for (int k = 0; k < 3; ++k) out[k][B] = base[k];
+            a.work[u] = at_w;
+            at_w += w[e];
         }
     }
-    if (tid == 0) a.hdr[0] = chunk;
-    if (err) atomicOr(a.status, err);
-}
-
-// Largest u in [0, n) with base[u] <= x: the owner of x (users without units share their
-// successor's base and are skipped).
-__device__ __forceinline__ int owner_of(const int32_t *base, int n, int x) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (base[mid] <= x) lo = mid;
-        else hi = mid;
+    if (tid == 0) {
+        a.work[B] = all_w;
+        a.share[0] = share_of(all_w, a.log_blocks);
     }
-    return lo;
+    if (err) atomicOr(a.status, err);
 }
 
 // x against the lanes 16 and 32 away.
@@ -252,10 +179,210 @@ __device__ __forceinline__ uint32_t values2(uint32_t codes, float scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, I));
 }
 
-// The 8 values of one dword of codes.
+// The 8 values of one dword of codes of one token.
 __device__ __forceinline__ u32x4_t values8(uint32_t codes, float scale) {
     return (u32x4_t){values2<0>(codes, scale), values2<1>(codes, scale), values2<2>(codes, scale), values2<3>(codes, scale)};
 }
+
+// One element pair of 4 tokens: the even element's values, then the odd one's.
+__device__ __forceinline__ void values_v(uint32_t codes, uint32_t scales, uint32_t &e0, uint32_t &e1, uint32_t &o0, uint32_t &o1) {
+    const uint32_t v0 = values2<0>(codes, scale_of(scales, 0)), v1 = values2<1>(codes, scale_of(scales, 1));
+    const uint32_t v2 = values2<2>(codes, scale_of(scales, 2)), v3 = values2<3>(codes, scale_of(scales, 3));
+    e0 = pair16(v0, v1, false);
+    e1 = pair16(v2, v3, false);
+    o0 = pair16(v0, v1, true);
+    o1 = pair16(v2, v3, true);
+}
+
+// V scales of 4 tokens of which the first n exist.  Bytes past the history may be anything: scale
+// 2^-127 keeps their values finite, and their weights are 0.
+__device__ __forceinline__ uint32_t existing(uint32_t scales, int n) {
+    return n >= 4 ? scales : n <= 0 ? 0u : scales & ((1u << (8 * n)) - 1u);
+}
+
+__device__ __forceinline__ float inverse_of(float l) { return l > 0.f || l != l ? 1.f / l : 0.f; }   // a row that sees nothing is 0
+__device__ __forceinline__ float weight_of(float m, float top) {
+    return m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - top);
+}
+
+// A wave's query rows, 16 n + j from `first`, and their softmax: NT tiles of 16 rows.
+template <int HD, int NT>
+struct Queries {
+    static constexpr int TK = HD / 32, DT = HD / 16;
+    int limit[NT];                    // tokens that the row sees
+    int most, least;                  // largest and smallest limit of the wave's rows
+    u32x4_t qf[TK][NT];
+    f32x4_t o[DT][NT], lsum[NT];
+    float m[NT], nm[NT];
+
+    // Step s of a row's elements: lane group g holds the 8 from `base` + s * `step`.
+    template <class P>
+    __device__ __forceinline__ void load(const AttnArgs &a, const P &plan, const User &x, int h, int first, int j, int base, int step) {
+        most = 0;
+        least = x.len;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = first + 16 * n + j;
+            const bool live = r < x.n_rows;
+            int cnd, l, hq;
+            plan.row(x, h, live ? r : 0, cnd, l, hq);
+            const uint16_t *q = a.Q + cnd * a.q_cand + hq * a.q_head + l * a.q_query + base;
+#pragma unroll
+            for (int s = 0; s < TK; ++s)
+                qf[s][n] = live ? *reinterpret_cast<const u32x4_t *>(q + s * step) : (u32x4_t){0, 0, 0, 0};
+            limit[n] = live ? x.len : 0;
+            if (live && a.positions) {
+                const int pos = a.positions[(int64_t)cnd * a.L_q + l];
+                limit[n] = pos < 0 ? 0 : pos < x.len ? pos + 1 : x.len;
+            }
+            most = max(most, limit[n]);
+            if (live) least = min(least, limit[n]);
+            m[n] = -__builtin_inff();
+            nm[n] = 0.f;
+            lsum[n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d][n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) {
+            most = max(most, __shfl_xor(most, d));
+            least = min(least, __shfl_xor(least, d));
+        }
+        most = __builtin_amdgcn_readfirstlane(most);
+        least = __builtin_amdgcn_readfirstlane(least);
+    }
+
+    // Scores of page p: what a row does not see becomes -inf, and the running maximum moves if it must.
+    __device__ __forceinline__ void raise(f32x4_t (&S)[4][NT], int p, int g, float scale_log2) {
+        // The empty asm keeps these two branches branches: their bodies cost more than a turn's own
+        // vector work, and as selects they would be paid on every page.
+        if (p * kPage + kPage > least) {
+            asm volatile("");
+            const int key0 = p * kPage + 16 * g;   // this lane's tokens: key0 + 4 t + i
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (key0 + 4 * t + i >= limit[n]) S[t][n][i] = -__builtin_inff();
+        }
+        bool grow = false;
+        float mb[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float x = -__builtin_inff();
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x = fmaxf(x, S[t][n][i]);
+            mb[n] = max_over_groups(x) * scale_log2;
+            grow = grow || mb[n] > m[n] + kSlack;
+        }
+        if (__ballot(grow)) {
+            asm volatile("");
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float mn = fmaxf(m[n], mb[n]);
+                const float alpha = mn == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
+                m[n] = mn;
+                nm[n] = mn == -__builtin_inff() ? 0.f : -mn;
+                lsum[n] *= alpha;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[d][n] *= alpha;
+            }
+        }
+    }
+
+    // Scores into the weights pf (B operand of the two halves of 32 tokens) and their sums.
+    __device__ __forceinline__ void weigh(const f32x4_t (&S)[4][NT], float scale_log2, u32x4_t (&pf)[2][NT]) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                float w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[t][n][i], scale_log2, nm[n]));
+                pf[t >> 1][n][2 * (t & 1)] = pack_bf16x2(w[0], w[1]);
+                pf[t >> 1][n][2 * (t & 1) + 1] = pack_bf16x2(w[2], w[3]);
+            }
+        const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) lsum[n] = mfma_bf16(ones, pf[kk][n], lsum[n]);
+    }
+};
+
+// A run of the line of pages: the pieces of units that block `blk` takes, one after the other.
+struct Piece {
+    User x;
+    int h, tile, p0, p1;
+    bool whole;
+    int64_t slot;                     // of the partial result, unless whole
+    int n;                            // pieces of the unit, if it begins here and is cut
+};
+template <class P>
+__device__ __forceinline__ Piece piece_at(const AttnArgs &a, P &plan, int64_t at, int64_t end, int64_t blk) {
+    Piece c;
+    c.x = plan.enter(owner_of(plan.work, a.B_u, at));
+    // Within a user units and pages are counted in 64 bits; a unit's number fits 32.
+    const int64_t local = at - c.x.from;
+    const int64_t unit = local / c.x.pages;
+    c.p0 = (int)(local - unit * c.x.pages);
+    c.p1 = (int)min((int64_t)c.x.pages, c.p0 + (end - at));
+    c.h = (int)unit / c.x.tiles;
+    c.tile = (int)unit - c.h * c.x.tiles;
+    c.whole = c.p0 == 0 && c.p1 == c.x.pages;
+    c.slot = 2 * blk + (c.p0 == 0);
+    c.n = c.p0 == 0 && !c.whole ? (int)((at + c.x.pages - 1) / plan.share - blk) + 1 : 0;
+    return c;
+}
+
+// Where row r of the piece's user and head stands in O.
+template <class P>
+__device__ __forceinline__ int64_t out_at(const AttnArgs &a, const P &plan, const Piece &c, int r) {
+    int cnd, l, hq;
+    plan.row(c.x, c.h, r, cnd, l, hq);
+    return cnd * a.o_cand + hq * a.o_head + l * a.o_query;
+}
+
+// Blocks are dealt to the 8 dies in turn: give each die neighbouring runs, whose units share K and V.
+__device__ __forceinline__ int64_t run_of_block(int blocks) {
+    return (blocks & 7) ? blockIdx.x : (int64_t)(blockIdx.x & 7) * (blocks >> 3) + (blockIdx.x >> 3);
+}
+
+// The tiles of a run of pages: lane i keeps the page number of page base + i, so that a tile's address
+// needs no load of its own (64 pages at a time; a wait on the table in every turn cost the wide kernel
+// a third of its time).
+struct Pages {
+    const int32_t *row;
+    const char *tiles;                // head h of page 0
+    int64_t stride;                   // bytes from page to page
+    int base, last, num_pages, ids;
+    bool bad;
+    __device__ __forceinline__ void open(const AttnArgs &a, const Piece &c, int p0, int p1, int tile_bytes) {
+        row = a.table + (int64_t)c.x.u * a.table_stride;
+        tiles = a.tiles + (int64_t)c.h * tile_bytes;
+        stride = (int64_t)a.H_kv * tile_bytes;
+        num_pages = a.num_pages;
+        last = p1 - 1;
+        bad = false;
+        read(p0);
+    }
+    __device__ __forceinline__ void read(int p) {
+        base = p;
+        ids = row[min(p + ((int)threadIdx.x & 63), last)];
+    }
+    // The tile of page p (of the last page if p is behind it); p never decreases by more than the caller's look-ahead.
+    __device__ __forceinline__ const char *at(int p) {
+        p = min(p, last);
+        if (p - base >= 64) read(p);
+        int page = __builtin_amdgcn_readlane(ids, p - base);
+        if (page < 0 || page >= num_pages) { bad = true; page = 0; }
+        return tiles + page * stride;
+    }
+};
 
 // What a lane reads of a page.
 template <int HD>
@@ -290,82 +417,28 @@ struct PageRegs {
     }
 };
 
-template <int HD, int NT>
+template <int HD, int NT, bool SMALL>
 __global__ void __launch_bounds__(64) kv4_attn_kernel(AttnArgs a) {
-    constexpr int KS = HD / 32;   // 32-wide steps of d
-    constexpr int VJ = HD / 32;
-    constexpr int TILE = 68 * HD;
+    constexpr int VJ = HD / 32, TILE = 68 * HD;
+    __shared__ PlanLds<SMALL> small;
     const int lane = (int)threadIdx.x, g = lane >> 4, j = lane & 15;
-    const int chunk = a.hdr[0], n_units = a.ubase[a.B_u] * a.H_kv;
-    for (int unit = (int)blockIdx.x; unit < n_units; unit += (int)gridDim.x) {
-        // Units of a user in the order split, head, row tile: neighbours share their K and V.
-        const int u = owner_of(a.ubase, a.B_u, unit / a.H_kv);
-        const int c0 = a.off[u], n_rows = (a.off[u + 1] - c0) * a.L_q * a.G;
-        const int tiles = (n_rows + 16 * NT - 1) / (16 * NT);
-        const int local = unit - a.ubase[u] * a.H_kv;
-        const int tile_i = local % tiles, h = local / tiles % a.H_kv, split = local / tiles / a.H_kv;
-        const int len = clamp_len(a.lens[u], a.max_pages);
-        const int pages = (len + kPage - 1) / kPage;
-        const int n_pieces = pieces(pages, chunk);
-        const bool whole = n_pieces == 1;
-        const int p0 = cut(pages, n_pieces, split);
-
-        // This lane's query rows j, 16 + j, ..: their candidate, query and head, and what they see.
-        int64_t o_at[NT];
-        int limit[NT];
-        u32x4_t qf[KS][NT];
-        bool live[NT];
-        int most = 0, least = len;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int row = tile_i * 16 * NT + 16 * n + j;
-            live[n] = row < n_rows;
-            const int r = live[n] ? row : 0;
-            const int cand = a.perm[c0 + r / (a.L_q * a.G)], rest = r % (a.L_q * a.G);
-            const int l = rest / a.G, hq = h * a.G + rest % a.G;
-            o_at[n] = cand * a.o_cand + hq * a.o_head + l * a.o_query;
-            limit[n] = live[n] ? len : 0;
-            if (live[n] && a.positions) {
-                const int pos = a.positions[(int64_t)cand * a.L_q + l];
-                limit[n] = pos < 0 ? 0 : pos < len ? pos + 1 : len;
-            }
-            const uint16_t *q = a.Q + cand * a.q_cand + hq * a.q_head + l * a.q_query + g * (HD / 4);
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-                qf[s][n] = live[n] ? *reinterpret_cast<const u32x4_t *>(q + 8 * s) : (u32x4_t){0, 0, 0, 0};
-            most = max(most, limit[n]);
-            if (live[n]) least = min(least, limit[n]);
-        }
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) {
-            most = max(most, __shfl_xor(most, d));
-            least = min(least, __shfl_xor(least, d));
-        }
-        most = __builtin_amdgcn_readfirstlane(most);
-        least = __builtin_amdgcn_readfirstlane(least);
-        const int p1 = min(cut(pages, n_pieces, split + 1), (most + kPage - 1) / kPage);   // no row sees further pages
-
-        f32x4_t o[2 * VJ][NT], lsum[NT];
-        float m[NT], nm[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            m[n] = -__builtin_inff();
-            nm[n] = 0.f;
-            lsum[n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int x = 0; x < 2 * VJ; ++x) o[x][n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-        }
-        const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-        const int32_t *row = a.table + (int64_t)u * a.table_stride;
-        bool bad_page = false;
-        auto tile_at = [&](int p) {
-            int page = __builtin_amdgcn_readfirstlane(row[p]);
-            if (page < 0 || page >= a.num_pages) { bad_page = true; page = 0; }
-            return a.tiles + ((int64_t)page * a.H_kv + h) * TILE;
-        };
+    Plan<SMALL, 64> plan(a, reinterpret_cast<SmallPlan *>(&small));
+    const int64_t blk = run_of_block((int)gridDim.x), all = plan.work[a.B_u], end = min(all, (blk + 1) * plan.share);
+    int2 note = make_int2(0, 0);
+    for (int64_t at = blk * plan.share; at < end;) {
+        const Piece c = piece_at(a, plan, at, end, blk);
+        if (c.n) note = make_int2(c.n, min(a.R, c.x.n_rows - c.tile * a.R));
+        at += c.p1 - c.p0;
+        Queries<HD, NT> q;
+        // The d order of K and Q: lane group g takes the g-th quarter of a head, one piece of a K row.
+        q.load(a, plan, c.x, c.h, c.tile * 16 * NT, j, g * (HD / 4), 8);
+        const int p1 = min(c.p1, (q.most + kPage - 1) / kPage);   // no row sees further pages
+        Pages pages;
+        pages.bad = false;
+        if (c.p0 < p1) pages.open(a, c, c.p0, p1, TILE);
         PageRegs<HD> pg;
-        for (int p = p0; p < p1; ++p) {
-            const char *tile = tile_at(p);
+        for (int p = c.p0; p < p1; ++p) {
+            const char *tile = pages.at(p);
             pg.load_k(tile, g, j);
             pg.load_v(tile, g, j);
             f32x4_t S[4][NT];
@@ -375,279 +448,187 @@ __global__ void __launch_bounds__(64) kv4_attn_kernel(AttnArgs a) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) S[t][n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
+                for (int s = 0; s < HD / 32; ++s) {
                     const u32x4_t kf = values8(pg.k[t][s], ks);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) S[t][n] = mfma_bf16(kf, qf[s][n], S[t][n]);
+                    for (int n = 0; n < NT; ++n) S[t][n] = mfma_bf16(kf, q.qf[s][n], S[t][n]);
                 }
             }
-            const int key0 = p * kPage + 16 * g;   // this lane's tokens: key0 + 4 t + i
-            if (p * kPage + kPage > least) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (key0 + 4 * t + i >= limit[n]) S[t][n][i] = -__builtin_inff();
-            }
-            if (p * kPage + kPage > len) {
-                // Tokens past the history may hold anything: scale 2^-127 keeps their values finite,
-                // and their weights are 0.
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int n = len - (key0 + 4 * t);
-                    const uint32_t keep = n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
-#pragma unroll
-                    for (int jj = 0; jj < VJ; ++jj) pg.vs[jj][t] &= keep;
-                }
-            }
-            bool grow = false;
-            float mb[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float x = -__builtin_inff();
+            if (p * kPage + kPage > c.x.len) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x = fmaxf(x, S[t][n][i]);
-                mb[n] = max_over_groups(x) * a.scale_log2;
-                grow = grow || mb[n] > m[n] + kSlack;
-            }
-            if (__ballot(grow)) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float mn = fmaxf(m[n], mb[n]);
-                    const float alpha = mn == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
-                    m[n] = mn;
-                    nm[n] = mn == -__builtin_inff() ? 0.f : -mn;
-                    lsum[n] *= alpha;
-#pragma unroll
-                    for (int x = 0; x < 2 * VJ; ++x) o[x][n] *= alpha;
-                }
+                    for (int jj = 0; jj < VJ; ++jj) pg.vs[jj][t] = existing(pg.vs[jj][t], c.x.len - (p * kPage + 16 * g + 4 * t));
             }
             u32x4_t pf[2][NT];
+            q.raise(S, p, g, a.scale_log2);
+            q.weigh(S, a.scale_log2, pf);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    float w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[t][n][i], a.scale_log2, nm[n]));
-                    pf[t >> 1][n][2 * (t & 1)] = pack_bf16x2(w[0], w[1]);
-                    pf[t >> 1][n][2 * (t & 1) + 1] = pack_bf16x2(w[2], w[3]);
-                }
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) lsum[n] = mfma_bf16(ones, pf[kk][n], lsum[n]);
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                 for (int jj = 0; jj < VJ; ++jj) {
                     u32x4_t even, odd;
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t c = pg.v[jj][2 * kk + x], s = pg.vs[jj][2 * kk + x];
-                        const uint32_t v0 = values2<0>(c, scale_of(s, 0)), v1 = values2<1>(c, scale_of(s, 1));
-                        const uint32_t v2 = values2<2>(c, scale_of(s, 2)), v3 = values2<3>(c, scale_of(s, 3));
-                        even[2 * x] = pair16(v0, v1, false);
-                        even[2 * x + 1] = pair16(v2, v3, false);
-                        odd[2 * x] = pair16(v0, v1, true);
-                        odd[2 * x + 1] = pair16(v2, v3, true);
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t e0, e1, o0, o1;
+                        values_v(pg.v[jj][2 * kk + y], pg.vs[jj][2 * kk + y], e0, e1, o0, o1);
+                        even[2 * y] = e0;
+                        even[2 * y + 1] = e1;
+                        odd[2 * y] = o0;
+                        odd[2 * y + 1] = o1;
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        o[2 * jj][n] = mfma_bf16(even, pf[kk][n], o[2 * jj][n]);
-                        o[2 * jj + 1][n] = mfma_bf16(odd, pf[kk][n], o[2 * jj + 1][n]);
+                        q.o[2 * jj][n] = mfma_bf16(even, pf[kk][n], q.o[2 * jj][n]);
+                        q.o[2 * jj + 1][n] = mfma_bf16(odd, pf[kk][n], q.o[2 * jj + 1][n]);
                     }
                 }
-            }
         }
-        if (bad_page && lane == 0) atomicOr(a.status, kStPage);
+        if (pages.bad && lane == 0) atomicOr(a.status, kStPage);
 
         // Lane (g, j) holds of query j the elements 32 jj + 8 g + 2 i (even tile) and + 1 (odd tile).
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            if (!live[n]) continue;
-            const float l = lsum[n][0];
-            if (whole) {
-                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;   // a row that sees nothing is 0
+            const int in_unit = 16 * n + j, r = c.tile * 16 * NT + in_unit;
+            if (r >= c.x.n_rows) continue;
+            const float l = q.lsum[n][0];
+            const int64_t o_at = out_at(a, plan, c, r);
+            if (c.n && g == 0) a.note_o[blk * a.R + in_unit] = o_at;
+            if (c.whole) {
+                const float inv = inverse_of(l);
 #pragma unroll
                 for (int jj = 0; jj < VJ; ++jj) {
                     u32x4_t w;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(o[2 * jj][n][i] * inv, o[2 * jj + 1][n][i] * inv);
-                    *reinterpret_cast<u32x4_t *>(a.O + o_at[n] + 32 * jj + 8 * g) = w;
+                    for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(q.o[2 * jj][n][i] * inv, q.o[2 * jj + 1][n][i] * inv);
+                    *reinterpret_cast<u32x4_t *>(a.O + o_at + 32 * jj + 8 * g) = w;
                 }
             } else {
-                // Partial results in the units' order.
-                const int64_t at = ((int64_t)(unit - (a.ubase[u] - a.pbase[u]) * a.H_kv)) * (16 * NT) + 16 * n + j;
-                if (g == 0) a.ml[at] = make_float2(m[n], l);
-                float *to = a.part + at * HD;
+                const int64_t to = c.slot * (16 * NT) + in_unit;
+                if (g == 0) a.ml[to] = make_float2(q.m[n], l);
 #pragma unroll
                 for (int jj = 0; jj < VJ; ++jj) {
                     f32x4_t w0, w1;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        w0[2 * i] = o[2 * jj][n][i];
-                        w0[2 * i + 1] = o[2 * jj + 1][n][i];
-                        w1[2 * i] = o[2 * jj][n][2 + i];
-                        w1[2 * i + 1] = o[2 * jj + 1][n][2 + i];
+                        w0[2 * i] = q.o[2 * jj][n][i];
+                        w0[2 * i + 1] = q.o[2 * jj + 1][n][i];
+                        w1[2 * i] = q.o[2 * jj][n][2 + i];
+                        w1[2 * i + 1] = q.o[2 * jj + 1][n][2 + i];
                     }
-                    *reinterpret_cast<f32x4_t *>(to + 32 * jj + 8 * g) = w0;
-                    *reinterpret_cast<f32x4_t *>(to + 32 * jj + 8 * g + 4) = w1;
+                    *reinterpret_cast<f32x4_t *>(a.part + to * HD + 32 * jj + 8 * g) = w0;
+                    *reinterpret_cast<f32x4_t *>(a.part + to * HD + 32 * jj + 8 * g + 4) = w1;
                 }
             }
         }
     }
+    if (lane == 0) a.note[blk] = note;
 }
 
 // ---- the wide kernel -----------------------------------------------------------------------
 
-// A page in LDS: K rows [64 tokens][HD] and V^T rows [HD][64 tokens], bf16.  The 16-byte chunks of a
-// row stand permuted by an XOR with a row number so that the 16 rows of one operand read fall on
-// different banks: for K the row's place j in the operand, for V^T the row itself.
+// Two page buffers in LDS: K rows [64 tokens][HD] and V^T rows [HD][64 tokens], bf16.  The 16-byte
+// chunks of a row stand permuted by an XOR with a number of the row, so that the 16 rows of one operand
+// read fall on different banks (for K the row's place j in the operand; where a row is 128 bytes, two
+// neighbouring rows share the 256 bytes of all banks and half that number is taken).
 template <int HD>
 struct WideLds {
     static constexpr int KBYTES = kPage * HD * 2, PAGE = 2 * KBYTES;
     static __device__ __forceinline__ int k_at(int key, int c) {
         const int j = 4 * (key >> 4) + (key & 3);
-        return key * HD * 2 + ((c ^ (j & (HD / 8 - 1))) << 4);
+        return key * HD * 2 + ((c ^ (HD == 128 ? j : j >> 1)) << 4);
     }
-    static __device__ __forceinline__ int v_at(int d, int c) { return KBYTES + d * kPage * 2 + ((c ^ (d & 7)) << 4); }
+    static __device__ __forceinline__ int v_at(int d, int c) { return KBYTES + d * kPage * 2 + ((c ^ ((d >> 1) & 7)) << 4); }
 };
 
-template <int HD>
-__global__ void __launch_bounds__(64 * kWideWaves, 2) kv4_wide_kernel(AttnArgs a) {
+// A barrier that waits for this wave's LDS accesses only: codes in flight stay so.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+    wg_barrier();
+}
+
+template <int HD, bool SMALL>
+__global__ void __launch_bounds__(256, 2) kv4_wide_kernel(AttnArgs a) {
     typedef WideLds<HD> L;
-    constexpr int NT = 2, TK = HD / 32, DT = HD / 16, TILE = 68 * HD;
-    constexpr int JOBS = kPage * HD / 16 / (64 * kWideWaves);   // 8-byte pieces of K codes (and of V codes) per thread
+    constexpr int NT = 2, WAVES = 4, THREADS = 64 * WAVES, TK = HD / 32, DT = HD / 16, TILE = 68 * HD;
+    constexpr int JOBS = kPage * HD / 16 / THREADS;   // 8-byte pieces of a page's K codes (and of its V codes) per thread
     extern __shared__ __align__(16) char lds[];
-    __shared__ int s_most[kWideWaves];
+    __shared__ PlanLds<SMALL> small;
+    __shared__ int s_most[WAVES];
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, j = lane & 15;
-    const int chunk = a.hdr[0], n_units = a.ubase[a.B_u] * a.H_kv;
-    for (int unit = (int)blockIdx.x; unit < n_units; unit += (int)gridDim.x) {
-        const int u = owner_of(a.ubase, a.B_u, unit / a.H_kv);
-        const int c0 = a.off[u], n_rows = (a.off[u + 1] - c0) * a.L_q * a.G;
-        const int tiles = (n_rows + kWideRows - 1) / kWideRows;
-        const int local = unit - a.ubase[u] * a.H_kv;
-        const int tile_i = local % tiles, h = local / tiles % a.H_kv, split = local / tiles / a.H_kv;
-        const int len = clamp_len(a.lens[u], a.max_pages);
-        const int pages = (len + kPage - 1) / kPage;
-        const int n_pieces = pieces(pages, chunk);
-        const bool whole = n_pieces == 1;
-        const int p0 = cut(pages, n_pieces, split);
-
-        int64_t o_at[NT];
-        int limit[NT];
-        u32x4_t qf[TK][NT];
-        bool live[NT];
-        int most = 0, least = len;
+    Plan<SMALL, THREADS> plan(a, reinterpret_cast<SmallPlan *>(&small));
+    const int64_t blk = run_of_block((int)gridDim.x), line = plan.work[a.B_u], end = min(line, (blk + 1) * plan.share);
+    int2 note = make_int2(0, 0);
+    // This thread's operand reads and its places of converted pieces: K piece i is 16 elements of token
+    // i / (HD/16), V piece i 8 tokens of element pair i / 8.
+    int k_off[TK], v_off[2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int row = tile_i * kWideRows + wv * 16 * NT + 16 * n + j;
-            live[n] = row < n_rows;
-            const int r = live[n] ? row : 0;
-            const int cand = a.perm[c0 + r / (a.L_q * a.G)], rest = r % (a.L_q * a.G);
-            const int l = rest / a.G, hq = h * a.G + rest % a.G;
-            o_at[n] = cand * a.o_cand + hq * a.o_head + l * a.o_query;
-            limit[n] = live[n] ? len : 0;
-            if (live[n] && a.positions) {
-                const int pos = a.positions[(int64_t)cand * a.L_q + l];
-                limit[n] = pos < 0 ? 0 : pos < len ? pos + 1 : len;
-            }
-            const uint16_t *q = a.Q + cand * a.q_cand + hq * a.q_head + l * a.q_query + 8 * g;
+    for (int s = 0; s < TK; ++s) k_off[s] = L::k_at(16 * (j >> 2) + (j & 3), 4 * s + g);   // tile t: + 4 t rows
 #pragma unroll
-            for (int t = 0; t < TK; ++t)
-                qf[t][n] = live[n] ? *reinterpret_cast<const u32x4_t *>(q + 32 * t) : (u32x4_t){0, 0, 0, 0};
-            most = max(most, limit[n]);
-            if (live[n]) least = min(least, limit[n]);
-        }
+    for (int kk = 0; kk < 2; ++kk) v_off[kk] = L::v_at(j, 2 * g + kk);                       // tile x: + 16 x rows
+    for (int64_t at = blk * plan.share; at < end;) {
+        const Piece c = piece_at(a, plan, at, end, blk);
+        if (c.n) note = make_int2(c.n, min(a.R, c.x.n_rows - c.tile * a.R));
+        at += c.p1 - c.p0;
+        Queries<HD, NT> q;
+        q.load(a, plan, c.x, c.h, c.tile * kWideRows + wv * 16 * NT, j, 8 * g, 32);
+        if (lane == 0) s_most[wv] = q.most;
+        __syncthreads();   // also: the block's last reads of the previous piece's pages are done
+        int most = 0;
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1) {
-            most = max(most, __shfl_xor(most, d));
-            least = min(least, __shfl_xor(least, d));
-        }
-        most = __builtin_amdgcn_readfirstlane(most);
-        least = __builtin_amdgcn_readfirstlane(least);
-        if (lane == 0) s_most[wv] = most;
-        __syncthreads();   // also: the block's last reads of the previous unit's pages are done
-        int all = 0;
-#pragma unroll
-        for (int w = 0; w < kWideWaves; ++w) all = max(all, s_most[w]);
-        const int p1 = min(cut(pages, n_pieces, split + 1), (all + kPage - 1) / kPage);   // no row sees further pages
-
-        f32x4_t o[DT][NT], lsum[NT];
-        float m[NT], nm[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            m[n] = -__builtin_inff();
-            nm[n] = 0.f;
-            lsum[n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int x = 0; x < DT; ++x) o[x][n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-        }
-        const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-        const int32_t *row = a.table + (int64_t)u * a.table_stride;
-        bool bad_page = false;
-
-        // Codes and scales of a page, this thread's pieces: K piece c is 16 elements of token
-        // c / (HD/16); V piece c is 8 tokens of element pair c / 8.
-        u32x2_t kc[JOBS], vc[JOBS], vs[JOBS];
-        uint32_t ks[JOBS];
-        auto fetch = [&](int p) {
-            int page = __builtin_amdgcn_readfirstlane(row[p]);
-            if (page < 0 || page >= a.num_pages) { bad_page = true; page = 0; }
-            const char *tile = a.tiles + ((int64_t)page * a.H_kv + h) * TILE;
-#pragma unroll
-            for (int i = 0; i < JOBS; ++i) {
-                const int c = tid + i * 64 * kWideWaves;
-                const int key = c / (HD / 16), part = c % (HD / 16);
-                kc[i] = *reinterpret_cast<const u32x2_t *>(tile + 8 * c);
-                ks[i] = (uint8_t)tile[64 * HD + (part >> 1) * 64 + (key & 48) + 4 * (key & 3) + ((key >> 2) & 3)];
-                vc[i] = *reinterpret_cast<const u32x2_t *>(tile + 32 * HD + 8 * c);
-                vs[i] = *reinterpret_cast<const u32x2_t *>(tile + 66 * HD + (c >> 7) * 64 + 8 * (c & 7));
-            }
-        };
-        auto convert = [&](int p) {
-            char *to = lds + (p & 1) * L::PAGE;
-#pragma unroll
-            for (int i = 0; i < JOBS; ++i) {
-                const int c = tid + i * 64 * kWideWaves;
-                const int key = c / (HD / 16), part = c % (HD / 16);
-                const float s = scale_of(ks[i], 0);
-                *reinterpret_cast<u32x4_t *>(to + L::k_at(key, 2 * part)) = values8(kc[i][0], s);
-                *reinterpret_cast<u32x4_t *>(to + L::k_at(key, 2 * part + 1)) = values8(kc[i][1], s);
-                const int pair = c >> 3, k0 = 8 * (c & 7);
-                u32x4_t even, odd;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t sc = vs[i][x];
-                    // Tokens past the history may hold anything: scale 2^-127 keeps their values
-                    // finite, and their weights are 0.
-                    const int n = len - (p * kPage + k0 + 4 * x);
-                    if (n < 4) sc &= n <= 0 ? 0u : (1u << (8 * n)) - 1u;
-                    const uint32_t v0 = values2<0>(vc[i][x], scale_of(sc, 0)), v1 = values2<1>(vc[i][x], scale_of(sc, 1));
-                    const uint32_t v2 = values2<2>(vc[i][x], scale_of(sc, 2)), v3 = values2<3>(vc[i][x], scale_of(sc, 3));
-                    even[2 * x] = pair16(v0, v1, false);
-                    even[2 * x + 1] = pair16(v2, v3, false);
-                    odd[2 * x] = pair16(v0, v1, true);
-                    odd[2 * x + 1] = pair16(v2, v3, true);
-                }
-                *reinterpret_cast<u32x4_t *>(to + L::v_at(2 * pair, k0 >> 3)) = even;
-                *reinterpret_cast<u32x4_t *>(to + L::v_at(2 * pair + 1, k0 >> 3)) = odd;
-            }
-        };
+        for (int w = 0; w < WAVES; ++w) most = max(most, s_most[w]);
+        const int p0 = c.p0, p1 = min(c.p1, (most + kPage - 1) / kPage);   // no row sees further pages
         if (p0 < p1) {
-            fetch(p0);
-            convert(p0);
-            if (p0 + 1 < p1) fetch(p0 + 1);
-        }
-        __syncthreads();
-        for (int p = p0; p < p1; ++p) {
-            const char *from = lds + (p & 1) * L::PAGE;
-            f32x4_t S[4][NT];
-            const bool busy = p * kPage < most;   // some row of this wave sees the page
-            if (busy) {
+            Pages pages;
+            pages.open(a, c, p0, p1, TILE);
+            u32x2_t kc[JOBS], vc[JOBS], vs[JOBS];
+            uint32_t ks[JOBS];
+            auto fetch = [&](int p) {
+                const char *tile = pages.at(p);
+#pragma unroll
+                for (int y = 0; y < JOBS; ++y) {
+                    const int i = tid + y * THREADS, key = i / (HD / 16), part = i % (HD / 16);
+                    kc[y] = *reinterpret_cast<const u32x2_t *>(tile + 8 * i);
+                    ks[y] = (uint8_t)tile[64 * HD + (part >> 1) * 64 + (key & 48) + 4 * (key & 3) + ((key >> 2) & 3)];
+                    vc[y] = *reinterpret_cast<const u32x2_t *>(tile + 32 * HD + 8 * i);
+                    vs[y] = *reinterpret_cast<const u32x2_t *>(tile + 66 * HD + (i >> 7) * 64 + 8 * (i & 7));
+                }
+            };
+            auto convert = [&](int p) {
+                char *to = lds + (p & 1) * L::PAGE;
+#pragma unroll
+                for (int y = 0; y < JOBS; ++y) {
+                    const int i = tid + y * THREADS, key = i / (HD / 16), part = i % (HD / 16);
+                    const float s = scale_of(ks[y], 0);
+                    *reinterpret_cast<u32x4_t *>(to + L::k_at(key, 2 * part)) = values8(kc[y][0], s);
+                    *reinterpret_cast<u32x4_t *>(to + L::k_at(key, 2 * part + 1)) = values8(kc[y][1], s);
+                }
+                const int left = c.x.len - min(p, p1 - 1) * kPage;   // tokens of the page that exist
+                if (left < kPage) {
+#pragma unroll
+                    for (int y = 0; y < JOBS; ++y)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) vs[y][x] = existing(vs[y][x], left - (8 * ((tid + y * THREADS) & 7) + 4 * x));
+                }
+#pragma unroll
+                for (int y = 0; y < JOBS; ++y) {
+                    const int i = tid + y * THREADS, pair = i >> 3;
+                    u32x4_t even, odd;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t e0, e1, o0, o1;
+                        values_v(vc[y][x], vs[y][x], e0, e1, o0, o1);
+                        even[2 * x] = e0;
+                        even[2 * x + 1] = e1;
+                        odd[2 * x] = o0;
+                        odd[2 * x + 1] = o1;
+                    }
+                    *reinterpret_cast<u32x4_t *>(to + L::v_at(2 * pair, i & 7)) = even;
+                    *reinterpret_cast<u32x4_t *>(to + L::v_at(2 * pair + 1, i & 7)) = odd;
+                }
+            };
+            auto scores = [&](int p, f32x4_t (&S)[4][NT]) {
+                const char *from = lds + (p & 1) * L::PAGE;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -656,164 +637,122 @@ __global__ void __launch_bounds__(64 * kWideWaves, 2) kv4_wide_kernel(AttnArgs a
                 for (int s = 0; s < TK; ++s)
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
-                        const u32x4_t kf = *reinterpret_cast<const u32x4_t *>(from + L::k_at(16 * (j >> 2) + 4 * t + (j & 3), 4 * s + g));
+                        const u32x4_t kf = *reinterpret_cast<const u32x4_t *>(from + k_off[s] + t * 4 * HD * 2);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) S[t][n] = mfma_bf16(kf, qf[s][n], S[t][n]);
+                        for (int n = 0; n < NT; ++n) S[t][n] = mfma_bf16(kf, q.qf[s][n], S[t][n]);
                     }
-            }
-            // The other page buffer was last read before the barrier that ended the previous turn.
-            if (p + 1 < p1) {
-                convert(p + 1);
-                if (p + 2 < p1) fetch(p + 2);
-            }
-            if (busy) {
-                const int key0 = p * kPage + 16 * g;   // this lane's tokens: key0 + 4 t + i
-                if (p * kPage + kPage > least) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (key0 + 4 * t + i >= limit[n]) S[t][n][i] = -__builtin_inff();
-                }
-                bool grow = false;
-                float mb[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float x = -__builtin_inff();
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x = fmaxf(x, S[t][n][i]);
-                    mb[n] = max_over_groups(x) * a.scale_log2;
-                    grow = grow || mb[n] > m[n] + kSlack;
-                }
-                if (__ballot(grow)) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float mn = fmaxf(m[n], mb[n]);
-                        const float alpha = mn == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
-                        m[n] = mn;
-                        nm[n] = mn == -__builtin_inff() ? 0.f : -mn;
-                        lsum[n] *= alpha;
-#pragma unroll
-                        for (int x = 0; x < DT; ++x) o[x][n] *= alpha;
-                    }
-                }
+            };
+            auto accumulate = [&](int p, const f32x4_t (&S)[4][NT]) {
+                const char *from = lds + (p & 1) * L::PAGE;
                 u32x4_t pf[2][NT];
+                q.weigh(S, a.scale_log2, pf);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        float w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[t][n][i], a.scale_log2, nm[n]));
-                        pf[t >> 1][n][2 * (t & 1)] = pack_bf16x2(w[0], w[1]);
-                        pf[t >> 1][n][2 * (t & 1) + 1] = pack_bf16x2(w[2], w[3]);
-                    }
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) lsum[n] = mfma_bf16(ones, pf[kk][n], lsum[n]);
+                for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                     for (int x = 0; x < DT; ++x) {
-                        const u32x4_t vf = *reinterpret_cast<const u32x4_t *>(from + L::v_at(16 * x + j, 2 * g + kk));
+                        const u32x4_t vf = *reinterpret_cast<const u32x4_t *>(from + v_off[kk] + x * 16 * kPage * 2);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) o[x][n] = mfma_bf16(vf, pf[kk][n], o[x][n]);
+                        for (int n = 0; n < NT; ++n) q.o[x][n] = mfma_bf16(vf, pf[kk][n], q.o[x][n]);
                     }
-                }
+            };
+            f32x4_t S[4][NT];
+            fetch(p0);
+            convert(p0);
+            fetch(p0 + 1);
+            lds_barrier();
+            // Pages behind the last are taken again from the last one (into a buffer that nothing reads),
+            // which keeps the turns free of branches.
+            for (int p = p0; p < p1; ++p) {
+                convert(p + 1);   // its buffer was last read before the barrier that ended the previous turn
+                fetch(p + 2);
+                scores(p, S);
+                q.raise(S, p, g, a.scale_log2);
+                accumulate(p, S);
+                lds_barrier();
             }
-            __syncthreads();
+            if (pages.bad && tid == 0) atomicOr(a.status, kStPage);
         }
-        if (bad_page && tid == 0) atomicOr(a.status, kStPage);
 
         // Lane (g, j) holds of query j the elements 16 x + 4 g + i.
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            if (!live[n]) continue;
-            const float l = lsum[n][0];
-            if (whole) {
-                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;   // a row that sees nothing is 0
+            const int in_unit = wv * 16 * NT + 16 * n + j, r = c.tile * kWideRows + in_unit;
+            if (r >= c.x.n_rows) continue;
+            const float l = q.lsum[n][0];
+            const int64_t o_at = out_at(a, plan, c, r);
+            if (c.n && g == 0) a.note_o[blk * a.R + in_unit] = o_at;
+            if (c.whole) {
+                const float inv = inverse_of(l);
 #pragma unroll
                 for (int x = 0; x < DT; ++x)
-                    *reinterpret_cast<u32x2_t *>(a.O + o_at[n] + 16 * x + 4 * g) =
-                        (u32x2_t){pack_bf16x2(o[x][n][0] * inv, o[x][n][1] * inv), pack_bf16x2(o[x][n][2] * inv, o[x][n][3] * inv)};
+                    *reinterpret_cast<u32x2_t *>(a.O + o_at + 16 * x + 4 * g) =
+                        (u32x2_t){pack_bf16x2(q.o[x][n][0] * inv, q.o[x][n][1] * inv), pack_bf16x2(q.o[x][n][2] * inv, q.o[x][n][3] * inv)};
             } else {
-                const int64_t at = ((int64_t)(unit - (a.ubase[u] - a.pbase[u]) * a.H_kv)) * kWideRows + wv * 16 * NT + 16 * n + j;
-                if (g == 0) a.ml[at] = make_float2(m[n], l);
+                const int64_t to = c.slot * kWideRows + in_unit;
+                if (g == 0) a.ml[to] = make_float2(q.m[n], l);
 #pragma unroll
-                for (int x = 0; x < DT; ++x) *reinterpret_cast<f32x4_t *>(a.part + at * HD + 16 * x + 4 * g) = o[x][n];
+                for (int x = 0; x < DT; ++x) *reinterpret_cast<f32x4_t *>(a.part + to * HD + 16 * x + 4 * g) = q.o[x][n];
             }
         }
     }
+    if (tid == 0) a.note[blk] = note;
 }
 
-// Joins the partial results of the row tiles that were split: O = sum_s w_s O_s / sum_s w_s l_s with
-// w_s = 2^(m_s - max m).  A block per row: the pieces' weights once into LDS, then wave w sums the
-// pieces w, w + 4, .. (lane i: HD/64 neighbouring elements), and the four sums meet in LDS.
+// ---- joining partial results ---------------------------------------------------------------
+
+// O = sum_s w_s O_s / sum_s w_s l_s with w_s = 2^(m_s - max m) over the n pieces of a unit: slot
+// 2 b + 1 of the block b that it begins in, and slots 2 (b + s) of those after it.  A block takes 16 rows
+// of the unit that its note names; its 8 waves share the rows out, and where there are fewer rows than
+// waves, several waves share the pieces of a row (lane i: HD/64 neighbouring elements).
 template <int HD>
-__global__ void __launch_bounds__(256) kv4_join_kernel(AttnArgs a) {
-    constexpr int E = HD / 64, kBatch = 512;
-    __shared__ float s_wt[kBatch], s_sum[4][HD], s_red[4], s_l[4];
-    const int tid = (int)threadIdx.x, lane = tid & 63, wv = tid >> 6;
-    const int R = a.rows_per_unit;
-    const int64_t n_rows_all = (int64_t)a.tbase[a.B_u] * a.H_kv * R;
-    const int chunk = a.hdr[0];
-    for (int64_t x = blockIdx.x; x < n_rows_all; x += gridDim.x) {
-        const int th = (int)(x / R), r_in = (int)(x % R);
-        const int u = owner_of(a.tbase, a.B_u, th / a.H_kv);
-        const int c0 = a.off[u], n_rows = (a.off[u + 1] - c0) * a.L_q * a.G;
-        const int tiles = (n_rows + R - 1) / R;
-        const int local = th - a.tbase[u] * a.H_kv;
-        const int tile_i = local % tiles, h = local / tiles;
-        const int r = tile_i * R + r_in;
-        if (r >= n_rows) continue;
-        const int n = pieces((clamp_len(a.lens[u], a.max_pages) + kPage - 1) / kPage, chunk);
-        const int64_t first = ((int64_t)a.pbase[u] * a.H_kv + h * tiles + tile_i) * R + r_in;
-        const int64_t step = (int64_t)tiles * a.H_kv * R;
-        float top = -__builtin_inff();
-        for (int s = tid; s < n; s += 256) top = fmaxf(top, a.ml[first + s * step].x);
-        for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-        if (lane == 0) s_red[wv] = top;
-        __syncthreads();
-        top = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+__global__ void __launch_bounds__(512) kv4_join_kernel(AttnArgs a) {
+    constexpr int E = HD / 64;
+    __shared__ float s_acc[8][HD];
+    const int lane = (int)threadIdx.x & 63, wv = (int)threadIdx.x >> 6, r_first = 16 * (int)blockIdx.y;
+    const int64_t b = blockIdx.x;
+    const int2 note = a.note[b];
+    const int n = note.x, rows = min(16, note.y - r_first);
+    if (n == 0 || rows <= 0) return;
+    const int abreast = rows >= 5 ? 8 : rows >= 3 ? 4 : rows, share = 8 / abreast;   // rows at a time, waves per row
+    auto at = [&](int s, int r) { return (2 * (b + s) + (s == 0)) * a.R + r; };
+    for (int r0 = 0; r0 < rows; r0 += abreast) {
+        const int k = r0 + wv / share, r = r_first + k, part = wv % share;
+        const bool live = k < rows;
         float acc[E] = {}, l = 0.f;
-        for (int s0 = 0; s0 < n; s0 += kBatch) {
-            const int nb = min(kBatch, n - s0);
-            for (int s = tid; s < nb; s += 256) {
-                const float2 ml = a.ml[first + (s0 + s) * step];
-                const float w = ml.x == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
-                s_wt[s] = w;
+        if (live) {
+            float top = -__builtin_inff();
+            for (int s = lane; s < n; s += 64) top = fmaxf(top, a.ml[at(s, r)].x);
+            for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+            for (int s0 = 0; s0 < n; s0 += 64) {
+                const float2 ml = s0 + lane < n ? a.ml[at(s0 + lane, r)] : make_float2(-__builtin_inff(), 0.f);
+                const float w = weight_of(ml.x, top);
                 l += w * ml.y;
-            }
-            __syncthreads();
-            const float *p = a.part + (first + s0 * step) * HD + lane * E;
+                const int nb = min(64, n - s0);
 #pragma unroll 8
-            for (int s = wv; s < nb; s += 4) {
-                const float w = s_wt[s];
+                for (int s = part; s < nb; s += share) {
+                    const float ws = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), s));
+                    const float *p = a.part + at(s0 + s, r) * HD + lane * E;
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] += w * p[s * step * HD + e];
+                    for (int e = 0; e < E; ++e) acc[e] += ws * p[e];
+                }
             }
+            for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
+        }
+        if (share > 1) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) s_acc[wv][lane * E + e] = acc[e];
             __syncthreads();
-        }
-        for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
-        if (lane == 0) s_l[wv] = l;
+            if (live && part == 0)
+                for (int w = 1; w < share; ++w)
 #pragma unroll
-        for (int e = 0; e < E; ++e) s_sum[wv][lane * E + e] = acc[e];
-        __syncthreads();
-        if (tid < HD / 2) {
-            l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-            float y[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                y[e] = ((s_sum[0][2 * tid + e] + s_sum[1][2 * tid + e]) + (s_sum[2][2 * tid + e] + s_sum[3][2 * tid + e])) * inv;
-            const int cand = a.perm[c0 + r / (a.L_q * a.G)], rest = r % (a.L_q * a.G);
-            uint16_t *to = a.O + cand * a.o_cand + (int64_t)(h * a.G + rest % a.G) * a.o_head + (int64_t)(rest / a.G) * a.o_query;
-            reinterpret_cast<uint32_t *>(to)[tid] = pack_bf16x2(y[0], y[1]);
+                    for (int e = 0; e < E; ++e) acc[e] += s_acc[wv + w][lane * E + e];
         }
-        __syncthreads();
+        if (live && part == 0) {
+            const float inv = inverse_of(l);
+            uint16_t *to = a.O + a.note_o[b * a.R + r] + lane * E;
+            if constexpr (E == 2) *reinterpret_cast<uint32_t *>(to) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+            else *to = (uint16_t)pack_bf16x2(acc[0] * inv, 0.f);
+        }
     }
 }
 
@@ -822,29 +761,30 @@ inline int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 // Waves that group the candidates: their counts, one per wave and user, stay within 128 KB of LDS.
 inline int prep_waves(int B_u) { return std::max(1, std::min(kPrep / 64, 32768 / B_u)); }
 
-template <int HD>
-hipError_t launch(const AttnArgs &a, int64_t max_units, hipStream_t s) {
-    const int waves = a.map ? prep_waves(a.B_u) : 0;
-    const size_t lds = ((size_t)waves * a.B_u + a.B_u + 1) * sizeof(int);
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kv4_prep_kernel),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, 152 * 1024);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kv4_prep_kernel, dim3(1), dim3(kPrep), lds, s, a, waves);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    const dim3 grid((unsigned)std::min<int64_t>(max_units, 2 * a.units));
-    if (a.rows_per_unit == 16) hipLaunchKernelGGL((kv4_attn_kernel<HD, 1>), grid, dim3(64), 0, s, a);
-    else if (a.rows_per_unit == 32) hipLaunchKernelGGL((kv4_attn_kernel<HD, 2>), grid, dim3(64), 0, s, a);
+template <int HD, bool SMALL>
+hipError_t launch(const AttnArgs &a, int64_t line_most, hipStream_t s) {
+    hipError_t e = hipSuccess;
+    if constexpr (!SMALL) {
+        const int waves = a.map ? prep_waves(a.B_u) : 0;
+        const size_t lds = ((size_t)waves * a.B_u + a.B_u + 1) * sizeof(int);
+        e = hipFuncSetAttribute(reinterpret_cast<const void *>(kv4_prep_kernel), hipFuncAttributeMaxDynamicSharedMemorySize, 152 * 1024);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(kv4_prep_kernel, dim3(1), dim3(kPrep), lds, s, a, waves);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    // No more blocks than pages; a block past the line's end returns at once.
+    const dim3 grid((unsigned)std::min<int64_t>(line_most, 1ll << a.log_blocks));
+    if (a.R == 16) hipLaunchKernelGGL((kv4_attn_kernel<HD, 1, SMALL>), grid, dim3(64), 0, s, a);
+    else if (a.R == 32) hipLaunchKernelGGL((kv4_attn_kernel<HD, 2, SMALL>), grid, dim3(64), 0, s, a);
     else {
-        const auto k = kv4_wide_kernel<HD>;
+        const auto k = kv4_wide_kernel<HD, SMALL>;
         e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, 2 * WideLds<HD>::PAGE);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(k, grid, dim3(64 * kWideWaves), 2 * WideLds<HD>::PAGE, s, a);
+        hipLaunchKernelGGL(k, grid, dim3(256), 2 * WideLds<HD>::PAGE, s, a);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (a.max_pages > 1) {   // a history of one page is never split
-        const int64_t rows = (int64_t)a.B_c * a.L_q * a.G * a.H_kv;
-        hipLaunchKernelGGL(kv4_join_kernel<HD>, dim3((unsigned)std::min<int64_t>(rows, 2048)), dim3(256), 0, s, a);
-    }
+    if (a.max_pages > 1)   // a history of one page is never cut
+        hipLaunchKernelGGL(kv4_join_kernel<HD>, dim3(grid.x, (unsigned)((a.R + 15) / 16)), dim3(512), 0, s, a);
     return hipGetLastError();
 }
 
@@ -853,24 +793,23 @@ hipError_t launch(const AttnArgs &a, int64_t max_units, hipStream_t s) {
 Kv4AttnLayout kv4_attn_layout(int B_u, int B_c, int H_q, int H_kv, int L_q, int head_dim, int max_pages) {
     Kv4AttnLayout w{};
     const int64_t rows = (int64_t)B_c * L_q * (H_q / H_kv);
-    // Rows beside one another in a wave: as many tiles of 16 as the average user's rows fill.
+    // Rows beside one another: as many as the average user has.
     const int64_t mean = rows / B_u;
-    w.rows_per_unit = mean <= 16 ? 16 : mean <= 32 ? 32 : kWideRows;
-    w.units = w.rows_per_unit <= 32 ? kNarrowUnits : kWideUnits;
-    const int64_t tiles = (rows / w.rows_per_unit + std::min(B_u, B_c)) * H_kv;   // at most
-    // A history of 1.5 chunk pages or more is cut into at most pages / chunk + 1/2 <= 4/3 pages / chunk
-    // pieces, and all pages over the chunk are at most the units aimed at.
-    w.part_units = max_pages > 1 ? std::min<int64_t>(2 * w.units, tiles * max_pages) : 0;
+    w.R = mean <= 16 ? 16 : mean <= 32 ? 32 : kWideRows;
+    w.log_blocks = w.R == kWideRows ? kLogWide : kLogNarrow;
+    const int64_t tiles = (rows / w.R + std::min(B_u, B_c)) * H_kv;   // at most
+    w.line_most = std::max<int64_t>(1, tiles * max_pages);
+    const int64_t blocks = std::min<int64_t>(w.line_most, 1ll << w.log_blocks), slots = max_pages > 1 ? 2 * blocks : 0;
     int64_t at = 0;
     auto take = [&](int64_t bytes) { const int64_t o = at; at = up(at + bytes, 256); return o; };
-    w.o_hdr = take(64);
+    w.o_share = take(8);
+    w.o_work = take((int64_t)(B_u + 1) * 8);
     w.o_perm = take((int64_t)B_c * 4);
     w.o_off = take((int64_t)(B_u + 1) * 4);
-    w.o_ubase = take((int64_t)(B_u + 1) * 4);
-    w.o_pbase = take((int64_t)(B_u + 1) * 4);
-    w.o_tbase = take((int64_t)(B_u + 1) * 4);
-    w.o_ml = take(w.part_units * w.rows_per_unit * 8);
-    w.o_part = take(w.part_units * w.rows_per_unit * head_dim * 4);
+    w.o_note = take(blocks * 8);
+    w.o_note_o = take(blocks * w.R * 8);
+    w.o_ml = take(slots * w.R * 8);
+    w.o_part = take(slots * w.R * head_dim * 4);
     w.total = at;
     return w;
 }
@@ -878,13 +817,16 @@ Kv4AttnLayout kv4_attn_layout(int B_u, int B_c, int H_q, int H_kv, int L_q, int 
 hipError_t launch_kv4_attention(const ikbo_kv4_attention_args &x, const Kv4AttnLayout &w, float scale, hipStream_t s) {
     AttnArgs a{};
     char *ws = static_cast<char *>(x.workspace);
-    auto i32 = [&](int64_t o) { return reinterpret_cast<int32_t *>(ws + o); };
     a.Q = static_cast<const uint16_t *>(x.Q);
     a.O = static_cast<uint16_t *>(x.O);
     a.tiles = static_cast<const char *>(x.tiles);
     a.table = x.block_table; a.lens = x.lens; a.map = x.map; a.positions = x.positions; a.status = x.status;
-    a.hdr = i32(w.o_hdr); a.perm = i32(w.o_perm); a.off = i32(w.o_off);
-    a.ubase = i32(w.o_ubase); a.pbase = i32(w.o_pbase); a.tbase = i32(w.o_tbase);
+    a.share = reinterpret_cast<int64_t *>(ws + w.o_share);
+    a.work = reinterpret_cast<int64_t *>(ws + w.o_work);
+    a.perm = reinterpret_cast<int32_t *>(ws + w.o_perm);
+    a.off = reinterpret_cast<int32_t *>(ws + w.o_off);
+    a.note = reinterpret_cast<int2 *>(ws + w.o_note);
+    a.note_o = reinterpret_cast<int64_t *>(ws + w.o_note_o);
     a.ml = reinterpret_cast<float2 *>(ws + w.o_ml);
     a.part = reinterpret_cast<float *>(ws + w.o_part);
     a.q_cand = x.q_cand; a.q_head = x.q_head; a.q_query = x.q_query;
@@ -892,13 +834,11 @@ hipError_t launch_kv4_attention(const ikbo_kv4_attention_args &x, const Kv4AttnL
     a.table_stride = x.table_stride;
     a.B_u = x.B_u; a.B_c = x.B_c; a.H_kv = x.H_kv; a.G = x.H_q / x.H_kv; a.L_q = x.L_q;
     a.max_pages = x.max_pages; a.num_pages = x.num_pages;
-    a.rows_per_unit = w.rows_per_unit;
-    a.units = w.units;
+    a.R = w.R; a.log_blocks = w.log_blocks;
     a.scale_log2 = scale * 1.4426950408889634f;
-    const int64_t rows = (int64_t)x.B_c * x.L_q * a.G;
-    const int64_t tiles = (rows / w.rows_per_unit + std::min(x.B_u, x.B_c)) * x.H_kv;
-    const int64_t max_units = std::max<int64_t>(1, std::min<int64_t>(tiles * x.max_pages, tiles + w.units));
-    return x.head_dim == 128 ? launch<128>(a, max_units, s) : launch<64>(a, max_units, s);
+    if (x.B_u <= kSmallUsers && x.B_c <= kSmallCands)
+        return x.head_dim == 128 ? launch<128, true>(a, w.line_most, s) : launch<64, true>(a, w.line_most, s);
+    return x.head_dim == 128 ? launch<128, false>(a, w.line_most, s) : launch<64, false>(a, w.line_most, s);
 }
 
 }  // namespace ikbo

@@ -23,11 +23,11 @@ hipError_t launch_rope(const ikbo_rope_args &a, hipStream_t s);
 hipError_t launch_kv4_write(const ikbo_kv4_rows_args &a, hipStream_t s);
 hipError_t launch_kv4_read(const ikbo_kv4_rows_args &a, hipStream_t s);
 
-// Workspace of the attention: byte offsets of its parts.
+// How the attention's work is cut (hist_plan.h), and the byte offsets of its workspace's parts.
 struct Kv4AttnLayout {
-    int rows_per_unit, units;          // query rows of one unit, and about how many units are made
-    int64_t o_hdr, o_perm, o_off, o_ubase, o_pbase, o_tbase, o_ml, o_part, total;
-    int64_t part_units;                // units that may leave a partial result
+    int R, log_blocks;
+    int64_t line_most;                 // pages of work, at most
+    int64_t o_share, o_work, o_perm, o_off, o_note, o_note_o, o_ml, o_part, total;
 };
 Kv4AttnLayout kv4_attn_layout(int B_u, int B_c, int H_q, int H_kv, int L_q, int head_dim, int max_pages);
 hipError_t launch_kv4_attention(const ikbo_kv4_attention_args &a, const Kv4AttnLayout &w, float scale, hipStream_t s);

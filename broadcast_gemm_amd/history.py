@@ -3,7 +3,8 @@
 ``FaPlan`` attends over dense K and V that the caller holds per request.  Here a user's history lives in a
 cache of 4-bit codes, in pages of 64 tokens that a block table names; it grows by tokens and has a length of
 its own.  The calls bind the C ABI (``ikbo_kv_*``, ``ikbo_rope``, ``ikbo_kv4_*`` in ``include/ikbo.h``, which
-states formulas and layouts); every step runs in the library's HIP kernels, there is no CPU path.
+states formulas and layouts); every step runs in the library's HIP kernels, there is no CPU path.  Arguments
+are checked and outputs allocated in ``csrc/torch_history.cpp``.
 
     t = kv_tables(counts, lens, table, ring, state, capacity, status)     # pages, slots, positions, rows of a step
     q, k = rope(q, k, t.positions, freq)                                  # rotary positions (rope_frequencies)
@@ -26,40 +27,16 @@ from typing import NamedTuple, Optional, Tuple
 
 import torch
 
-from . import IKBO_ERR_INVALID_ARG, IKBO_OK, IkboError, lib
+from . import IKBO_OK, IkboError, lib
 
 PAGE = 64                  # tokens per page of the 4-bit cache
 MAX_USERS = 4096
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
-_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
-_vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
-
-
-class _TablesArgs(ctypes.Structure):
-    _fields_ = ([(n, _vp) for n in ("counts", "lens", "lens_out", "block_table", "ring", "state", "state_out", "slots", "positions",
-                                    "rows", "starts", "status")]
-                + [("table_stride", _i64)] + [(n, _i32) for n in ("B_u", "max_pages", "num_pages", "page_size", "capacity")])
-
-
-class _RopeArgs(ctypes.Structure):
-    _fields_ = ([(n, _vp) for n in ("q", "k", "q_out", "k_out", "positions", "freq")]
-                + [(n, _i64) for n in ("q_token", "q_head", "k_token", "k_head", "q_out_token", "q_out_head", "k_out_token", "k_out_head")]
-                + [(n, _i32) for n in ("T", "H_q", "H_k", "head_dim", "rot_dim", "layout", "dtype", "inverse")]
-                + [("factor", ctypes.c_float)])
-
-
-class _RowsArgs(ctypes.Structure):
-    _fields_ = ([(n, _vp) for n in ("k", "v", "slots", "tiles", "status")]
-                + [(n, _i64) for n in ("k_token", "k_head", "v_token", "v_head")]
-                + [(n, _i32) for n in ("T", "H_kv", "head_dim", "num_pages", "dtype")])
-
-
-class _AttentionArgs(ctypes.Structure):
-    _fields_ = ([(n, _vp) for n in ("Q", "O", "tiles", "block_table", "lens", "map", "positions", "status", "workspace")]
-                + [(n, _i64) for n in ("workspace_bytes", "q_cand", "q_head", "q_query", "o_cand", "o_head", "o_query", "table_stride")]
-                + [(n, _i32) for n in ("B_u", "B_c", "H_q", "H_kv", "L_q", "head_dim", "max_pages", "num_pages")]
-                + [("scale", ctypes.c_float)])
+# The small calls are bound by the host: these are the cheap forms of current_device() and of
+# current_stream(device).cuda_stream (0.1 us each against 0.2 and 2.8), with the public ones to fall back on.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _check(status: int, what: str) -> None:
@@ -68,43 +45,49 @@ def _check(status: int, what: str) -> None:
 
 
 @contextlib.contextmanager
-def _on_device_and_stream(device, stream):
+def _on(device, stream):
     with torch.cuda.device(device):
         if stream is None:
             yield torch.cuda.current_stream().cuda_stream
         else:
-            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+            if not isinstance(stream, torch.cuda.Stream):   # a handle; 0 is the default stream
+                stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+            s = stream
             with torch.cuda.stream(s):
                 yield s.cuda_stream
 
 
-def _run(device, stream, call):
-    """call(stream handle) with ``device`` current and allocations on the stream."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return call(torch.cuda.current_stream().cuda_stream)
-    with _on_device_and_stream(device, stream) as handle:
-        return call(handle)
+def _run(device, stream, call, *args):
+    """call(stream handle, *args) with ``device`` current and allocations on the stream."""
+    if stream is None and _current_device() == device.index:
+        return call(_current_stream(device.index), *args)
+    with _on(device, stream) as handle:
+        return call(handle, *args)
 
 
-def _ints(device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
+def _status_of(result, what: str):
+    """A result of the binding, or the library's status raised."""
+    if type(result) is int:
+        raise IkboError(result, what)
+    return result
 
 
-def _table(device, table) -> None:
-    if table.dtype != torch.int32 or table.device != device or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"the block table must be an int32 tensor [users, pages] with contiguous rows on {device}")
+_ext = None
 
 
-def _status(device, status) -> None:
-    if status.dtype != torch.int32 or status.device != device or status.numel() != 1:
-        raise ValueError(f"status must be an int32 tensor of one element on {device}")
-
-
-def _shapes(ok: bool, what: str) -> None:
-    if not ok:
-        raise IkboError(IKBO_ERR_INVALID_ARG, what)
+def _binding():
+    """The torch binding (``_ikbo_torch.so``) with the library's entry points; raises if either is not built."""
+    global _ext
+    if _ext is None:
+        L = lib()
+        try:
+            from . import _ikbo_torch as ext
+        except ImportError as e:
+            raise ImportError("_ikbo_torch.so is not built; run `python -m broadcast_gemm_amd.build`") from e
+        names = ("ikbo_kv_tables", "ikbo_rope", "ikbo_kv4_write", "ikbo_kv4_read", "ikbo_kv4_attention_workspace", "ikbo_kv4_attention")
+        ext.bind([ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names])
+        _ext = ext
+    return _ext
 
 
 def _device(t):
@@ -116,7 +99,8 @@ def _device(t):
 def kv_status(status, stream=None) -> int:
     """Wait for the stream, then return and clear the condition recorded in ``status`` (an IKBO_* code)."""
     device = _device(status)
-    _status(device, status)
+    if status.dtype != torch.int32 or status.numel() != 1:
+        raise ValueError("status must be an int32 tensor of one element")
     return _run(device, stream, lambda s: lib().ikbo_kv_status(status.data_ptr(), s))
 
 
@@ -135,30 +119,9 @@ def kv_tables(counts, lens, block_table, ring, state, capacity: int, status, pag
 
     ``block_table`` and ``ring`` are updated in place; ``lens`` and ``state`` too if ``in_place``, otherwise new
     tensors hold them after the step.  ``out`` may supply the result's tensors (then they are what is written)."""
-    device = _device(lens)
-    _ints(device, counts=counts, lens=lens, ring=ring, state=state)
-    _table(device, block_table)
-    _status(device, status)
-    B = lens.numel()
-    _shapes(counts.numel() == B and block_table.shape[0] == B and state.numel() == 4, "inconsistent shapes")
-
-    def call(s):
-        if out is None:
-            rows = torch.empty((3, capacity), dtype=torch.int32, device=device)
-            new = (lens, state) if in_place else (torch.empty_like(lens), torch.empty_like(state))
-            t = StepTables(rows[0], rows[1], rows[2], torch.empty(B + 1, dtype=torch.int32, device=device), *new)
-        else:
-            t = StepTables(*out)
-            _ints(device, slots=t.slots, positions=t.positions, rows=t.rows, starts=t.starts, lens_out=t.lens, state_out=t.state)
-            _shapes(all(x.numel() == capacity for x in t[:3]) and t.starts.numel() == B + 1 and t.lens.numel() == B
-                    and t.state.numel() == 4, "out has other shapes")
-        args = _TablesArgs(counts.data_ptr(), lens.data_ptr(), t.lens.data_ptr(), block_table.data_ptr(), ring.data_ptr(), state.data_ptr(),
-                           t.state.data_ptr(), t.slots.data_ptr(), t.positions.data_ptr(), t.rows.data_ptr(), t.starts.data_ptr(),
-                           status.data_ptr(), block_table.stride(0), B, block_table.shape[1], ring.numel(), page_size, capacity)
-        _check(lib().ikbo_kv_tables(ctypes.byref(args), s), "ikbo_kv_tables")
-        return t
-
-    return _run(device, stream, call)
+    res = _run(_device(lens), stream, _binding().kv_tables, counts, lens, block_table, ring, state, capacity, status, page_size, in_place,
+               None if out is None else list(out))
+    return StepTables._make(_status_of(res, "ikbo_kv_tables"))
 
 
 def rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: Optional[dict] = None, device="cuda") -> Tuple[torch.Tensor, float]:
@@ -208,12 +171,6 @@ def rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: Optional[dic
     return f.to(device), factor
 
 
-def _heads(name, t, device, dtype, T, dim) -> None:
-    if t.dtype != dtype or t.device != device or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be a {dtype} tensor [tokens, heads, head_dim] with contiguous heads on {device}")
-    _shapes(t.shape[0] == T and t.shape[2] == dim, f"{name}: inconsistent shape")
-
-
 def _spans(t) -> Tuple[int, int]:
     """First and last byte address that a tensor's elements take."""
     if t.numel() == 0:
@@ -240,56 +197,38 @@ def rope(q, k, positions, freq, layout: str = "half", factor: float = 1.0, inver
     x = q if q is not None else k
     if x is None:
         raise ValueError("rope needs q or k")
-    device, dtype = _device(x), x.dtype
-    if dtype not in _DTYPES:
-        raise ValueError("q and k must be bfloat16 or float32")
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
-    T, dim = x.shape[0], x.shape[-1]
-    _ints(device, positions=positions)
-    if freq.dtype != torch.float64 or freq.device != device or not freq.is_contiguous():
-        raise ValueError(f"freq must be a contiguous float64 tensor on {device}")
-    _shapes(positions.shape == (T,) and freq.dim() == 1, "inconsistent shapes")
-    given = [t for t in (q, k) if t is not None]
-    for t in given:
-        _heads("q and k", t, device, dtype, T, dim)
+    q_out = k_out = None
+    if out is not None:
+        q_out, k_out = out
+        _rope_out(q, k, q_out, k_out)
+    return _status_of(_run(_device(x), stream, _binding().rope, q, k, positions, freq, ROPE_LAYOUTS[layout], factor, inverse, q_out, k_out),
+                      "ikbo_rope")
 
-    def call(s):
-        if out is None:
-            res = [None if t is None else torch.empty(t.shape, dtype=dtype, device=device) for t in (q, k)]
-        else:
-            res = list(out)
-            _shapes(len(res) == 2, "out must be (q, k)")
-            for t, o in zip((q, k), res):
-                if (t is None) != (o is None):
-                    raise ValueError("out must hold the outputs of the tensors that are given")
-                if t is None:
-                    continue
-                _heads("out", o, device, dtype, T, dim)
-                _shapes(o.shape == t.shape, "out: inconsistent shape")
-                _distinct("out", o)
-            outs = [o for o in res if o is not None]
-            for o in outs:
-                a = _spans(o)
-                for t in given:
-                    if o.data_ptr() == t.data_ptr() and o.stride() == t.stride() and o.shape == t.shape:
-                        continue
-                    b = _spans(t)
-                    if a[0] <= b[1] and b[0] <= a[1] and not _interleaved(o, t):
-                        raise ValueError("an output overlaps an input that it is not")
-            if len(outs) == 2:
-                a, b = _spans(outs[0]), _spans(outs[1])
-                if a[0] <= b[1] and b[0] <= a[1] and not _interleaved(*outs):
-                    raise ValueError("the outputs overlap")
-        qs, ks, qo, ko = (t.stride() if t is not None else (0, 0, 1) for t in (q, k, res[0], res[1]))
-        ptr = [0 if t is None else t.data_ptr() for t in (q, k, res[0], res[1])]
-        args = _RopeArgs(*ptr, positions.data_ptr(), freq.data_ptr(), qs[0], qs[1], ks[0], ks[1], qo[0], qo[1], ko[0], ko[1],
-                         T, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], dim, 2 * freq.numel(),
-                         ROPE_LAYOUTS[layout], _DTYPES[dtype], int(bool(inverse)), float(factor))
-        _check(lib().ikbo_rope(ctypes.byref(args), s), "ikbo_rope")
-        return res[0], res[1]
 
-    return _run(device, stream, call)
+def _rope_out(q, k, q_out, k_out) -> None:
+    pairs = []
+    for t, o in ((q, q_out), (k, k_out)):
+        if (t is None) != (o is None):
+            raise ValueError("out must hold the outputs of the tensors that are given")
+        if t is not None:
+            if t.dim() != 3 or o.dim() != 3:
+                raise ValueError("q, k and out must be tensors [tokens, heads, head_dim]")
+            _distinct("out", o)
+            pairs.append((t, o))
+    for _, o in pairs:
+        for t, _ in pairs:
+            if _meet(o, t) and not (o.data_ptr() == t.data_ptr() and o.stride() == t.stride() and o.shape == t.shape):
+                raise ValueError("an output overlaps an input that it is not")
+    if len(pairs) == 2 and _meet(pairs[0][1], pairs[1][1]):
+        raise ValueError("the outputs overlap")
+
+
+def _meet(a, b) -> bool:
+    """Whether elements of two tensors [T, H, dim] may share memory (different heads of one tensor do not)."""
+    x, y = _spans(a), _spans(b)
+    return x[0] <= y[1] and y[0] <= x[1] and not _interleaved(a, b)
 
 
 def _interleaved(a, b) -> bool:
@@ -305,61 +244,25 @@ def _interleaved(a, b) -> bool:
     return gap % size == 0 and within[0] <= gap // size and gap // size + within[1] <= st
 
 
-def _tiles(device, tiles):
-    if tiles.dtype != torch.uint8 or tiles.device != device or tiles.dim() != 3 or not tiles.is_contiguous():
-        raise ValueError(f"tiles must be a contiguous uint8 tensor [pages, heads, 68 * head_dim] on {device}")
-    _shapes(tiles.shape[2] % 68 == 0, "tiles: the last dimension must be 68 * head_dim")
-    return tiles.shape[0], tiles.shape[1], tiles.shape[2] // 68
-
-
 def kv4_write(k, v, slots, tiles, status, stream=None) -> None:
     """Put the rows k, v [T, H_kv, head_dim] (bf16 or float32) into the cache at their slots (``ikbo_kv4_write``)."""
-    device = _device(k)
-    pages, H, dim = _tiles(device, tiles)
-    if k.dtype not in _DTYPES:
-        raise ValueError("k and v must be bfloat16 or float32")
-    T = slots.numel()
-    _ints(device, slots=slots)
-    _status(device, status)
-    for name, t in (("k", k), ("v", v)):
-        _heads(name, t, device, k.dtype, T, dim)
-        _shapes(t.shape[1] == H, f"{name}: heads differ from the cache's")
-    args = _RowsArgs(k.data_ptr(), v.data_ptr(), slots.data_ptr(), tiles.data_ptr(), status.data_ptr(), k.stride(0), k.stride(1),
-                     v.stride(0), v.stride(1), T, H, dim, pages, _DTYPES[k.dtype])
-    _run(device, stream, lambda s: _check(lib().ikbo_kv4_write(ctypes.byref(args), s), "ikbo_kv4_write"))
+    _check(_run(_device(k), stream, _binding().kv4_write, k, v, slots, tiles, status), "ikbo_kv4_write")
 
 
 def kv4_read(slots, tiles, status, dtype=torch.bfloat16, out=None, stream=None):
     """The values of the cached rows at the slots: (k, v) [T, H_kv, head_dim] (``ikbo_kv4_read``).
 
     Rows of a slot of -1 are left as they were (unspecified without ``out``)."""
-    device = _device(tiles)
-    pages, H, dim = _tiles(device, tiles)
-    _ints(device, slots=slots)
-    _status(device, status)
-    T = slots.numel()
-
-    def call(s):
-        if out is None:
-            if dtype not in _DTYPES:
-                raise ValueError("dtype must be bfloat16 or float32")
-            res = tuple(torch.empty((T, H, dim), dtype=dtype, device=device) for _ in range(2))
-        else:
-            res = tuple(out)
-            _shapes(len(res) == 2, "out must be (k, v)")
-            if res[0].dtype not in _DTYPES:
-                raise ValueError("out must be bfloat16 or float32")
-            for t in res:
-                _heads("out", t, device, res[0].dtype, T, dim)
-                _shapes(t.shape[1] == H, "out: heads differ from the cache's")
-                _distinct("out", t)
-        k, v = res
-        args = _RowsArgs(k.data_ptr(), v.data_ptr(), slots.data_ptr(), tiles.data_ptr(), status.data_ptr(), k.stride(0), k.stride(1),
-                         v.stride(0), v.stride(1), T, H, dim, pages, _DTYPES[k.dtype])
-        _check(lib().ikbo_kv4_read(ctypes.byref(args), s), "ikbo_kv4_read")
-        return res
-
-    return _run(device, stream, call)
+    k = v = None
+    if out is not None:
+        k, v = out
+        for t in (k, v):
+            if t.dim() != 3:
+                raise ValueError("out must be tensors [tokens, heads, head_dim]")
+            _distinct("out", t)
+        if _meet(k, v):
+            raise ValueError("the outputs overlap")
+    return _status_of(_run(_device(tiles), stream, _binding().kv4_read, slots, tiles, status, dtype, k, v), "ikbo_kv4_read")
 
 
 def kv4_attention(Q, tiles, block_table, lens, mp, status, positions=None, scale: float = 0.0, out=None, stream=None):
@@ -369,46 +272,10 @@ def kv4_attention(Q, tiles, block_table, lens, mp, status, positions=None, scale
     ``mp`` [B_c] int32, or None where candidate b belongs to user b; -1 entries are padding.  ``positions`` [B_c, L_q]
     (or [B_c]) int32 limits each query to tokens up to its position.  O has Q's shape; the rows of padding are left as
     they were (unspecified without ``out``)."""
-    device = _device(Q)
-    pages, H, dim = _tiles(device, tiles)
-    if Q.dtype != torch.bfloat16 or Q.dim() not in (3, 4) or (Q.shape[-1] > 1 and Q.stride(-1) != 1):
-        raise ValueError("Q must be a bfloat16 tensor [B_c, H_q, L_q, head_dim] or [B_c, H_q, head_dim] with contiguous heads")
-    _table(device, block_table)
-    _ints(device, lens=lens)
-    _status(device, status)
-    B_c, H_q, L_q = Q.shape[0], Q.shape[1], Q.shape[2] if Q.dim() == 4 else 1
-    B_u = lens.numel()
-    _shapes(Q.shape[-1] == dim and block_table.shape[0] == B_u, "inconsistent shapes")
-    if mp is not None:
-        _ints(device, map=mp)
-        _shapes(mp.shape == (B_c,), "map: inconsistent shape")
-    if positions is not None:
-        _ints(device, positions=positions)
-        _shapes(positions.numel() == B_c * L_q, "positions: inconsistent shape")
-    need = lib().ikbo_kv4_attention_workspace(B_u, B_c, H_q, H, L_q, dim, block_table.shape[1])
-    if need < 0:
-        raise IkboError(int(need), "ikbo_kv4_attention")
-
-    def strides(t):
-        return (t.stride(0), t.stride(1), t.stride(2)) if t.dim() == 4 else (t.stride(0), t.stride(1), 0)
-
-    def call(s):
-        if out is None:
-            o = torch.empty(Q.shape, dtype=Q.dtype, device=device)
-        else:
-            o = out
-            if o.dtype != Q.dtype or o.device != device or o.shape != Q.shape or (dim > 1 and o.stride(-1) != 1):
-                raise ValueError("out must be a bfloat16 tensor shaped like Q with contiguous heads")
-            _distinct("out", o)
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        args = _AttentionArgs(Q.data_ptr(), o.data_ptr(), tiles.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
-                              0 if mp is None else mp.data_ptr(), 0 if positions is None else positions.data_ptr(), status.data_ptr(),
-                              ws.data_ptr(), need, *strides(Q), *strides(o), block_table.stride(0), B_u, B_c, H_q, H, L_q, dim,
-                              block_table.shape[1], pages, float(scale))
-        _check(lib().ikbo_kv4_attention(ctypes.byref(args), s), "ikbo_kv4_attention")
-        return o
-
-    return _run(device, stream, call)
+    if out is not None:
+        _distinct("out", out)
+    return _status_of(_run(_device(Q), stream, _binding().kv4_attention, Q, tiles, block_table, lens, mp, status, positions, scale, out),
+                      "ikbo_kv4_attention")
 
 
 class UserHistories:

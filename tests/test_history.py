@@ -11,6 +11,37 @@ import broadcast_gemm_amd as bga
 from broadcast_gemm_amd import history
 from history_ref import LEVELS, decode, encode, tables, turn
 
+
+# The structures of the C ABI.
+_vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+
+
+class _TablesArgs(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("counts", "lens", "lens_out", "block_table", "ring", "state", "state_out", "slots", "positions",
+                                    "rows", "starts", "status")]
+                + [("table_stride", _i64)] + [(n, _i32) for n in ("B_u", "max_pages", "num_pages", "page_size", "capacity")])
+
+
+class _RopeArgs(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("q", "k", "q_out", "k_out", "positions", "freq")]
+                + [(n, _i64) for n in ("q_token", "q_head", "k_token", "k_head", "q_out_token", "q_out_head", "k_out_token", "k_out_head")]
+                + [(n, _i32) for n in ("T", "H_q", "H_k", "head_dim", "rot_dim", "layout", "dtype", "inverse")]
+                + [("factor", ctypes.c_float)])
+
+
+class _RowsArgs(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("k", "v", "slots", "tiles", "status")]
+                + [(n, _i64) for n in ("k_token", "k_head", "v_token", "v_head")]
+                + [(n, _i32) for n in ("T", "H_kv", "head_dim", "num_pages", "dtype")])
+
+
+class _AttentionArgs(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("Q", "O", "tiles", "block_table", "lens", "map", "positions", "status", "workspace")]
+                + [(n, _i64) for n in ("workspace_bytes", "q_cand", "q_head", "q_query", "o_cand", "o_head", "o_query", "table_stride")]
+                + [(n, _i32) for n in ("B_u", "B_c", "H_q", "H_kv", "L_q", "head_dim", "max_pages", "num_pages")]
+                + [("scale", ctypes.c_float)])
+
+
 P = 1 << 20   # a stand-in address: every check below returns before any HIP call
 INVALID, UNSUPPORTED, ALIGNMENT = bga.IKBO_ERR_INVALID_ARG, bga.IKBO_ERR_UNSUPPORTED, bga.IKBO_ERR_ALIGNMENT
 
@@ -45,7 +76,7 @@ TABLES = dict(table_stride=9, B_u=3, max_pages=9, num_pages=40, page_size=64, ca
     (dict(status=0), INVALID), (dict(slots=0), INVALID), (dict(lens=P + 2), ALIGNMENT), (dict(rows=P + 1), ALIGNMENT),
     (dict(num_pages=1 << 25), UNSUPPORTED), (dict(max_pages=1 << 25, table_stride=1 << 25), UNSUPPORTED)])
 def test_tables_refusals(L, change, want):
-    assert call(L.ikbo_kv_tables, fill(history._TablesArgs, **{**TABLES, **change})) == want
+    assert call(L.ikbo_kv_tables, fill(_TablesArgs, **{**TABLES, **change})) == want
     assert L.ikbo_kv_tables(None, None) == INVALID
 
 
@@ -60,7 +91,7 @@ ROPE = dict(q_token=512, q_head=128, k_token=256, k_head=128, q_out_token=512, q
     (dict(q=0), INVALID), (dict(k_out=0), INVALID), (dict(positions=0), INVALID), (dict(freq=P + 4), ALIGNMENT),
     (dict(q=P + 1), ALIGNMENT), (dict(dtype=1, k=P + 2), ALIGNMENT), (dict(q_out=P, q_out_token=640), INVALID), (dict(H_q=5000), UNSUPPORTED)])
 def test_rope_refusals(L, change, want):
-    assert call(L.ikbo_rope, fill(history._RopeArgs, **{**ROPE, **change})) == want
+    assert call(L.ikbo_rope, fill(_RopeArgs, **{**ROPE, **change})) == want
     assert L.ikbo_rope(None, None) == INVALID
 
 
@@ -74,14 +105,14 @@ ROWS = dict(k_token=256, k_head=128, v_token=256, v_head=128, T=5, H_kv=2, head_
     (dict(k_token=260), ALIGNMENT), (dict(v_head=132), ALIGNMENT)])
 def test_rows_refusals(L, change, want):
     args = {**ROWS, **change}
-    assert call(L.ikbo_kv4_write, fill(history._RowsArgs, **args)) == want
-    assert call(L.ikbo_kv4_read, fill(history._RowsArgs, **args)) == want
+    assert call(L.ikbo_kv4_write, fill(_RowsArgs, **args)) == want
+    assert call(L.ikbo_kv4_read, fill(_RowsArgs, **args)) == want
     assert L.ikbo_kv4_write(None, None) == INVALID and L.ikbo_kv4_read(None, None) == INVALID
 
 
 def test_write_needs_both_tensors(L):
-    assert call(L.ikbo_kv4_write, fill(history._RowsArgs, **ROWS, v=0)) == INVALID
-    assert call(L.ikbo_kv4_read, fill(history._RowsArgs, **ROWS, k=0, v=0)) == bga.IKBO_OK
+    assert call(L.ikbo_kv4_write, fill(_RowsArgs, **ROWS, v=0)) == INVALID
+    assert call(L.ikbo_kv4_read, fill(_RowsArgs, **ROWS, k=0, v=0)) == bga.IKBO_OK
 
 
 ATTEND = dict(workspace_bytes=1 << 40, q_cand=512, q_head=128, q_query=128, o_cand=512, o_head=128, o_query=128, table_stride=9, B_u=3,
@@ -97,7 +128,7 @@ ATTEND = dict(workspace_bytes=1 << 40, q_cand=512, q_head=128, q_query=128, o_ca
     (dict(q_head=132), ALIGNMENT), (dict(o_query=4), ALIGNMENT), (dict(map=P + 2), ALIGNMENT), (dict(positions=P + 1), ALIGNMENT),
     (dict(B_c=1 << 28, L_q=64), UNSUPPORTED)])
 def test_attention_refusals(L, change, want):
-    assert call(L.ikbo_kv4_attention, fill(history._AttentionArgs, **{**ATTEND, **change})) == want
+    assert call(L.ikbo_kv4_attention, fill(_AttentionArgs, **{**ATTEND, **change})) == want
     assert L.ikbo_kv4_attention(None, None) == INVALID
 
 
