@@ -218,8 +218,8 @@ struct Queries {
     // Step s of a row's elements: lane group g holds the 8 from `base` + s * `step`.
     template <class P>
     __device__ __forceinline__ void load(const AttnArgs &a, const P &plan, const User &x, int h, int first, int j, int base, int step) {
-        most = 0;
-        least = x.len;
+        most = least = x.len;
+        if (a.positions) most = 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = first + 16 * n + j;
@@ -235,21 +235,26 @@ struct Queries {
                 const int pos = a.positions[(int64_t)cnd * a.L_q + l];
                 limit[n] = pos < 0 ? 0 : pos < x.len ? pos + 1 : x.len;
             }
-            most = max(most, limit[n]);
-            if (live) least = min(least, limit[n]);
             m[n] = -__builtin_inff();
             nm[n] = 0.f;
             lsum[n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[d][n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
         }
+        if (a.positions) {
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1) {
-            most = max(most, __shfl_xor(most, d));
-            least = min(least, __shfl_xor(least, d));
+            for (int n = 0; n < NT; ++n) {
+                most = max(most, limit[n]);
+                if (first + 16 * n + j < x.n_rows) least = min(least, limit[n]);
+            }
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) {
+                most = max(most, __shfl_xor(most, d));
+                least = min(least, __shfl_xor(least, d));
+            }
+            most = __builtin_amdgcn_readfirstlane(most);
+            least = __builtin_amdgcn_readfirstlane(least);
         }
-        most = __builtin_amdgcn_readfirstlane(most);
-        least = __builtin_amdgcn_readfirstlane(least);
     }
 
     // Scores of page p: what a row does not see becomes -inf, and the running maximum moves if it must.
@@ -361,14 +366,17 @@ struct Pages {
     int64_t stride;                   // bytes from page to page
     int base, last, num_pages, ids;
     bool bad;
-    __device__ __forceinline__ void open(const AttnArgs &a, const Piece &c, int p0, int p1, int tile_bytes) {
+    __device__ __forceinline__ void open(const AttnArgs &a, const Piece &c, int tile_bytes) {
         row = a.table + (int64_t)c.x.u * a.table_stride;
         tiles = a.tiles + (int64_t)c.h * tile_bytes;
         stride = (int64_t)a.H_kv * tile_bytes;
         num_pages = a.num_pages;
-        last = p1 - 1;
+        // Entries behind the history may hold anything; an empty one has none.
+        last = min(c.p1, pages_of(c.x.len)) - 1;
         bad = false;
-        read(p0);
+        base = 0;
+        ids = 0;
+        if (c.p0 <= last) read(c.p0);
     }
     __device__ __forceinline__ void read(int p) {
         base = p;
@@ -429,13 +437,12 @@ __global__ void __launch_bounds__(64) kv4_attn_kernel(AttnArgs a) {
         const Piece c = piece_at(a, plan, at, end, blk);
         if (c.n) note = make_int2(c.n, min(a.R, c.x.n_rows - c.tile * a.R));
         at += c.p1 - c.p0;
+        Pages pages;   // the table's entry is on its way while the queries are found
+        pages.open(a, c, TILE);
         Queries<HD, NT> q;
         // The d order of K and Q: lane group g takes the g-th quarter of a head, one piece of a K row.
         q.load(a, plan, c.x, c.h, c.tile * 16 * NT, j, g * (HD / 4), 8);
         const int p1 = min(c.p1, (q.most + kPage - 1) / kPage);   // no row sees further pages
-        Pages pages;
-        pages.bad = false;
-        if (c.p0 < p1) pages.open(a, c, c.p0, p1, TILE);
         PageRegs<HD> pg;
         for (int p = c.p0; p < p1; ++p) {
             const char *tile = pages.at(p);
@@ -570,6 +577,8 @@ __global__ void __launch_bounds__(256, 2) kv4_wide_kernel(AttnArgs a) {
         const Piece c = piece_at(a, plan, at, end, blk);
         if (c.n) note = make_int2(c.n, min(a.R, c.x.n_rows - c.tile * a.R));
         at += c.p1 - c.p0;
+        Pages pages;
+        pages.open(a, c, TILE);
         Queries<HD, NT> q;
         q.load(a, plan, c.x, c.h, c.tile * kWideRows + wv * 16 * NT, j, 8 * g, 32);
         if (lane == 0) s_most[wv] = q.most;
@@ -579,8 +588,6 @@ __global__ void __launch_bounds__(256, 2) kv4_wide_kernel(AttnArgs a) {
         for (int w = 0; w < WAVES; ++w) most = max(most, s_most[w]);
         const int p0 = c.p0, p1 = min(c.p1, (most + kPage - 1) / kPage);   // no row sees further pages
         if (p0 < p1) {
-            Pages pages;
-            pages.open(a, c, p0, p1, TILE);
             u32x2_t kc[JOBS], vc[JOBS], vs[JOBS];
             uint32_t ks[JOBS];
             auto fetch = [&](int p) {
@@ -603,7 +610,7 @@ __global__ void __launch_bounds__(256, 2) kv4_wide_kernel(AttnArgs a) {
                     *reinterpret_cast<u32x4_t *>(to + L::k_at(key, 2 * part)) = values8(kc[y][0], s);
                     *reinterpret_cast<u32x4_t *>(to + L::k_at(key, 2 * part + 1)) = values8(kc[y][1], s);
                 }
-                const int left = c.x.len - min(p, p1 - 1) * kPage;   // tokens of the page that exist
+                const int left = c.x.len - min(p, pages.last) * kPage;   // tokens of the page that exist
                 if (left < kPage) {
 #pragma unroll
                     for (int y = 0; y < JOBS; ++y)

@@ -1,7 +1,7 @@
 // hist_cache.hip -- writing rows of keys and values into the 4-bit cache, and reading them back
 // (ikbo_kv4_write, ikbo_kv4_read).  The tile of a (page, head) is described in ikbo.h.
 //
-// Write: a block takes 64 token rows of one head.  8 elements of a row (one thread, 16 or 32 bytes)
+// Write: a block takes 64 token rows of one head (16 where 64 would leave most of the chip idle).  8 elements of a row (one thread, 16 or 32 bytes)
 // become 4 bytes of codes; 4 neighbouring threads hold the 32 elements of one scale and share their
 // largest magnitude by two lane exchanges.  The scale is a power of two, so x / 2^e and the hardware's
 // conversion to the nearest code (ties to even) are exact: the stored bytes are a function of the inputs
@@ -17,8 +17,6 @@ namespace ikbo {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 64;   // token rows per block
-
 __device__ __forceinline__ int scale_place(int t) { return (t & 48) + 4 * (t & 3) + ((t >> 2) & 3); }
 
 template <bool F32>
@@ -70,7 +68,7 @@ __device__ __forceinline__ uint32_t encode8(float (&x)[8], uint32_t *scale, bool
     return w;
 }
 
-template <int HD, bool F32>
+template <int HD, bool F32, int kRows>
 __global__ void __launch_bounds__(kThreads) kv4_write_kernel(ikbo_kv4_rows_args a) {
     constexpr int CH = HD / 8;           // threads per row
     constexpr int PAIRS = HD / 2;
@@ -122,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(ikbo_kv4_rows_args 
     }
     __syncthreads();
     // The V codes of one element pair, this thread's share of the rows.
-    constexpr int PART = kRows * PAIRS / kThreads;   // rows per thread: 16 (HD 128) or 8
+    constexpr int PART = kRows * PAIRS / kThreads;   // rows per thread: at most 16
     const int pair = tid % PAIRS, first = tid / PAIRS * PART;
     for (int r = first; r < first + PART;) {
         const int slot = s_slot[r];
@@ -202,15 +200,22 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(ikbo_kv4_rows_args a
     }
 }
 
+template <int HD, bool F32>
+hipError_t launch_write(const ikbo_kv4_rows_args &a, hipStream_t s) {
+    // 64 rows make the wide stores of V; below two blocks for each of 256 CUs the time of one block counts,
+    // and 16 rows take a third of it (59 tokens, 4 heads: 12 against 4 us).
+    const int64_t wide = (int64_t)((a.T + 63) / 64) * a.H_kv;
+    if (wide >= 512) hipLaunchKernelGGL((kv4_write_kernel<HD, F32, 64>), dim3((unsigned)((a.T + 63) / 64), (unsigned)a.H_kv), dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((kv4_write_kernel<HD, F32, 16>), dim3((unsigned)((a.T + 15) / 16), (unsigned)a.H_kv), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_kv4_write(const ikbo_kv4_rows_args &a, hipStream_t s) {
-    const dim3 grid((unsigned)((a.T + kRows - 1) / kRows), (unsigned)a.H_kv);
-    auto go = [&](auto k) { hipLaunchKernelGGL(k, grid, dim3(kThreads), 0, s, a); };
     const bool f = a.dtype == IKBO_DTYPE_F32;
-    if (a.head_dim == 128) f ? go(kv4_write_kernel<128, true>) : go(kv4_write_kernel<128, false>);
-    else f ? go(kv4_write_kernel<64, true>) : go(kv4_write_kernel<64, false>);
-    return hipGetLastError();
+    if (a.head_dim == 128) return f ? launch_write<128, true>(a, s) : launch_write<128, false>(a, s);
+    return f ? launch_write<64, true>(a, s) : launch_write<64, false>(a, s);
 }
 
 hipError_t launch_kv4_read(const ikbo_kv4_rows_args &a, hipStream_t s) {
