@@ -327,6 +327,17 @@ struct Piece {
     int64_t slot;                     // of the partial result, unless whole
     int n;                            // pieces of the unit, if it begins here and is cut
 };
+// Where the run of block `blk` begins (that of block `blk` - 1 ends).
+template <class P>
+__device__ __forceinline__ int64_t edge_of(const AttnArgs &a, const P &plan, int64_t blk) {
+    const int64_t all = plan.work[a.B_u], x = blk * plan.share, near = plan.share >> 3;
+    if (x <= 0) return 0;
+    if (x >= all) return all;
+    const int u = owner_of(plan.work, a.B_u, x);
+    const int64_t pages = plan.pages_of_user(u), in = (x - plan.work[u]) % pages;
+    if (in <= near && in <= pages - in) return x - in;
+    return pages - in <= near ? x + pages - in : x;
+}
 template <class P>
 __device__ __forceinline__ Piece piece_at(const AttnArgs &a, P &plan, int64_t at, int64_t end, int64_t blk) {
     Piece c;
@@ -340,7 +351,9 @@ __device__ __forceinline__ Piece piece_at(const AttnArgs &a, P &plan, int64_t at
     c.tile = (int)unit - c.h * c.x.tiles;
     c.whole = c.p0 == 0 && c.p1 == c.x.pages;
     c.slot = 2 * blk + (c.p0 == 0);
-    c.n = c.p0 == 0 && !c.whole ? (int)((at + c.x.pages - 1) / plan.share - blk) + 1 : 0;
+    // The pieces end at the runs' ends that lie further than `near` from both edges of the unit.
+    const int64_t near = plan.share >> 3;
+    c.n = c.p0 == 0 && !c.whole ? (int)((at + c.x.pages - near - 1) / plan.share - (at + near) / plan.share) + 1 : 0;
     return c;
 }
 
@@ -433,10 +446,10 @@ __global__ void __launch_bounds__(64, 2) kv4_attn_kernel(AttnArgs a) {
     constexpr int VJ = HD / 32, TILE = 68 * HD;
     __shared__ PlanLds<SMALL> small;
     const int lane = (int)threadIdx.x, g = lane >> 4, j = lane & 15;
-    Plan<SMALL, 64> plan(a, reinterpret_cast<SmallPlan *>(&small));
-    const int64_t blk = run_of_block((int)gridDim.x), all = plan.work[a.B_u], end = min(all, (blk + 1) * plan.share);
+    Plan<SMALL, 64> plan(a, small);
+    const int64_t blk = run_of_block((int)gridDim.x), end = edge_of(a, plan, blk + 1);
     int2 note = make_int2(0, 0);
-    for (int64_t at = blk * plan.share; at < end;) {
+    for (int64_t at = edge_of(a, plan, blk); at < end;) {
         const Piece c = piece_at(a, plan, at, end, blk);
         if (c.n) note = make_int2(c.n, min(a.R, c.x.n_rows - c.tile * a.R));
         at += c.p1 - c.p0;
@@ -557,7 +570,7 @@ __device__ __forceinline__ void lds_barrier() {
     wg_barrier();
 }
 
-template <int HD, bool SMALL>
+template <int HD>
 __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
     typedef WideLds<HD> L;
     constexpr int NT = 2, WAVES = 8, ROWS = 32 * WAVES, THREADS = 64 * WAVES, TK = HD / 32, DT = HD / 16, TILE = 68 * HD;
@@ -567,11 +580,11 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
     constexpr bool BOTH = PIECES >= THREADS;
     static_assert(BOTH || 2 * PIECES == THREADS, "every thread takes K, V or both");
     extern __shared__ __align__(16) char lds[];
-    __shared__ PlanLds<SMALL> small;
+    __shared__ PlanLds<false> in_workspace;
     __shared__ int s_most[WAVES];
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, j = lane & 15;
-    Plan<SMALL, THREADS> plan(a, reinterpret_cast<SmallPlan *>(&small));
-    const int64_t blk = run_of_block((int)gridDim.x), line = plan.work[a.B_u], end = min(line, (blk + 1) * plan.share);
+    Plan<false, THREADS> plan(a, in_workspace);
+    const int64_t blk = run_of_block((int)gridDim.x), end = edge_of(a, plan, blk + 1);
     int2 note = make_int2(0, 0);
     // This thread's operand reads (K tile t: + 4 t rows; V tile x: + 16 x rows), and where its pieces come from and
     // go to: K piece i is 16 elements of token i / (HD/16), V piece i 8 tokens of element pair i / 8.
@@ -593,7 +606,7 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
             v_to[y][x] = L::v_at(2 * pair + x, i & 7);
         }
     }
-    for (int64_t at = blk * plan.share; at < end;) {
+    for (int64_t at = edge_of(a, plan, blk); at < end;) {
         const Piece c = piece_at(a, plan, at, end, blk);
         if (c.n) note = make_int2(c.n, min(a.R, c.x.n_rows - c.tile * a.R));
         at += c.p1 - c.p0;
@@ -741,59 +754,55 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
 
 // ---- joining partial results ---------------------------------------------------------------
 
-// O = sum_s w_s O_s / sum_s w_s l_s with w_s = 2^(m_s - max m) over the n pieces of a unit: slot
-// 2 b + 1 of the block b that it begins in, and slots 2 (b + s) of those after it.  A block takes 16 rows
-// of the unit that its note names; its 8 waves share the rows out, and where there are fewer rows than
-// waves, several waves share the pieces of a row (lane i: HD/64 neighbouring elements).
+// O = sum_s w_s O_s / sum_s w_s l_s with w_s = 2^(m_s - max m) over the n pieces of a unit (slots: hist_plan.h).
+// A block takes 16 rows of the unit that its note names, one for each of its 16 half waves (a lane holds
+// HD/32 neighbouring elements); where there are fewer rows, several half waves share a row's pieces.
 template <int HD>
 __global__ void __launch_bounds__(512) kv4_join_kernel(AttnArgs a) {
-    constexpr int E = HD / 64;
-    __shared__ float s_acc[8][HD];
-    const int lane = (int)threadIdx.x & 63, wv = (int)threadIdx.x >> 6, r_first = 16 * (int)blockIdx.y;
+    constexpr int E = HD / 32;
+    typedef float vec_t __attribute__((ext_vector_type(E)));
+    __shared__ vec_t s_acc[16][32];
+    const int lane = (int)threadIdx.x & 63, i = lane & 31, half = (int)threadIdx.x >> 5, r_first = 16 * (int)blockIdx.y;
     const int64_t b = blockIdx.x;
     const int2 note = a.note[b];
     const int n = note.x, rows = min(16, note.y - r_first);
     if (n == 0 || rows <= 0) return;
-    const int abreast = rows >= 5 ? 8 : rows >= 3 ? 4 : rows, share = 8 / abreast;   // rows at a time, waves per row
-    auto at = [&](int s, int r) { return (2 * (b + s) + (s == 0)) * a.R + r; };
-    for (int r0 = 0; r0 < rows; r0 += abreast) {
-        const int k = r0 + wv / share, r = r_first + k, part = wv % share;
-        const bool live = k < rows;
-        float acc[E] = {}, l = 0.f;
-        if (live) {
-            float top = -__builtin_inff();
-            for (int s = lane; s < n; s += 64) top = fmaxf(top, a.ml[at(s, r)].x);
-            for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-            for (int s0 = 0; s0 < n; s0 += 64) {
-                const float2 ml = s0 + lane < n ? a.ml[at(s0 + lane, r)] : make_float2(-__builtin_inff(), 0.f);
-                const float w = weight_of(ml.x, top);
-                l += w * ml.y;
-                const int nb = min(64, n - s0);
-#pragma unroll 8
-                for (int s = part; s < nb; s += share) {
-                    const float ws = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), s));
-                    const float *p = a.part + at(s0 + s, r) * HD + lane * E;
+    int abreast = 1;
+    while (abreast < rows) abreast <<= 1;
+    const int share = 16 / abreast, k = half / share, r = r_first + k, part = half - k * share;   // half waves per row
+    const bool live = k < rows;
+    const int64_t o_at = live ? a.note_o[b * a.R + r] : 0;
+    auto at = [&](int s) { return (2 * (b + s) + (s == 0)) * a.R + r; };
+    float top = -__builtin_inff(), l = 0.f;
+    if (live)
+        for (int s = i; s < n; s += 32) top = fmaxf(top, a.ml[at(s)].x);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += ws * p[e];
-                }
-            }
-            for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    vec_t acc = {};
+    for (int s0 = 0; s0 < n; s0 += 32) {
+        const float2 ml = live && s0 + i < n ? a.ml[at(s0 + i)] : make_float2(-__builtin_inff(), 0.f);
+        const float w = weight_of(ml.x, top);
+        l += w * ml.y;
+        const int nb = min(32, n - s0);
+        for (int s1 = 0; s1 < nb; s1 += share) {
+            const int s = s1 + part;
+            const float ws = __shfl(w, (lane & 32) + (s & 31));
+            if (live && s < nb) acc += ws * *reinterpret_cast<const vec_t *>(a.part + at(s0 + s) * HD + i * E);
         }
-        if (share > 1) {
+    }
 #pragma unroll
-            for (int e = 0; e < E; ++e) s_acc[wv][lane * E + e] = acc[e];
-            __syncthreads();
-            if (live && part == 0)
-                for (int w = 1; w < share; ++w)
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += s_acc[wv + w][lane * E + e];
-        }
-        if (live && part == 0) {
-            const float inv = inverse_of(l);
-            uint16_t *to = a.O + a.note_o[b * a.R + r] + lane * E;
-            if constexpr (E == 2) *reinterpret_cast<uint32_t *>(to) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-            else *to = (uint16_t)pack_bf16x2(acc[0] * inv, 0.f);
-        }
+    for (int d = 16; d; d >>= 1) l += __shfl_xor(l, d);
+    if (share > 1) {
+        s_acc[half][i] = acc;
+        __syncthreads();
+        if (part == 0)
+            for (int w = 1; w < share; ++w) acc += s_acc[half + w][i];
+    }
+    if (live && part == 0) {
+        acc *= inverse_of(l);
+        uint16_t *to = a.O + o_at + i * E;
+        if constexpr (E == 4) *reinterpret_cast<u32x2_t *>(to) = (u32x2_t){pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
+        else *reinterpret_cast<uint32_t *>(to) = pack_bf16x2(acc[0], acc[1]);
     }
 }
 
@@ -802,10 +811,11 @@ inline int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 // Waves that group the candidates: their counts, one per wave and user, stay within 128 KB of LDS.
 inline int prep_waves(int B_u) { return std::max(1, std::min(kPrep / 64, 32768 / B_u)); }
 
-template <int HD, bool SMALL>
+template <int HD>
 hipError_t launch(const AttnArgs &a, int64_t line_most, hipStream_t s) {
     hipError_t e = hipSuccess;
-    if constexpr (!SMALL) {
+    const bool wide = a.R == 256, small = !wide && a.B_u <= kSmallUsers && a.B_c <= kSmallCands;
+    if (!small) {
         const int waves = a.map ? prep_waves(a.B_u) : 0;
         const size_t lds = ((size_t)waves * a.B_u + a.B_u + 1) * sizeof(int);
         e = hipFuncSetAttribute(reinterpret_cast<const void *>(kv4_prep_kernel), hipFuncAttributeMaxDynamicSharedMemorySize, 152 * 1024);
@@ -815,13 +825,15 @@ hipError_t launch(const AttnArgs &a, int64_t line_most, hipStream_t s) {
     }
     // No more blocks than pages; a block past the line's end returns at once.
     const dim3 grid((unsigned)std::min<int64_t>(line_most, 1ll << a.log_blocks));
-    if (a.R == 16) hipLaunchKernelGGL((kv4_attn_kernel<HD, 1, SMALL>), grid, dim3(64), 0, s, a);
-    else if (a.R == 32) hipLaunchKernelGGL((kv4_attn_kernel<HD, 2, SMALL>), grid, dim3(64), 0, s, a);
-    else {
-        const auto k = kv4_wide_kernel<HD, SMALL>;
+    if (wide) {
+        const auto k = kv4_wide_kernel<HD>;
         e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, 2 * WideLds<HD>::PAGE);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(k, grid, dim3(512), 2 * WideLds<HD>::PAGE, s, a);
+    } else {
+        const auto k = a.R == 16 ? (small ? kv4_attn_kernel<HD, 1, true> : kv4_attn_kernel<HD, 1, false>)
+                                 : (small ? kv4_attn_kernel<HD, 2, true> : kv4_attn_kernel<HD, 2, false>);
+        hipLaunchKernelGGL(k, grid, dim3(64), 0, s, a);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (a.max_pages > 1)   // a history of one page is never cut
@@ -879,9 +891,7 @@ hipError_t launch_kv4_attention(const ikbo_kv4_attention_args &x, const Kv4AttnL
     a.max_pages = x.max_pages; a.num_pages = x.num_pages;
     a.R = w.R; a.log_blocks = w.log_blocks;
     a.scale_log2 = scale * 1.4426950408889634f;
-    if (x.B_u <= kSmallUsers && x.B_c <= kSmallCands)
-        return x.head_dim == 128 ? launch<128, true>(a, w.line_most, s) : launch<64, true>(a, w.line_most, s);
-    return x.head_dim == 128 ? launch<128, false>(a, w.line_most, s) : launch<64, false>(a, w.line_most, s);
+    return x.head_dim == 128 ? launch<128>(a, w.line_most, s) : launch<64>(a, w.line_most, s);
 }
 
 }  // namespace ikbo

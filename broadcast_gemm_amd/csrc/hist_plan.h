@@ -6,6 +6,10 @@
 // even whatever the lengths are, and a unit is cut only where a run ends.  Neighbouring units share
 // their K and V.
 //
+// A run's end that falls within an eighth of a run of a unit's edge moves to that edge: runs then differ by a
+// quarter at most, and many short units (1080 units of 15 pages in 256 runs) are hardly cut at all, which costs
+// less than writing and joining their pieces.
+//
 // A block leaves at most two partial results: one of the unit that its run begins inside (slot 2 b),
 // one of a unit that begins in its run and goes on after it (slot 2 b + 1).  So the pieces of a unit
 // whose pages are [from, to) of the line are slot 2 b0 + 1 of the block b0 = from / share and the
@@ -15,8 +19,9 @@
 // many there are, and where the rows of O stand.
 //
 // The line is described by the prefix sums over the users of their pages of work.  For up to 256 users
-// and 1024 candidates every block forms them in LDS, which costs less than waiting for a launch of
-// one block that does it (about 2 us against 10); beyond that the launch does.
+// and 1024 candidates every block of the narrow kernel forms them in LDS (2 us); beyond that, and for the
+// wide kernel, whose blocks come back to other users' candidates too often to list them again each time,
+// a launch of one block does (6 us and more).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -89,12 +94,12 @@ __device__ __forceinline__ int owner_of(const T *base, int n, T x) {
 
 struct SmallPlan {
     int64_t work[kSmallUsers + 1];
-    int cnt[kSmallUsers];
+    int cnt[kSmallUsers], pages[kSmallUsers];
     uint16_t map[kSmallCands];        // 0xFFFF: no user
     uint16_t list[kSmallCands];       // the candidates of user `listed`, ascending
     int listed, bad;
 };
-template <bool SMALL>
+template <bool SMALL>                 // otherwise the plan stands in the workspace
 using PlanLds = typename std::conditional<SMALL, SmallPlan, int>::type;
 
 struct User {
@@ -109,7 +114,7 @@ struct Plan {
     const int64_t *work;
     int64_t share;
 
-    __device__ __forceinline__ Plan(const AttnArgs &a_, SmallPlan *sm_) : a(a_), sm(sm_) {
+    __device__ __forceinline__ Plan(const AttnArgs &a_, PlanLds<SMALL> &lds) : a(a_), sm(reinterpret_cast<SmallPlan *>(&lds)) {
         if constexpr (!SMALL) {
             work = a.work;
             share = a.share[0];
@@ -148,7 +153,9 @@ struct Plan {
             const int u = lane * per + e;
             const int rows = e < per && u < B ? sm->cnt[u] * a.L_q * a.G : 0;
             wrong = wrong || len[e] < 0 || len[e] > a.max_pages * kPage;
-            w[e] = (int64_t)tiles_of(rows) * a.H_kv * max(1, pages_of(clamp_len(len[e], a.max_pages)));
+            const int pages = max(1, pages_of(clamp_len(len[e], a.max_pages)));
+            if (tid < 64 && e < per && u < B) sm->pages[u] = pages;
+            w[e] = (int64_t)tiles_of(rows) * a.H_kv * pages;
             sum_w += w[e];
         }
         int64_t at_w = wave_before(sum_w, &all_w);
@@ -167,6 +174,11 @@ struct Plan {
         const bool any = __ballot(wrong) != 0;
         __syncthreads();
         if (blockIdx.x == 0 && tid == 0 && (any || sm->bad)) atomicOr(a.status, (any ? kStPage : 0u) | (uint32_t)sm->bad);
+    }
+
+    __device__ __forceinline__ int pages_of_user(int u) const {
+        if constexpr (SMALL) return sm->pages[u];
+        else return max(1, pages_of(clamp_len(a.lens[u], a.max_pages)));
     }
 
     // The whole block comes here with the same u: its candidates become known (SMALL).
