@@ -1,14 +1,17 @@
 // hist_cache.hip -- writing rows of keys and values into the 4-bit cache, and reading them back
 // (ikbo_kv4_write, ikbo_kv4_read).  The tile of a (page, head) is described in ikbo.h.
 //
-// Write: a block takes 64 token rows of one head (16 where 64 would leave most of the chip idle).  8 elements of a row (one thread, 16 or 32 bytes)
-// become 4 bytes of codes; 4 neighbouring threads hold the 32 elements of one scale and share their
-// largest magnitude by two lane exchanges.  The scale is a power of two, so x / 2^e and the hardware's
-// conversion to the nearest code (ties to even) are exact: the stored bytes are a function of the inputs
-// alone.  K codes are rows of the tile and are stored as they come.  V codes stand token by token
-// behind each element pair, so they go through LDS, and each thread stores the tokens of one element
-// pair: 16 or 4 bytes at once where neighbouring rows have neighbouring slots in a tile, single bytes
-// otherwise.
+// Write: a block takes 64 token rows of one head (16 where 64 would leave most of the chip idle).
+// 8 elements of a row (one thread, 16 or 32 bytes) become 4 bytes of codes; 4 neighbouring threads hold the
+// 32 elements of one scale and share their largest magnitude by two lane exchanges.  The scale is a power
+// of two, so the hardware's conversion (x / 2^e to the nearest code, ties to even, never beyond 6) is
+// exact: the stored bytes are a function of the inputs alone.  K codes are rows of the tile and are
+// stored as they come.  V codes stand token by token behind each element pair, so they go through LDS, and
+// each thread stores the tokens of one element pair: 16 or 4 bytes at once where neighbouring rows have
+// neighbouring slots in a page, single bytes otherwise.
+//
+// Read: for K a thread takes 8 elements of a row, for V an element pair of 4 rows: one access where their
+// slots are neighbours, and the lanes of a wave, neighbouring pairs, write whole rows.
 #include "hist_internal.h"
 
 #include "lce_device.h"
@@ -19,53 +22,93 @@ namespace {
 constexpr int kThreads = 256;
 __device__ __forceinline__ int scale_place(int t) { return (t & 48) + 4 * (t & 3) + ((t >> 2) & 3); }
 
-template <bool F32>
-__device__ __forceinline__ void load8(const void *base, int64_t at, float (&x)[8]) {
-    if constexpr (F32) {
+// 8 elements of a row as they stand in memory.
+template <bool F32> struct Eight;
+template <> struct Eight<false> {
+    u32x4_t w;
+    __device__ __forceinline__ void load(const void *base, int64_t at) {
+        w = *reinterpret_cast<const u32x4_t *>(static_cast<const uint16_t *>(base) + at);
+    }
+    __device__ __forceinline__ void clear() { w = (u32x4_t){0, 0, 0, 0}; }
+    // The largest magnitude, as the bits of a float32.
+    __device__ __forceinline__ uint32_t top() const {
+        typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+        u16x2_t m = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, w[e] & 0x7FFF7FFFu));
+        return (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
+    }
+    // What the cache cannot hold: NaN becomes 0 and infinity the largest finite value.
+    __device__ __forceinline__ void mend() {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint32_t y = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t v = (w[e] >> (16 * k)) & 0xFFFFu, m = v & 0x7FFFu;
+                y |= (m > 0x7F80u ? 0u : m == 0x7F80u ? v - 1u : v) << (16 * k);
+            }
+            w[e] = y;
+        }
+    }
+    __device__ __forceinline__ uint32_t codes(float scale) const {
+        uint32_t c = 0;
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, (uint32_t)w[0]), scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, (uint32_t)w[1]), scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, (uint32_t)w[2]), scale, 2);
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, (uint32_t)w[3]), scale, 3);
+    }
+};
+template <> struct Eight<true> {
+    uint32_t w[8];
+    __device__ __forceinline__ void load(const void *base, int64_t at) {
         const u32x4_t *p = reinterpret_cast<const u32x4_t *>(static_cast<const float *>(base) + at);
         const u32x4_t a = p[0], b = p[1];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[e] = __builtin_bit_cast(float, (uint32_t)a[e]);
-            x[4 + e] = __builtin_bit_cast(float, (uint32_t)b[e]);
-        }
-    } else {
-        const u32x4_t a = *reinterpret_cast<const u32x4_t *>(static_cast<const uint16_t *>(base) + at);
+        for (int e = 0; e < 4; ++e) { w[e] = a[e]; w[4 + e] = b[e]; }
+    }
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[2 * e] = __builtin_bit_cast(float, a[e] << 16);
-            x[2 * e + 1] = __builtin_bit_cast(float, a[e] & 0xFFFF0000u);
+        for (int e = 0; e < 8; ++e) w[e] = 0;
+    }
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, w[e] & 0x7FFFFFFFu);
+        return m;
+    }
+    __device__ __forceinline__ void mend() {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t m = w[e] & 0x7FFFFFFFu;
+            w[e] = m > 0x7F800000u ? 0u : m == 0x7F800000u ? w[e] - 1u : w[e];
         }
     }
-}
+    __device__ __forceinline__ uint32_t codes(float scale) const {
+        auto x = [&](int e) { return __builtin_bit_cast(float, w[e]); };
+        uint32_t c = 0;
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x(0), x(1), scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x(2), x(3), scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x(4), x(5), scale, 2);
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x(6), x(7), scale, 3);
+    }
+};
 
 // 8 elements of one row as 4 bytes of codes; *scale is the byte of their 32 elements (the threads
 // 4q .. 4q+3 hold them).
-__device__ __forceinline__ uint32_t encode8(float (&x)[8], uint32_t *scale, bool *odd) {
-    constexpr float kMost = 3.3895313892515355e38f;   // beyond the largest value the cache holds
-    float top = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        if (x[e] != x[e]) { x[e] = 0.f; *odd = true; }
-        if (__builtin_fabsf(x[e]) > kMost) {
-            *odd = *odd || __builtin_isinf(x[e]);
-            x[e] = __builtin_copysignf(kMost, x[e]);
-        }
-        top = fmaxf(top, __builtin_fabsf(x[e]));
+template <bool F32>
+__device__ __forceinline__ uint32_t encode8(Eight<F32> &x, uint32_t *scale, bool *odd) {
+    if (x.top() >= 0x7F800000u) {
+        *odd = true;
+        x.mend();
     }
-    top = fmaxf(top, __shfl_xor(top, 1));
-    top = fmaxf(top, __shfl_xor(top, 2));
-    const uint32_t bits = __builtin_bit_cast(uint32_t, top);
-    int e2 = (int)(bits >> 23) - 127 - 2 + ((bits & 0x7FFFFFu) > 0x400000u);   // top <= 6 * 2^e2
+    uint32_t top = x.top();
+    top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, true));   // lane ^ 1
+    top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, true));   // lane ^ 2
+    int e2 = (int)(top >> 23) - 127 - 2 + ((top & 0x7FFFFFu) > 0x400000u);   // top <= 6 * 2^e2
     e2 = e2 < -125 ? -125 : e2 > 125 ? 125 : e2;
     *scale = (uint32_t)(e2 + 127);
-    const float inv = __builtin_bit_cast(float, (uint32_t)(127 - e2) << 23);
-    uint32_t w = 0;
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0] * inv, x[1] * inv, 1.0f, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2] * inv, x[3] * inv, 1.0f, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4] * inv, x[5] * inv, 1.0f, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6] * inv, x[7] * inv, 1.0f, 3);
-    return w;
+    return x.codes(__builtin_bit_cast(float, *scale << 23));
 }
 
 template <int HD, bool F32, int kRows>
@@ -77,35 +120,50 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(ikbo_kv4_rows_args 
     __shared__ int s_slot[kRows];
     __shared__ uint32_t s_v[PAIRS * VROW / 4];
     __shared__ uint32_t s_flag;
+    __shared__ uint64_t s_next;
     const int tid = (int)threadIdx.x, h = (int)blockIdx.y;
     const int64_t r0 = (int64_t)blockIdx.x * kRows;
     const int nr = (int)min((int64_t)kRows, a.T - r0);
+    // All of the thread's rows are on their way before their slots are known.
+    constexpr int ITEMS = kRows * CH, TURNS = (ITEMS + kThreads - 1) / kThreads;
+    Eight<F32> kx[TURNS], vx[TURNS];
+#pragma unroll
+    for (int y = 0; y < TURNS; ++y) {
+        const int x = tid + y * kThreads, r = x / CH, c = x % CH;
+        kx[y].clear();
+        vx[y].clear();
+        if (x < ITEMS && r < nr) {
+            kx[y].load(a.k, (r0 + r) * a.k_token + h * a.k_head + 8 * c);
+            vx[y].load(a.v, (r0 + r) * a.v_token + h * a.v_head + 8 * c);
+        }
+    }
     if (tid == 0) s_flag = 0;
     __syncthreads();
-    if (tid < kRows) {
+    if (tid < 64) {
         int slot = tid < nr ? a.slots[r0 + tid] : -1;
         if (slot < -1 || slot >= a.num_pages * IKBO_KV4_PAGE) {
             if (h == 0) atomicOr(&s_flag, kStPage);
             slot = -1;
         }
-        s_slot[tid] = slot;
+        if (tid < kRows) s_slot[tid] = slot;
+        // Bit r: row r stands right behind row r - 1 in the same page.
+        const int before = __shfl_up(slot, 1);
+        const uint64_t next = __ballot(tid > 0 && before >= 0 && slot == before + 1 && slot % IKBO_KV4_PAGE != 0);
+        if (tid == 0) s_next = next;
     }
     __syncthreads();
     char *tiles = static_cast<char *>(a.tiles);
     uint8_t *vb = reinterpret_cast<uint8_t *>(s_v);
-    for (int x = tid; x < kRows * CH; x += kThreads) {
-        const int r = x / CH, c = x % CH;
+#pragma unroll
+    for (int y = 0; y < TURNS; ++y) {
+        const int x = tid + y * kThreads, r = x / CH, c = x % CH;
+        if (x >= ITEMS) break;
         const int slot = s_slot[r];
         const bool live = slot >= 0;
-        float kx[8] = {}, vx[8] = {};
-        if (live) {
-            load8<F32>(a.k, (r0 + r) * a.k_token + h * a.k_head + 8 * c, kx);
-            load8<F32>(a.v, (r0 + r) * a.v_token + h * a.v_head + 8 * c, vx);
-        }
         uint32_t ks, vs;
         bool odd = false;
-        const uint32_t kw = encode8(kx, &ks, &odd), vw = encode8(vx, &vs, &odd);
-        if (odd) atomicOr(&s_flag, kStNonfinite);
+        const uint32_t kw = encode8(kx[y], &ks, &odd), vw = encode8(vx[y], &vs, &odd);
+        if (odd && live) atomicOr(&s_flag, kStNonfinite);
         if (live) {
             char *tile = tiles + ((int64_t)(slot / IKBO_KV4_PAGE) * a.H_kv + h) * TILE;
             const int t = slot % IKBO_KV4_PAGE;
@@ -119,35 +177,36 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(ikbo_kv4_rows_args 
         }
     }
     __syncthreads();
-    // The V codes of one element pair, this thread's share of the rows.
-    constexpr int PART = kRows * PAIRS / kThreads;   // rows per thread: at most 16
+    // The V codes of one element pair, this thread's share of the rows (at most 16): the stores may have any
+    // alignment, and a run within a page stays within the pair's 64 bytes.
+    constexpr int PART = kRows * PAIRS / kThreads;
     const int pair = tid % PAIRS, first = tid / PAIRS * PART;
-    for (int r = first; r < first + PART;) {
-        const int slot = s_slot[r];
-        if (slot < 0) { ++r; continue; }
-        const int t = slot % IKBO_KV4_PAGE;
-        char *to = tiles + ((int64_t)(slot / IKBO_KV4_PAGE) * a.H_kv + h) * TILE + PAIRS * 64 + pair * 64 + t;
-        int run = 1;
-        while (run < 16 && r + run < first + PART && s_slot[r + run] == slot + run && (t + run) % 16 != 0) ++run;
-        const uint8_t *from = vb + pair * VROW + r;
-        if (run == 16) {   // then t % 16 == 0
-            u32x4_t w;
+    const uint64_t next = s_next;
+    auto together = [&](int r, int n) { return ((next >> r) & ((1ull << n) - 2)) == (1ull << n) - 2; };   // rows r .. r + n - 1
+    auto place = [&](int slot) {
+        return tiles + ((int64_t)(slot / IKBO_KV4_PAGE) * a.H_kv + h) * TILE + PAIRS * 64 + pair * 64 + slot % IKBO_KV4_PAGE;
+    };
+    const uint8_t *from = vb + pair * VROW + first;
+    if (PART == 16 && together(first, 16)) {
+        u32x4_t w;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = reinterpret_cast<const uint32_t *>(from)[e];
-            *reinterpret_cast<u32x4_t *>(to) = w;
-        } else {
-            for (int e = 0; e < run;) {
-                if ((t + e) % 4 == 0 && e + 4 <= run) {
-                    const uint32_t w = from[e] | (from[e + 1] << 8) | (from[e + 2] << 16) | ((uint32_t)from[e + 3] << 24);
-                    *reinterpret_cast<uint32_t *>(to + e) = w;
-                    e += 4;
-                } else {
-                    to[e] = (char)from[e];
-                    ++e;
+        for (int e = 0; e < 4; ++e) w[e] = reinterpret_cast<const uint32_t *>(from)[e];
+        __builtin_memcpy(place(s_slot[first]), &w, 16);
+    } else {
+        constexpr int STEP = PART < 4 ? PART : 4;
+#pragma unroll
+        for (int r = 0; r < PART; r += STEP) {
+            if (STEP == 4 && together(first + r, 4)) {
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(from + r);
+                __builtin_memcpy(place(s_slot[first + r]), &w, 4);
+            } else {
+#pragma unroll
+                for (int e = 0; e < STEP; ++e) {
+                    const int slot = s_slot[first + r + e];
+                    if (slot >= 0) *place(slot) = (char)from[r + e];
                 }
             }
         }
-        r += run;
     }
     if (tid == 0 && s_flag) atomicOr(a.status, s_flag);
 }
@@ -163,41 +222,71 @@ __device__ __forceinline__ void store8(void *base, int64_t at, const uint32_t (&
     }
 }
 
-// Read: a thread takes 8 elements of one row of K and of V.
+template <bool F32>
+__device__ __forceinline__ void store2(void *base, int64_t at, uint32_t w) {
+    if constexpr (F32) *reinterpret_cast<u32x2_t *>(static_cast<float *>(base) + at) = (u32x2_t){w << 16, w & 0xFFFF0000u};
+    else *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(base) + at) = w;
+}
+
 template <int HD, bool F32>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(ikbo_kv4_rows_args a) {
     constexpr int CH = HD / 8, PAIRS = HD / 2, TILE = 68 * HD;
     const int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t r = x / CH;
-    const int c = (int)(x % CH), h = (int)blockIdx.y;
-    if (r >= a.T) return;
-    const int slot = a.slots[r];
-    if (slot < 0 || slot >= a.num_pages * IKBO_KV4_PAGE) {
-        if (slot != -1 && c == 0 && h == 0) atomicOr(a.status, kStPage);
-        return;
-    }
-    const char *tile = static_cast<const char *>(a.tiles) + ((int64_t)(slot / IKBO_KV4_PAGE) * a.H_kv + h) * TILE;
-    const int t = slot % IKBO_KV4_PAGE;
-    auto values = [&](uint32_t codes, uint32_t scale, uint32_t (&w)[4]) {
-        const float s = __builtin_bit_cast(float, scale << 23);
-        w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 0));
-        w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 1));
-        w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 2));
-        w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 3));
+    const int h = (int)blockIdx.y, n_slots = a.num_pages * IKBO_KV4_PAGE;
+    auto tile_of = [&](int slot) {
+        return static_cast<const char *>(a.tiles) + ((int64_t)(slot / IKBO_KV4_PAGE) * a.H_kv + h) * TILE;
     };
-    uint32_t w[4];
-    if (a.k) {
-        values(*reinterpret_cast<const uint32_t *>(tile + t * PAIRS + 4 * c),
-               (uint8_t)tile[64 * HD + (c / 4) * 64 + scale_place(t)], w);
-        store8<F32>(a.k, r * a.k_token + h * a.k_head + 8 * c, w);
+    const int64_t r = x / CH;
+    if (r < a.T) {
+        const int c = (int)(x % CH), slot = a.slots[r];
+        if (slot < 0 || slot >= n_slots) {
+            if (slot != -1 && c == 0 && h == 0) atomicOr(a.status, kStPage);
+        } else if (a.k) {
+            const char *tile = tile_of(slot);
+            const int t = slot % IKBO_KV4_PAGE;
+            const uint32_t codes = *reinterpret_cast<const uint32_t *>(tile + t * PAIRS + 4 * c);
+            const float s = __builtin_bit_cast(float, (uint32_t)(uint8_t)tile[64 * HD + (c / 4) * 64 + scale_place(t)] << 23);
+            uint32_t w[4];
+            w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 0));
+            w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 1));
+            w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 2));
+            w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 3));
+            store8<F32>(a.k, r * a.k_token + h * a.k_head + 8 * c, w);
+        }
     }
-    if (a.v) {
-        uint32_t codes = 0;
+    const int64_t r4 = x / PAIRS * 4;
+    if (!a.v || r4 >= a.T) return;
+    const int pair = (int)(x % PAIRS);
+    int slot[4];
+    bool near = true;   // four neighbouring slots of one page
 #pragma unroll
-        for (int e = 0; e < 4; ++e) codes |= (uint32_t)(uint8_t)tile[PAIRS * 64 + (4 * c + e) * 64 + t] << (8 * e);
-        values(codes, (uint8_t)tile[66 * HD + (c / 4) * 64 + t], w);
-        store8<F32>(a.v, r * a.v_token + h * a.v_head + 8 * c, w);
+    for (int e = 0; e < 4; ++e) {
+        slot[e] = r4 + e < a.T ? a.slots[r4 + e] : -1;
+        if (slot[e] >= n_slots) slot[e] = -1;
+        near = near && slot[0] >= 0 && slot[e] == slot[0] + e && slot[0] % IKBO_KV4_PAGE <= IKBO_KV4_PAGE - 4;
     }
+    const int64_t v_at = 32 * HD + pair * 64, s_at = 66 * HD + (pair / 16) * 64;
+    uint32_t codes = 0, scales = 0;
+    if (near) {
+        const char *tile = tile_of(slot[0]) + slot[0] % IKBO_KV4_PAGE;
+        __builtin_memcpy(&codes, tile + v_at, 4);     // any alignment
+        __builtin_memcpy(&scales, tile + s_at, 4);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (slot[e] >= 0) {
+                const char *tile = tile_of(slot[e]) + slot[e] % IKBO_KV4_PAGE;
+                codes |= (uint32_t)(uint8_t)tile[v_at] << (8 * e);
+                scales |= (uint32_t)(uint8_t)tile[s_at] << (8 * e);
+            }
+    }
+    auto put = [&](int e, auto w) {
+        if (slot[e] >= 0) store2<F32>(a.v, (r4 + e) * a.v_token + h * a.v_head + 2 * pair, __builtin_bit_cast(uint32_t, w));
+    };
+    put(0, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, __builtin_bit_cast(float, (scales & 0xFFu) << 23), 0));
+    put(1, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, __builtin_bit_cast(float, (scales >> 8 & 0xFFu) << 23), 1));
+    put(2, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, __builtin_bit_cast(float, (scales >> 16 & 0xFFu) << 23), 2));
+    put(3, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, __builtin_bit_cast(float, (scales >> 24) << 23), 3));
 }
 
 template <int HD, bool F32>
@@ -219,7 +308,7 @@ hipError_t launch_kv4_write(const ikbo_kv4_rows_args &a, hipStream_t s) {
 }
 
 hipError_t launch_kv4_read(const ikbo_kv4_rows_args &a, hipStream_t s) {
-    const int64_t threads = (int64_t)a.T * (a.head_dim / 8);
+    const int64_t threads = ((int64_t)a.T + 3) / 4 * (a.head_dim / 2);
     const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), (unsigned)a.H_kv);
     auto go = [&](auto k) { hipLaunchKernelGGL(k, grid, dim3(kThreads), 0, s, a); };
     const bool f = a.dtype == IKBO_DTYPE_F32;
