@@ -11,7 +11,7 @@
 //
 // In-place lengths and ring state may only change once every block has read them: a block counts
 // itself in state[2] when it is done, and the last one writes lens_out and state_out and sets the
-// count back to 0.  The ring's popped and pushed places are disjoint (their sum is at most the
+// count back to 0 (out of place the first block writes them at once).  The ring's popped and pushed places are disjoint (their sum is at most the
 // ring), and so are the table entries read (the page a request's next token falls into) and
 // written (the ones behind it): those are updated where they are.
 //
@@ -117,6 +117,23 @@ __global__ void __launch_bounds__(kMost) kv_tables_kernel(ikbo_kv_tables_args a)
     }
     __syncthreads();
 
+    auto commit = [&] {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int i = tid * per + e;
+            if (e < per && i < B) a.lens_out[i] = err ? len[e] : cnt[e] < 0 ? 0 : len[e] + cnt[e];
+        }
+        if (tid == 0) {
+            const long long h = (long long)head + all.take;
+            a.state[2] = 0;
+            a.state_out[0] = err ? head : (int)(h >= N ? h - N : h);
+            a.state_out[1] = (int)(err ? nfree : nfree - all.take + all.give);
+            if (a.state_out != a.state) a.state_out[2] = a.state_out[3] = 0;
+        }
+    };
+    const bool in_place = a.lens_out == a.lens || a.state_out == a.state;
+    if (!in_place && blockIdx.x == 0) commit();
+
     const long long step = (long long)gridDim.x * nt, first = (long long)blockIdx.x * nt + tid;
     auto at_ring = [&](long long i) { return i >= N ? i - N : i; };
     if (err) {   // the whole step is refused
@@ -152,34 +169,23 @@ __global__ void __launch_bounds__(kMost) kv_tables_kernel(ikbo_kv_tables_args a)
         if (bad) atomicOr(a.status, bad);
     }
 
-    // The last block to come here writes what the others have read.
+    // In place, the last block to come here writes what the others have read (their reads are complete: they
+    // went into what they have stored).
+    if (!in_place) return;
     __syncthreads();
-    if (tid == 0) {
-        __threadfence();
-        s_last = gridDim.x == 1 || atomicAdd(reinterpret_cast<unsigned *>(a.state + 2), 1u) == gridDim.x - 1;
-    }
+    if (tid == 0)
+        s_last = __hip_atomic_fetch_add(reinterpret_cast<unsigned *>(a.state + 2), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
     __syncthreads();
-    if (!s_last) return;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        const int i = tid * per + e;
-        if (e < per && i < B) a.lens_out[i] = err ? len[e] : cnt[e] < 0 ? 0 : len[e] + cnt[e];
-    }
-    if (tid == 0) {
-        a.state[2] = 0;
-        a.state_out[0] = (int)(err ? head : at_ring((long long)head + all.take));
-        a.state_out[1] = (int)(err ? nfree : nfree - all.take + all.give);
-        if (a.state_out != a.state) a.state_out[2] = a.state_out[3] = 0;
-    }
+    if (s_last) commit();
 }
 
 }  // namespace
 
 hipError_t launch_kv_tables(const ikbo_kv_tables_args &a, hipStream_t s) {
-    // Small blocks scan sooner; every block repeats the scan, so a thread takes a few rows.
+    // Small blocks scan sooner; every block repeats the scan, which costs what a row's chain of reads does.
     const int threads = a.B_u <= 1024 ? 256 : kMost;
     const long long items = std::max<long long>(a.capacity, a.B_u + 1);
-    const int blocks = (int)std::min<long long>(256, std::max<long long>(1, (items + 2 * threads - 1) / (2 * threads)));
+    const int blocks = (int)std::min<long long>(256, std::max<long long>(1, (items + threads - 1) / threads));
     const size_t lds = 4 * (size_t)(a.B_u + 1) * sizeof(int);   // at most 64 KB and 16 bytes
     if (lds > 60 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kv_tables_kernel), hipFuncAttributeMaxDynamicSharedMemorySize, 66 * 1024);
