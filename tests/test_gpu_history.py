@@ -537,6 +537,47 @@ def test_attend_positions(lens, B_c, Hq, Hkv, Lq, mapping, dim):
     attend_case(B_c * dim, lens, B_c, Hq, Hkv, Lq, dim, mapping=mapping, positions=True)
 
 
+@pytest.mark.parametrize("B_u, B_c, Hq, Hkv, Lq, dim, longest, mapping, positions", [
+    (300, 300, 4, 2, 1, 64, 200, "none", False),        # more users than a block's own plan holds
+    (2500, 2400, 2, 1, 1, 64, 130, "none", False),
+    (4096, 4096, 1, 1, 1, 64, 70, "random", True),
+    (257, 3000, 1, 1, 1, 128, 300, "random", False),
+    (2, 1025, 1, 1, 1, 64, 500, "random", True),         # many rows: the wide kernel, rows limited by position
+    (3, 1200, 2, 1, 1, 64, 900, "even", True),
+    (5, 900, 3, 3, 2, 128, 333, "random", False),
+    (1, 700, 1, 1, 1, 128, 4500, "even", True),          # long enough to be cut in many runs
+    (1, 64, 4, 1, 2, 128, 9000, "even", False),
+    (2, 2, 16, 1, 1, 64, 20000, "none", False),          # more than 64 pieces to join
+    (1, 1, 1, 1, 1, 128, 30000, "none", False),
+    (7, 50, 2, 1, 1, 128, 40, "random", False)])
+def test_attend_plans(B_u, B_c, Hq, Hkv, Lq, dim, longest, mapping, positions):
+    """Every way the work is planned, dealt and joined; a sample of the candidates against the definition."""
+    t = torch()
+    log(f"attend plan B_u={B_u} B_c={B_c} heads={Hq}/{Hkv} L_q={Lq} dim={dim} longest={longest} {mapping} {positions}")
+    rng = np.random.default_rng(B_u + B_c)
+    lens = rng.integers(0, longest + 1, B_u)
+    lens[rng.integers(0, B_u)] = longest
+    if B_u > 5:
+        lens[rng.random(B_u) < 0.1] = 0
+    width = -(-longest // 64)
+    tiles, d_table, table, k, v = history(rng, lens, width, Hkv, dim)
+    mp = {"even": np.arange(B_c) * B_u // B_c, "random": rng.integers(-1, B_u, B_c), "none": None}[mapping]
+    pos = rng.integers(-1, longest + 3, (B_c, Lq)).astype(np.int32) if positions else None
+    Q = dev(rng.standard_normal((B_c, Hq, Lq, dim)) * 1.5, t.bfloat16)
+    st = word()
+    out = t.full_like(Q, 5.0)
+    H().kv4_attention(Q, tiles, d_table, dev(lens.astype(np.int32)), None if mp is None else dev(mp.astype(np.int32)), st,
+                      positions=None if pos is None else dev(pos), out=out)
+    assert H().kv_status(st) == bga.IKBO_OK
+    pick = np.unique(np.concatenate([[0, B_c - 1], rng.integers(0, B_c, 40)]))
+    users = np.arange(B_c) if mp is None else mp
+    want, bound = ref.attend(f64(Q)[pick], k, v, table, lens, users[pick], None if pos is None else pos[pick])
+    got = f64(out)
+    live = users[pick] >= 0
+    bounded(got[pick][live], want[live], bound[live], t.bfloat16, "sampled candidates")
+    assert (got[users < 0] == 5).all() and np.isfinite(got).all()
+
+
 def test_attend_scale_and_wide_table():
     attend_case(1, [100, 700], 2, 4, 2, 1, 128, mapping="none", scale=0.31, width=50)
     attend_case(2, [100, 700], 2, 4, 2, 1, 64, mapping="none", scale=3.0)
