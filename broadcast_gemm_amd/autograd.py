@@ -103,24 +103,25 @@ class IkboLce(torch.nn.Module):
 
 
 class RopeFunction(torch.autograd.Function):
-    """(q, k) turned by their positions, both directions in the library."""
+    """(q, k) turned by their positions (``inverse``: turned back), both directions in the library.
+
+    The gradient is the same function the other way round, so it can be differentiated again."""
 
     @staticmethod
-    def forward(ctx, q, k, positions, freq, layout, factor):
-        q_out, k_out = history.rope(q, k, positions, freq, layout=layout, factor=factor)
+    def forward(ctx, q, k, positions, freq, layout, factor, inverse=False):
+        q_out, k_out = history.rope(q, k, positions, freq, layout=layout, factor=factor, inverse=inverse)
         ctx.save_for_backward(positions, freq)
-        ctx.how = (layout, factor)
+        ctx.how = (layout, factor, not inverse)
         return q_out, k_out
 
     @staticmethod
     def backward(ctx, dq, dk):
         positions, freq = ctx.saved_tensors
-        layout, factor = ctx.how
         dq, dk = (None if d is None or not need else d if d.stride(-1) == 1 else d.contiguous()
                   for d, need in zip((dq, dk), ctx.needs_input_grad))
         if dq is not None or dk is not None:
-            dq, dk = history.rope(dq, dk, positions, freq, layout=layout, factor=factor, inverse=True)
-        return dq, dk, None, None, None, None
+            dq, dk = RopeFunction.apply(dq, dk, positions, freq, *ctx.how)
+        return dq, dk, None, None, None, None, None
 
 
 class IkboRope(torch.nn.Module):

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kMost) kv_tables_kernel(ikbo_kv_tables_args a)
             if (a.state_out != a.state) a.state_out[2] = a.state_out[3] = 0;
         }
     };
-    const bool in_place = a.lens_out == a.lens || a.state_out == a.state;
+    const bool in_place = a.lens_out == a.lens || a.lens_out == a.counts || a.state_out == a.state;
     if (!in_place && blockIdx.x == 0) commit();
 
     const long long step = (long long)gridDim.x * nt, first = (long long)blockIdx.x * nt + tid;

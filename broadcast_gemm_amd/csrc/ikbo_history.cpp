@@ -45,7 +45,10 @@ int ikbo_kv_status(uint32_t *status, void *stream) {
     if ((e = hipMemcpy(&word, status, sizeof word, hipMemcpyDeviceToHost)) != hipSuccess)
         return hip_fail(e, "hipMemcpy(status)");
     if (word == 0) return IKBO_OK;
-    if ((e = hipMemset(status, 0, sizeof word)) != hipSuccess) return hip_fail(e, "hipMemset(status)");
+    // On the caller's stream, so that what it enqueues next comes behind.
+    if ((e = hipMemsetAsync(status, 0, sizeof word, static_cast<hipStream_t>(stream))) != hipSuccess ||
+        (e = hipStreamSynchronize(static_cast<hipStream_t>(stream))) != hipSuccess)
+        return hip_fail(e, "hipMemset(status)");
     if (word & kStMap) return IKBO_ERR_MAP_RANGE;
     if (word & kStPage) return IKBO_ERR_PAGE_RANGE;
     if (word & kStNoPages) return IKBO_ERR_NO_PAGES;

@@ -217,9 +217,10 @@ def _rope_out(q, k, q_out, k_out) -> None:
                 raise ValueError("q, k and out must be tensors [tokens, heads, head_dim]")
             _distinct("out", o)
             pairs.append((t, o))
-    for _, o in pairs:
+    for own, o in pairs:
         for t, _ in pairs:
-            if _meet(o, t) and not (o.data_ptr() == t.data_ptr() and o.stride() == t.stride() and o.shape == t.shape):
+            same = t is own and o.data_ptr() == t.data_ptr() and o.stride() == t.stride() and o.shape == t.shape
+            if not same and _meet(o, t):
                 raise ValueError("an output overlaps an input that it is not")
     if len(pairs) == 2 and _meet(pairs[0][1], pairs[1][1]):
         raise ValueError("the outputs overlap")
@@ -271,7 +272,7 @@ def kv4_attention(Q, tiles, block_table, lens, mp, status, positions=None, scale
     Q [B_c, H_q, L_q, head_dim] bf16 (or [B_c, H_q, head_dim]: one query each), any strides that are multiples of 8;
     ``mp`` [B_c] int32, or None where candidate b belongs to user b; -1 entries are padding.  ``positions`` [B_c, L_q]
     (or [B_c]) int32 limits each query to tokens up to its position.  O has Q's shape; the rows of padding are left as
-    they were (unspecified without ``out``)."""
+    they were (unspecified without ``out``).  ``out`` may be Q."""
     if out is not None:
         _distinct("out", out)
     return _status_of(_run(_device(Q), stream, _binding().kv4_attention, Q, tiles, block_table, lens, mp, status, positions, scale, out),
@@ -312,6 +313,16 @@ class UserHistories:
     def append(self, k, v, counts, stream=None) -> StepTables:
         """Take in one step: rows k, v [T, H_kv, head_dim] hold the users' new tokens one user after the other
         (``counts`` [users] int32 of them; rows behind the last are padding)."""
+        # Everything that could refuse the write is checked before the tables move on.
+        H, dim = self.tiles.shape[1], self.tiles.shape[2] // 68
+        for name, x in (("k", k), ("v", v)):
+            if x.device != self.tiles.device or x.dtype not in (torch.bfloat16, torch.float32) or x.dtype != k.dtype:
+                raise ValueError(f"{name} must be bfloat16 or float32 on {self.tiles.device}, k and v alike")
+            if x.dim() != 3 or x.shape != (k.shape[0], H, dim) or x.stride(2) != 1:
+                raise ValueError(f"{name} must be [T, {H}, {dim}] with contiguous heads, k and v alike")
+            whole = 8 if x.dtype == torch.bfloat16 else 4
+            if x.data_ptr() % 16 or x.stride(0) % whole or x.stride(1) % whole:
+                raise ValueError(f"{name}: rows must be 16-byte aligned")
         t = kv_tables(counts, self.lens, self.table, self.ring, self.state, k.shape[0], self.status, in_place=True, stream=stream)
         if self.freq is not None:
             k = rope(None, k, t.positions, self.freq, layout=self.layout, factor=self.factor, stream=stream)[1]

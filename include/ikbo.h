@@ -1,6 +1,7 @@
 /*
  * ikbo.h -- C ABI of libikbo: the IKBO Linear Compression Embedding forward (and its
- * backward) on AMD Instinct MI355X (gfx950).
+ * backward) on AMD Instinct MI355X (gfx950), target attention, and target attention over
+ * cached user histories.
  *
  * The operation (IKBO recsys blog, "Deep Dive: Linear Compression"; aibriefing
  * article, "kernel deep-dive case 1"):
@@ -289,8 +290,8 @@ int ikbo_kv_status(uint32_t *status, void *stream);
  *     slots = block_table[i][pos / page_size] * page_size + pos % page_size,
  *     positions = pos = lens[i] + t,  rows = i;
  * the rows from starts[B_u] to capacity are filled with -1.  lens_out[i] = lens[i] + counts[i]
- * (0 for a leaving request); lens_out may be lens and state_out may be state (updated in
- * place: one step after the other, also on replays of a captured graph).
+ * (0 for a leaving request); lens_out may be lens or counts, and state_out may be state (updated in
+ * place: one step after the other, also on replays of a captured graph).  No other buffers overlap.
  * A step that does not fit (free pages, table columns or capacity: IKBO_ERR_NO_PAGES; a
  * negative or overlong length, a count below -1, a ring state out of range:
  * IKBO_ERR_PAGE_RANGE) is refused as a whole: slots, positions and rows become -1, starts 0,
@@ -383,7 +384,8 @@ int ikbo_kv4_read(const ikbo_kv4_rows_args *args, void *stream);
  * are recorded as MAP_RANGE and left likewise.  Lengths outside [0, 64 * max_pages] are recorded
  * as PAGE_RANGE and clamped, as are page numbers outside [0, num_pages) (page 0 is read then).
  * Scores, softmax and sums are float32 (the weights reach the matrix cores as bf16); O is rounded
- * once.  scale = 0 means 1/sqrt(head_dim); negative, NaN and infinite scales are INVALID_ARG.
+ * once.  O may be Q (same strides) and does not overlap it otherwise.  The same call gives the same bits; a row's
+ * last bits may depend on the other rows and lengths of the call.  scale = 0 means 1/sqrt(head_dim); negative, NaN and infinite scales are INVALID_ARG.
  * head_dim 64 or 128, H_q a multiple of H_kv, 1 <= B_u <= IKBO_KV_MAX_USERS, L_q >= 1.
  * workspace: ikbo_kv4_attention_workspace bytes, 16-byte aligned, not shared with a call that may
  * overlap; nothing in it has to be kept between calls.

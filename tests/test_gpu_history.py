@@ -177,6 +177,29 @@ def test_tables_steps_replay_in_a_graph():
     assert h.kv_status(st) == bga.IKBO_OK
 
 
+def test_tables_without_rows_and_lengths_into_counts():
+    t = torch()
+    h = H()
+    lens, counts = dev(np.array([64, 10, 0], np.int32)), t.zeros(3, dtype=t.int32, device="cuda")
+    table, ring = dev(np.array([[0, -1], [1, -1], [-1, -1]], np.int32)), dev(np.array([2, 3, 4], np.int32))
+    state, st = t.tensor([1, 1, 0, 0], dtype=t.int32, device="cuda"), word()
+    got = h.kv_tables(counts, lens, table, ring, state, 0, st)
+    assert got.slots.numel() == 0 and got.starts.tolist() == [0] * 4 and got.lens.tolist() == [64, 10, 0] and got.state.tolist()[:2] == [1, 1]
+    # 40 000 rows in many blocks, the new lengths written over the counts that every block reads.
+    B = 4000
+    rng = np.random.default_rng(1)
+    step = make_step(rng, B, 3, 64, 3, 20)
+    cap = int(np.maximum(step[0], 0).sum())
+    d = [dev(x) for x in step[:4]]
+    state = t.tensor([step[4], step[5], 0, 0], dtype=t.int32, device="cuda")
+    rows = t.empty((3, cap), dtype=t.int32, device="cuda")
+    out = h.StepTables(rows[0], rows[1], rows[2], t.empty(B + 1, dtype=t.int32, device="cuda"), d[0], t.empty_like(state))
+    h.kv_tables(d[0], d[1], d[2], d[3], state, cap, st, out=out)
+    want = ref.tables(step[0], step[1], step[2].copy(), step[3].copy(), step[4], step[5], cap)
+    assert np.array_equal(rows.cpu().numpy(), np.stack(want[:3])) and np.array_equal(d[0].cpu().numpy(), want[4])
+    assert h.kv_status(st) == bga.IKBO_OK and state.tolist() == [step[4], step[5], 0, 0]
+
+
 # ---- rotary positions ----------------------------------------------------------------------
 
 
@@ -265,6 +288,8 @@ def test_rope_refusals():
         h.rope(y[:6], None, p, f, out=(y[1:], None))
     with pytest.raises(ValueError):
         h.rope(x, None, p, f, out=(x[:1].expand(6, 4, 64), None))
+    with pytest.raises(ValueError):
+        h.rope(x, y[:6], p, f, out=(y[:6], x))     # each other's input
     with pytest.raises(bga.IkboError):
         h.rope(x, None, p, t.ones(33, dtype=t.float64, device="cuda"))
     e = h.rope(x[:0], None, p[:0], f)[0]
@@ -302,6 +327,12 @@ def test_rope_gradient(layout):
     only_q = m(q, None, dev(pos))
     assert only_q[1] is None
     only_q[0].sum().backward()
+    # The gradient is linear in the upstream gradient: differentiated again, it turns forward.
+    up = dev(wq, t.float32).requires_grad_()
+    g, = t.autograd.grad(m(q, None, dev(pos))[0], q, up, create_graph=True)
+    gg, = t.autograd.grad(g, up, dev(wq, t.float32))
+    back, bound = ref.turn(f64(dev(wq, t.float32)), pos, f, layout, m.factor)
+    bounded(f64(gg), back, bound, t.float32, "gradient of the gradient")
 
 
 # ---- the cache: write and read -------------------------------------------------------------
@@ -681,6 +712,33 @@ def test_attend_strides_past_32_bits():
     assert t.equal(got, want)
 
 
+@pytest.mark.parametrize("B_u, B_c, Lq, n, dim", [(2, 12, 64, 1500, 64), (1, 1, 1, 9000, 128), (3, 40, 5, 300, 128)])
+def test_attend_over_its_queries_and_replayed(B_u, B_c, Lq, n, dim):
+    """O written over Q (also where units are cut), and the call captured and replayed with other queries between."""
+    t = torch()
+    rng = np.random.default_rng(16)
+    lens = np.full(B_u, n)
+    tiles, d_table, table, k, v = history(rng, lens, -(-n // 64), 2, dim)
+    mp = dev((np.arange(B_c) % B_u).astype(np.int32))
+    st, d_lens = word(), dev(lens.astype(np.int32))
+    Q = t.zeros(B_c, 4, Lq, dim, dtype=t.bfloat16, device="cuda")
+    graph = t.cuda.CUDAGraph()
+    t.cuda.synchronize()
+    with t.cuda.graph(graph):
+        O = H().kv4_attention(Q, tiles, d_table, d_lens, mp, st)
+    for rep in range(4):
+        q = dev(rng.standard_normal(tuple(Q.shape)), t.bfloat16)
+        want = H().kv4_attention(q, tiles, d_table, d_lens, mp, st)
+        Q.copy_(q)
+        t.cuda.synchronize()
+        graph.replay()
+        t.cuda.synchronize()
+        assert t.equal(O, want), rep
+        same = q.clone()
+        assert H().kv4_attention(same, tiles, d_table, d_lens, mp, st, out=same) is not None and t.equal(same, want)
+    assert H().kv_status(st) == bga.IKBO_OK
+
+
 def test_attend_refusals():
     t = torch()
     h = H()
@@ -763,6 +821,14 @@ def test_histories_grow_and_are_attended():
         assert (out[dev(~live)] == 5).all() and hist.check() == bga.IKBO_OK
     with pytest.raises(ValueError):
         hist.attend(Q, None)
+    # A step that the write would refuse leaves the tables where they are.
+    k = t.zeros(6, Hkv, dim, dtype=t.bfloat16, device="cuda")
+    ones = t.ones(users, dtype=t.int32, device="cuda")
+    before = (hist.lens.clone(), hist.state.clone(), hist.table.clone())
+    for bad in ((k, k.float()), (k, k[:5]), (k[:, :1], k[:, :1]), (k.half(), k.half()), (k, k.cpu()), (k[..., :32], k[..., :32])):
+        with pytest.raises(ValueError):
+            hist.append(*bad, ones)
+    assert all(t.equal(x, y) for x, y in zip(before, (hist.lens, hist.state, hist.table)))
 
 
 def test_captured_steps_and_two_graphs_and_streams():
