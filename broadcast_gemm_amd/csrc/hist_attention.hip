@@ -22,8 +22,8 @@
 // Two kernels.  In the narrow one a block is one wave with 16 or 32 rows, which converts the codes it
 // reads for itself, registers to registers: with few rows the cache's bytes are what counts, and 8 waves
 // on a CU keep 5 TB/s of them coming.  Every wave repeats the conversion, so with many rows per user and
-// head a block of 8 waves, 32 rows each, converts a page once into LDS (bf16, two pages deep) and each
-// wave reads its operands there.
+// head a block of 8 waves, 32 rows each, converts a page once into LDS (bf16) and each wave reads its
+// operands there.
 //
 // How the work is dealt to the blocks, and what joins their partial results: hist_plan.h.
 #include <algorithm>
@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kLogNarrow = 11;        // one wave each, 8 at a time on each of 256 CUs
 constexpr int kLogWide = 8;           // 8 waves each, one at a time on each CU
+constexpr int kBuffers = 4;           // pages in LDS (wide kernel)
 constexpr float kSlack = 8.0f;
 
 // One block.  Groups the candidates by user (perm, off: a stable counting sort, one run of
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(64, 2) kv4_attn_kernel(AttnArgs a) {
 
 // ---- the wide kernel -----------------------------------------------------------------------
 
-// Two page buffers in LDS: K rows [64 tokens][HD] and V^T rows [HD][64 tokens], bf16.  The 16-byte
+// Four page buffers in LDS: K rows [64 tokens][HD] and V^T rows [HD][64 tokens], bf16.  The 16-byte
 // chunks of a row stand permuted by an XOR with a number of the row.  A 16-byte read of a wave is served 16
 // lanes at a time, and not in their order: lanes 0-3, 12-15, 20-23 and 24-27, then 4-11, 16-19 and 28-31, and so
 // on (measured with pairs of patterns).  With lane 16 g + j that is every j once, some with g and the others with
@@ -657,7 +658,7 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
                 }
             };
             auto convert = [&](int p) {
-                char *to = lds + (p & 1) * L::PAGE;
+                char *to = lds + (p & (kBuffers - 1)) * L::PAGE;
 #pragma unroll
                 for (int y = 0; y < JOBS; ++y) {
                     if (has_k) {
@@ -682,7 +683,7 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
                 }
             };
             auto scores = [&](int p, f32x4_t (&S)[4][NT]) {
-                const char *from = lds + (p & 1) * L::PAGE;
+                const char *from = lds + (p & (kBuffers - 1)) * L::PAGE;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -697,7 +698,7 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
                     }
             };
             auto product = [&](int p, int kk, const u32x4_t (&pf)[2][NT]) {
-                const char *from = lds + (p & 1) * L::PAGE;
+                const char *from = lds + (p & (kBuffers - 1)) * L::PAGE;
 #pragma unroll
                 for (int x = 0; x < DT; ++x) {
                     const u32x4_t vf = *reinterpret_cast<const u32x4_t *>(from + v_off[kk] + x * 16 * kPage * 2);
@@ -717,20 +718,26 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
             tail(p0);
             convert(p0);
             fetch(p0 + 1);
+            tail(p0 + 1);
+            convert(p0 + 1);
+            fetch(p0 + 2);
             lds_barrier();
-            // Pages behind the last are taken again from the last one (into a buffer that nothing reads),
-            // which keeps the turns free of branches.  The next page's conversion stands behind the scores'
-            // matrix instructions, which it can overlap (in front of them: 6% slower); its buffer was last
-            // read before the barrier that ended the previous turn.
-            // Waves without a row that sees the page do the same work on masked scores: a branch around it cost
-            // the others a tenth of their time.
-            for (int p = p0; p < p1; ++p) {
-                tail(p + 1);
+            // Two pages a barrier: a page's buffer takes the one four pages on, two turns after the barrier behind
+            // its last reads.  Pages behind the last are taken again from the last one (into buffers that nothing
+            // reads), which keeps the turns free of branches.  The conversion stands behind the scores' matrix
+            // instructions, which it can overlap (in front of them: 6% slower).  Waves without a row that sees
+            // the page do the same work on masked scores: a branch around it cost the others a tenth.
+            auto turn = [&](int p) {
+                tail(p + 2);
                 scores(p, S);
-                convert(p + 1);
-                fetch(p + 2);
+                convert(p + 2);
+                fetch(p + 3);
                 q.raise(S, p, g, a.scale_log2);
                 accumulate(p, S);
+            };
+            for (int p = p0; p < p1; p += 2) {
+                turn(p);
+                if (p + 1 < p1) turn(p + 1);
                 lds_barrier();
             }
             if (pages.bad && tid == 0) atomicOr(a.status, kStPage);
@@ -836,9 +843,9 @@ hipError_t launch(const AttnArgs &a, int64_t line_most, hipStream_t s) {
     const dim3 grid((unsigned)std::min<int64_t>(line_most, 1ll << a.log_blocks));
     if (wide) {
         const auto k = kv4_wide_kernel<HD>;
-        e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, 2 * WideLds<HD>::PAGE);
+        e = hipFuncSetAttribute(reinterpret_cast<const void *>(k), hipFuncAttributeMaxDynamicSharedMemorySize, kBuffers * WideLds<HD>::PAGE);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(k, grid, dim3(512), 2 * WideLds<HD>::PAGE, s, a);
+        hipLaunchKernelGGL(k, grid, dim3(512), kBuffers * WideLds<HD>::PAGE, s, a);
     } else {
         const auto k = a.R == 16 ? (small ? kv4_attn_kernel<HD, 1, true> : kv4_attn_kernel<HD, 1, false>)
                                  : (small ? kv4_attn_kernel<HD, 2, true> : kv4_attn_kernel<HD, 2, false>);
