@@ -159,11 +159,13 @@ __global__ void __launch_bounds__(kPrep) kv4_prep_kernel(AttnArgs a, int waves) 
     if (err) atomicOr(a.status, err);
 }
 
-// x against the lanes 16 and 32 away.
+// x against the lanes 32 away, and 16 away where a group is 16 lanes.
+template <int W>
 __device__ __forceinline__ float max_over_groups(float x) {
     const uint32_t b = __builtin_bit_cast(uint32_t, x);
     const auto p = __builtin_amdgcn_permlane32_swap(b, b, false, false);
     const float y = fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
+    if constexpr (W == 32) return y;
     const uint32_t c = __builtin_bit_cast(uint32_t, y);
     const auto q = __builtin_amdgcn_permlane16_swap(c, c, false, false);
     return fmaxf(__builtin_bit_cast(float, (uint32_t)q[0]), __builtin_bit_cast(float, (uint32_t)q[1]));
@@ -206,15 +208,28 @@ __device__ __forceinline__ float weight_of(float m, float top) {
     return m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - top);
 }
 
-// A wave's query rows, 16 n + j from `first`, and their softmax: NT tiles of 16 rows.
-template <int HD, int NT>
+using ikbo::mfma_bf16;
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// 32x32x16 bf16 MFMA: lane (g, j) = 32 g + j supplies A[j][8 g ..] and B[8 g ..][j]; acc[i] of it is D[8 (i / 4) + 4 g + i % 4][j].
+__device__ __forceinline__ f32x16_t mfma_bf16(const u32x4_t &a, const u32x4_t &b, f32x16_t acc) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+}
+
+// A wave's query rows, W n + j from `first`, and their softmax: NT tiles of W rows, on the W x W matrix instruction;
+// lane = W g + j.  Of a page's scores a lane holds EACH per query, element e (S[e / ACC][n][e % ACC]) being that of
+// token W/2 (e / 8) + 8 g + e % 8 with W = 32, 16 g + e with W = 16.
+template <int HD, int NT, int W>
 struct Queries {
-    static constexpr int TK = HD / 32, DT = HD / 16;
+    static constexpr int TK = HD * W / 512, DT = HD / W, ACC = W * W / 64, TILES = kPage / W, EACH = TILES * ACC, STEPS = EACH / 8;
+    typedef float acc_t __attribute__((ext_vector_type(ACC)));
     int limit[NT];                    // tokens that the row sees
     int most, least;                  // largest and smallest limit of the wave's rows
     u32x4_t qf[TK][NT];
-    f32x4_t o[DT][NT], lsum[NT];
+    acc_t o[DT][NT], lsum[NT];
     float m[NT], nm[NT];
+
+    static __device__ __forceinline__ int token(int e, int g) { return W == 16 ? 16 * g + e : 16 * (e >> 3) + 8 * g + (e & 7); }
 
     // Step s of a row's elements: lane group g holds the 8 from `base` + s * `step`.
     template <class P>
@@ -223,7 +238,7 @@ struct Queries {
         if (a.positions) most = 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = first + 16 * n + j;
+            const int r = first + W * n + j;
             const bool live = r < x.n_rows;
             int cnd, l, hq;
             plan.row(x, h, live ? r : 0, cnd, l, hq);
@@ -238,18 +253,18 @@ struct Queries {
             }
             m[n] = -__builtin_inff();
             nm[n] = 0.f;
-            lsum[n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+            lsum[n] = (acc_t)(0.f);
 #pragma unroll
-            for (int d = 0; d < DT; ++d) o[d][n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+            for (int d = 0; d < DT; ++d) o[d][n] = (acc_t)(0.f);
         }
         if (a.positions) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 most = max(most, limit[n]);
-                if (first + 16 * n + j < x.n_rows) least = min(least, limit[n]);
+                if (first + W * n + j < x.n_rows) least = min(least, limit[n]);
             }
 #pragma unroll
-            for (int d = 1; d < 16; d <<= 1) {
+            for (int d = 1; d < W; d <<= 1) {
                 most = max(most, __shfl_xor(most, d));
                 least = min(least, __shfl_xor(least, d));
             }
@@ -259,19 +274,17 @@ struct Queries {
     }
 
     // Scores of page p: what a row does not see becomes -inf, and the running maximum moves if it must.
-    __device__ __forceinline__ void raise(f32x4_t (&S)[4][NT], int p, int g, float scale_log2) {
+    __device__ __forceinline__ void raise(acc_t (&S)[TILES][NT], int p, int g, float scale_log2) {
         // The empty asm keeps these two branches branches: their bodies cost more than a turn's own
         // vector work, and as selects they would be paid on every page.
         if (p * kPage + kPage > least) {
             asm volatile("");
-            const int key0 = p * kPage + 16 * g;   // this lane's tokens: key0 + 4 t + i
+            const int key0 = p * kPage + token(0, g);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (key0 + 4 * t + i >= limit[n]) S[t][n][i] = -__builtin_inff();
+                for (int e = 0; e < EACH; ++e)
+                    if (key0 + token(e, 0) >= limit[n]) S[e / ACC][n][e % ACC] = -__builtin_inff();
         }
         bool grow = false;
         float mb[NT];
@@ -279,10 +292,8 @@ struct Queries {
         for (int n = 0; n < NT; ++n) {
             float x = -__builtin_inff();
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x = fmaxf(x, S[t][n][i]);
-            mb[n] = max_over_groups(x) * scale_log2;
+            for (int e = 0; e < EACH; ++e) x = fmaxf(x, S[e / ACC][n][e % ACC]);
+            mb[n] = max_over_groups<W>(x) * scale_log2;
             grow = grow || mb[n] > m[n] + kSlack;
         }
         if (__ballot(grow)) {
@@ -300,23 +311,23 @@ struct Queries {
         }
     }
 
-    // Scores into the weights pf (B operand of the two halves of 32 tokens) and their sums.
-    __device__ __forceinline__ void weigh(const f32x4_t (&S)[4][NT], float scale_log2, u32x4_t (&pf)[2][NT], int t0 = 0, int t1 = 4) {
+    // Scores into the weights pf (B operand of the steps of 512 / W tokens) and their sums, steps [s0, s1).
+    __device__ __forceinline__ void weigh(const acc_t (&S)[TILES][NT], float scale_log2, u32x4_t (&pf)[STEPS][NT], int s0 = 0, int s1 = STEPS) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int t = t0; t < t1; ++t) {
+            for (int e = 8 * s0; e < 8 * s1; e += 4) {
                 float w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[t][n][i], scale_log2, nm[n]));
-                pf[t >> 1][n][2 * (t & 1)] = pack_bf16x2(w[0], w[1]);
-                pf[t >> 1][n][2 * (t & 1) + 1] = pack_bf16x2(w[2], w[3]);
+                for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[e / ACC][n][e % ACC + i], scale_log2, nm[n]));
+                pf[e >> 3][n][(e & 7) >> 1] = pack_bf16x2(w[0], w[1]);
+                pf[e >> 3][n][((e & 7) >> 1) + 1] = pack_bf16x2(w[2], w[3]);
             }
         const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
-        for (int kk = t0 / 2; kk < t1 / 2; ++kk)
+        for (int s = s0; s < s1; ++s)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) lsum[n] = mfma_bf16(ones, pf[kk][n], lsum[n]);
+            for (int n = 0; n < NT; ++n) lsum[n] = mfma_bf16(ones, pf[s][n], lsum[n]);
     }
 };
 
@@ -456,7 +467,7 @@ __global__ void __launch_bounds__(64, 2) kv4_attn_kernel(AttnArgs a) {
         at += c.p1 - c.p0;
         Pages pages;   // the table's entry is on its way while the queries are found
         pages.open(a, c, TILE);
-        Queries<HD, NT> q;
+        Queries<HD, NT, 16> q;
         // The d order of K and Q: lane group g takes the g-th quarter of a head, one piece of a K row.
         q.load(a, plan, c.x, c.h, c.tile * 16 * NT, j, g * (HD / 4), 8);
         const int p1 = min(c.p1, (q.most + kPage - 1) / kPage);   // no row sees further pages
@@ -561,17 +572,15 @@ __global__ void __launch_bounds__(64, 2) kv4_attn_kernel(AttnArgs a) {
 template <int HD>
 struct WideLds {
     static constexpr int KBYTES = kPage * HD * 2, PAGE = 2 * KBYTES;
-    static __device__ __forceinline__ int half_of(int row, int turn) {
-        const int q = (row >> 1) & 7;
-        return q ^ ((((q >> 1) ^ (q >> 2)) & 1) * turn);
-    }
-    // Chunk c of token `key`; j is the token's place in the operand, and neighbouring g read neighbouring chunks.
+    // Chunk c of token `key`.
     static __device__ __forceinline__ int k_at(int key, int c) {
-        const int j = 4 * (key >> 4) + (key & 3);
-        return key * HD * 2 + ((c ^ (HD == 128 ? j : half_of(j, 1))) << 4);
+        const int j = (key & 19) | (key & 4) << 1 | (key & 8) >> 1;   // the token's place in the operand
+        return key * HD * 2 + ((c ^ (HD == 128 ? j & 15 : (j >> 1) & 7)) << 4);
     }
-    // Chunk c of element d: neighbouring g read chunks 2 apart.
-    static __device__ __forceinline__ int v_at(int d, int c) { return KBYTES + d * kPage * 2 + ((c ^ half_of(d, 2)) << 4); }
+    // Chunk c of element d; the rows of a pair change places with every pair, for the writes.
+    static __device__ __forceinline__ int v_at(int d, int c) {
+        return KBYTES + (d ^ ((d >> 1) & 1)) * kPage * 2 + ((c ^ ((d >> 1) & 7)) << 4);
+    }
 };
 
 // A barrier that waits for this wave's LDS accesses only: codes in flight stay so.
@@ -583,7 +592,7 @@ __device__ __forceinline__ void lds_barrier() {
 template <int HD>
 __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
     typedef WideLds<HD> L;
-    constexpr int NT = 2, WAVES = 8, ROWS = 32 * WAVES, THREADS = 64 * WAVES, TK = HD / 32, DT = HD / 16, TILE = 68 * HD;
+    constexpr int WAVES = 8, ROWS = 32 * WAVES, THREADS = 64 * WAVES, TK = HD / 16, DT = HD / 32, TILE = 68 * HD;
     // 8-byte pieces of a page's K codes (and of its V codes) and how many of them a thread takes; with more
     // threads than pieces the first half of the threads takes K and the second V.
     constexpr int PIECES = kPage * HD / 16, JOBS = PIECES >= THREADS ? PIECES / THREADS : 1;
@@ -592,17 +601,17 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
     extern __shared__ __align__(16) char lds[];
     __shared__ PlanLds<false> in_workspace;
     __shared__ int s_most[WAVES];
-    const int tid = (int)threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 4, j = lane & 15;
+    const int tid = (int)threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 5, j = lane & 31;
     Plan<false, THREADS> plan(a, in_workspace);
     const int64_t blk = run_of_block((int)gridDim.x), end = edge_of(a, plan, blk + 1);
     int2 note = make_int2(0, 0);
     // This thread's operand reads (K tile t: + 4 t rows; V tile x: + 16 x rows), and where its pieces come from and
     // go to: K piece i is 16 elements of token i / (HD/16), V piece i 8 tokens of element pair i / 8.
-    int k_off[TK], v_off[2], k_to[JOBS][2], v_to[JOBS][2], code_at[JOBS], ks_at[JOBS], vs_at[JOBS];
+    int k_off[TK], v_off[4], k_to[JOBS][2], v_to[JOBS][2], code_at[JOBS], ks_at[JOBS], vs_at[JOBS];
 #pragma unroll
-    for (int s = 0; s < TK; ++s) k_off[s] = L::k_at(16 * (j >> 2) + (j & 3), 4 * s + g);
+    for (int s = 0; s < TK; ++s) k_off[s] = L::k_at((j & 19) | (j & 4) << 1 | (j & 8) >> 1, 2 * s + g);
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) v_off[kk] = L::v_at(j, 2 * g + kk);
+    for (int s = 0; s < 4; ++s) v_off[s] = L::v_at(j, 2 * s + g);
     const bool has_k = BOTH || tid < PIECES, has_v = BOTH || tid >= PIECES;
 #pragma unroll
     for (int y = 0; y < JOBS; ++y) {
@@ -622,8 +631,8 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
         at += c.p1 - c.p0;
         Pages pages;
         pages.open(a, c, TILE);
-        Queries<HD, NT> q;
-        q.load(a, plan, c.x, c.h, c.tile * ROWS + wv * 16 * NT, j, 8 * g, 32);
+        Queries<HD, 1, 32> q;
+        q.load(a, plan, c.x, c.h, c.tile * ROWS + wv * 32, j, 8 * g, 16);
         if (lane == 0) s_most[wv] = q.most;
         __syncthreads();   // also: the block's last reads of the previous piece's pages are done
         int most = 0;
@@ -682,38 +691,35 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
                     }
                 }
             };
-            auto scores = [&](int p, f32x4_t (&S)[4][NT]) {
+            auto scores = [&](int p, f32x16_t (&S)[2][1]) {
                 const char *from = lds + (p & (kBuffers - 1)) * L::PAGE;
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) S[t][n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+                S[0][0] = S[1][0] = (f32x16_t)(0.f);
 #pragma unroll
                 for (int s = 0; s < TK; ++s)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const u32x4_t kf = *reinterpret_cast<const u32x4_t *>(from + k_off[s] + t * 4 * HD * 2);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) S[t][n] = mfma_bf16(kf, q.qf[s][n], S[t][n]);
+                    for (int t = 0; t < 2; ++t) {
+                        const u32x4_t kf = *reinterpret_cast<const u32x4_t *>(from + k_off[s] + t * 32 * HD * 2);
+                        S[t][0] = mfma_bf16(kf, q.qf[s][0], S[t][0]);
                     }
             };
-            auto product = [&](int p, int kk, const u32x4_t (&pf)[2][NT]) {
+            auto product = [&](int p, int s, const u32x4_t (&pf)[4][1]) {
                 const char *from = lds + (p & (kBuffers - 1)) * L::PAGE;
 #pragma unroll
                 for (int x = 0; x < DT; ++x) {
-                    const u32x4_t vf = *reinterpret_cast<const u32x4_t *>(from + v_off[kk] + x * 16 * kPage * 2);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) q.o[x][n] = mfma_bf16(vf, pf[kk][n], q.o[x][n]);
+                    const u32x4_t vf = *reinterpret_cast<const u32x4_t *>(from + v_off[s] + x * 32 * kPage * 2);
+                    q.o[x][0] = mfma_bf16(vf, pf[s][0], q.o[x][0]);
                 }
             };
-            auto accumulate = [&](int p, const f32x4_t (&S)[4][NT]) {
-                u32x4_t pf[2][NT];
+            auto accumulate = [&](int p, const f32x16_t (&S)[2][1]) {
+                u32x4_t pf[4][1];
                 q.weigh(S, a.scale_log2, pf, 0, 2);   // by halves: the second's weights overlap the first's products
                 product(p, 0, pf);
-                q.weigh(S, a.scale_log2, pf, 2, 4);
                 product(p, 1, pf);
+                q.weigh(S, a.scale_log2, pf, 2, 4);
+                product(p, 2, pf);
+                product(p, 3, pf);
             };
-            f32x4_t S[4][NT];
+            f32x16_t S[2][1];
             fetch(p0);
             tail(p0);
             convert(p0);
@@ -743,25 +749,33 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
             if (pages.bad && tid == 0) atomicOr(a.status, kStPage);
         }
 
-        // Lane (g, j) holds of query j the elements 16 x + 4 g + i.
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int in_unit = wv * 16 * NT + 16 * n + j, r = c.tile * ROWS + in_unit;
-            if (r >= c.x.n_rows) continue;
-            const float l = q.lsum[n][0];
+        // Lane (g, j) holds of query j the elements 32 x + 8 y + 4 g + i.
+        const int in_unit = wv * 32 + j, r = c.tile * ROWS + in_unit;
+        if (r < c.x.n_rows) {
+            const float l = q.lsum[0][0];
             const int64_t o_at = out_at(a, plan, c, r);
             if (c.n && g == 0) a.note_o[blk * a.R + in_unit] = o_at;
             if (c.whole) {
                 const float inv = inverse_of(l);
 #pragma unroll
                 for (int x = 0; x < DT; ++x)
-                    *reinterpret_cast<u32x2_t *>(a.O + o_at + 16 * x + 4 * g) =
-                        (u32x2_t){pack_bf16x2(q.o[x][n][0] * inv, q.o[x][n][1] * inv), pack_bf16x2(q.o[x][n][2] * inv, q.o[x][n][3] * inv)};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const f32x16_t &o = q.o[x][0];
+                        *reinterpret_cast<u32x2_t *>(a.O + o_at + 32 * x + 8 * y + 4 * g) =
+                            (u32x2_t){pack_bf16x2(o[4 * y] * inv, o[4 * y + 1] * inv), pack_bf16x2(o[4 * y + 2] * inv, o[4 * y + 3] * inv)};
+                    }
             } else {
                 const int64_t to = c.slot * ROWS + in_unit;
-                if (g == 0) a.ml[to] = make_float2(q.m[n], l);
+                if (g == 0) a.ml[to] = make_float2(q.m[0], l);
 #pragma unroll
-                for (int x = 0; x < DT; ++x) *reinterpret_cast<f32x4_t *>(a.part + to * HD + 16 * x + 4 * g) = q.o[x][n];
+                for (int x = 0; x < DT; ++x)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const f32x16_t &o = q.o[x][0];
+                        *reinterpret_cast<f32x4_t *>(a.part + to * HD + 32 * x + 8 * y + 4 * g) =
+                            (f32x4_t){o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]};
+                    }
             }
         }
     }
