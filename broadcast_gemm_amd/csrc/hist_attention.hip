@@ -19,6 +19,10 @@
 // the product, and their sums are sums of the rounded ones (an all-ones A operand): half a step of
 // bf16 on a weight, as in the dense attention.
 //
+// The wide kernel does the same with v_mfma_f32_32x32x16_bf16 and lane = 32 g + j: row j of tile t is token 32 t +
+// j with bits 2 and 3 exchanged, and the lane ends up with tokens 16 s + 8 g + i, i < 8, for its four steps s.  Half
+// the matrix instructions leave more room for vector work beside them: head 128 205 -> 202 us, head 64 101 -> 94.
+//
 // Two kernels.  In the narrow one a block is one wave with 16 or 32 rows, which converts the codes it
 // reads for itself, registers to registers: with few rows the cache's bytes are what counts, and 8 waves
 // on a CU keep 5 TB/s of them coming.  Every wave repeats the conversion, so with many rows per user and
@@ -231,37 +235,41 @@ struct Queries {
 
     static __device__ __forceinline__ int token(int e, int g) { return W == 16 ? 16 * g + e : 16 * (e >> 3) + 8 * g + (e & 7); }
 
-    // Step s of a row's elements: lane group g holds the 8 from `base` + s * `step`.
+    const uint16_t *from[NT];         // the rows in Q
+    int64_t to[NT];                   // and in O
+    int pos[NT];
+    bool live[NT];
+
     template <class P>
-    __device__ __forceinline__ void load(const AttnArgs &a, const P &plan, const User &x, int h, int first, int j, int base, int step) {
+    __device__ __forceinline__ void find(const AttnArgs &a, const P &plan, const User &x, int h, int first, int j) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = first + W * n + j;
+            live[n] = r < x.n_rows;
+            int cnd, l, hq;
+            plan.row(x, h, live[n] ? r : 0, cnd, l, hq);
+            from[n] = a.Q + cnd * a.q_cand + hq * a.q_head + l * a.q_query;
+            to[n] = cnd * a.o_cand + hq * a.o_head + l * a.o_query;
+            if (a.positions) pos[n] = a.positions[(int64_t)cnd * a.L_q + l];
+        }
+    }
+    // Step s of a row's elements: lane group g holds the 8 from `base` + s * `step`.
+    __device__ __forceinline__ void load(const AttnArgs &a, const User &x, int base, int step) {
         most = least = x.len;
         if (a.positions) most = 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = first + W * n + j;
-            const bool live = r < x.n_rows;
-            int cnd, l, hq;
-            plan.row(x, h, live ? r : 0, cnd, l, hq);
-            const uint16_t *q = a.Q + cnd * a.q_cand + hq * a.q_head + l * a.q_query + base;
 #pragma unroll
             for (int s = 0; s < TK; ++s)
-                qf[s][n] = live ? *reinterpret_cast<const u32x4_t *>(q + s * step) : (u32x4_t){0, 0, 0, 0};
-            limit[n] = live ? x.len : 0;
-            if (live && a.positions) {
-                const int pos = a.positions[(int64_t)cnd * a.L_q + l];
-                limit[n] = pos < 0 ? 0 : pos < x.len ? pos + 1 : x.len;
-            }
-            m[n] = -__builtin_inff();
-            nm[n] = 0.f;
-            lsum[n] = (acc_t)(0.f);
-#pragma unroll
-            for (int d = 0; d < DT; ++d) o[d][n] = (acc_t)(0.f);
+                qf[s][n] = live[n] ? *reinterpret_cast<const u32x4_t *>(from[n] + base + s * step) : (u32x4_t){0, 0, 0, 0};
+            limit[n] = live[n] ? x.len : 0;
+            if (live[n] && a.positions) limit[n] = pos[n] < 0 ? 0 : pos[n] < x.len ? pos[n] + 1 : x.len;
         }
         if (a.positions) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 most = max(most, limit[n]);
-                if (first + W * n + j < x.n_rows) least = min(least, limit[n]);
+                if (live[n]) least = min(least, limit[n]);
             }
 #pragma unroll
             for (int d = 1; d < W; d <<= 1) {
@@ -270,6 +278,17 @@ struct Queries {
             }
             most = __builtin_amdgcn_readfirstlane(most);
             least = __builtin_amdgcn_readfirstlane(least);
+        }
+    }
+
+    __device__ __forceinline__ void start() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n] = -__builtin_inff();
+            nm[n] = 0.f;
+            lsum[n] = (acc_t)(0.f);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d][n] = (acc_t)(0.f);
         }
     }
 
@@ -342,44 +361,45 @@ struct Piece {
 // Where the run of block `blk` begins (that of block `blk` - 1 ends).
 template <class P>
 __device__ __forceinline__ int64_t edge_of(const AttnArgs &a, const P &plan, int64_t blk) {
-    const int64_t all = plan.work[a.B_u], x = blk * plan.share, near = plan.share >> 3;
+    const int64_t all = plan.work[a.B_u], x = blk * plan.share, near = near_of(plan.share);
     if (x <= 0) return 0;
     if (x >= all) return all;
     const int u = owner_of(plan.work, a.B_u, x);
-    const int64_t pages = plan.pages_of_user(u), in = (x - plan.work[u]) % pages;
+    const int64_t pages = plan.pages_of_user(u), in_u = x - plan.work[u], in = in_u - over(in_u, pages) * pages;
     if (in <= near && in <= pages - in) return x - in;
     return pages - in <= near ? x + pages - in : x;
 }
 template <class P>
-__device__ __forceinline__ Piece piece_at(const AttnArgs &a, P &plan, int64_t at, int64_t end, int64_t blk) {
+__device__ __forceinline__ Piece piece_at(const AttnArgs &a, P &plan, User &x, int64_t at, int64_t end, int64_t blk) {
     Piece c;
-    c.x = plan.enter(owner_of(plan.work, a.B_u, at));
+    if (at >= x.to) x = plan.enter(owner_of(plan.work, a.B_u, at));   // most runs stay with one user
+    c.x = x;
     // Within a user units and pages are counted in 64 bits; a unit's number fits 32.
     const int64_t local = at - c.x.from;
-    const int64_t unit = local / c.x.pages;
+    const int64_t unit = over(local, c.x.pages);
     c.p0 = (int)(local - unit * c.x.pages);
     c.p1 = (int)min((int64_t)c.x.pages, c.p0 + (end - at));
-    c.h = (int)unit / c.x.tiles;
+    c.h = (int)((uint32_t)unit / (uint32_t)c.x.tiles);
     c.tile = (int)unit - c.h * c.x.tiles;
     c.whole = c.p0 == 0 && c.p1 == c.x.pages;
     c.slot = 2 * blk + (c.p0 == 0);
     // The pieces end at the runs' ends that lie further than `near` from both edges of the unit.
-    const int64_t near = plan.share >> 3;
-    c.n = c.p0 == 0 && !c.whole ? (int)((at + c.x.pages - near - 1) / plan.share - (at + near) / plan.share) + 1 : 0;
+    const int64_t near = near_of(plan.share);
+    c.n = c.p0 == 0 && !c.whole ? (int)(over(at + c.x.pages - near - 1, plan.share) - over(at + near, plan.share)) + 1 : 0;
     return c;
-}
-
-// Where row r of the piece's user and head stands in O.
-template <class P>
-__device__ __forceinline__ int64_t out_at(const AttnArgs &a, const P &plan, const Piece &c, int r) {
-    int cnd, l, hq;
-    plan.row(c.x, c.h, r, cnd, l, hq);
-    return cnd * a.o_cand + hq * a.o_head + l * a.o_query;
 }
 
 // Blocks are dealt to the 8 dies in turn: give each die neighbouring runs, whose units share K and V.
 __device__ __forceinline__ int64_t run_of_block(int blocks) {
     return (blocks & 7) ? blockIdx.x : (int64_t)(blockIdx.x & 7) * (blocks >> 3) + (blockIdx.x >> 3);
+}
+
+// Bytes in device memory, said to the compiler: an address put together from integers is a flat one to it otherwise,
+// and the wait for an LDS read then waits for every such load in flight as well.
+typedef const __attribute__((address_space(1))) char *global_bytes;
+template <class T>
+__device__ __forceinline__ T load(global_bytes p) {
+    return *(const __attribute__((address_space(1))) T *)p;
 }
 
 // The tiles of a run of pages: lane i keeps the page number of page base + i, so that a tile's address
@@ -408,7 +428,7 @@ struct Pages {
         ids = row[min(p + ((int)threadIdx.x & 63), last)];
     }
     // The tile of page p (of the last page if p is behind it); p never decreases by more than the caller's look-ahead.
-    __device__ __forceinline__ const char *at(int p) {
+    __device__ __forceinline__ global_bytes at(int p) {
         p = min(p, last);
         if (p - base >= 64) read(p);
         int page = __builtin_amdgcn_readlane(ids, p - base);
@@ -416,7 +436,7 @@ struct Pages {
         // In scalar registers: loads then take it as their base.
         const uint64_t at = reinterpret_cast<uint64_t>(tiles) + (uint64_t)page * stride;
         const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at), hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
-        return reinterpret_cast<const char *>(((uint64_t)hi << 32) | lo);
+        return (global_bytes)(((uint64_t)hi << 32) | lo);
     }
 };
 
@@ -428,27 +448,27 @@ struct PageRegs {
     uint32_t k[4][KW];
     uint32_t ks;
     u32x4_t v[VJ], vs[VJ];
-    __device__ __forceinline__ void load_k(const char *tile, int g, int j) {
+    __device__ __forceinline__ void load_k(global_bytes tile, int g, int j) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const char *p = tile + (16 * (j >> 2) + 4 * t + (j & 3)) * (HD / 2) + g * (HD / 8);
+            const global_bytes p = tile + (16 * (j >> 2) + 4 * t + (j & 3)) * (HD / 2) + g * (HD / 8);
             if constexpr (HD == 128) {
-                const u32x4_t w = *reinterpret_cast<const u32x4_t *>(p);
+                const u32x4_t w = load<u32x4_t>(p);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) k[t][i] = w[i];
             } else {
-                const u32x2_t w = *reinterpret_cast<const u32x2_t *>(p);
+                const u32x2_t w = load<u32x2_t>(p);
                 k[t][0] = w[0];
                 k[t][1] = w[1];
             }
         }
-        ks = *reinterpret_cast<const uint32_t *>(tile + 64 * HD + (HD == 128 ? g : g >> 1) * 64 + 4 * j);
+        ks = load<uint32_t>(tile + 64 * HD + (HD == 128 ? g : g >> 1) * 64 + 4 * j);
     }
-    __device__ __forceinline__ void load_v(const char *tile, int g, int j) {
+    __device__ __forceinline__ void load_v(global_bytes tile, int g, int j) {
 #pragma unroll
         for (int jj = 0; jj < VJ; ++jj) {
-            v[jj] = *reinterpret_cast<const u32x4_t *>(tile + 32 * HD + (16 * jj + j) * 64 + 16 * g);
-            vs[jj] = *reinterpret_cast<const u32x4_t *>(tile + 66 * HD + jj * 64 + 16 * g);
+            v[jj] = load<u32x4_t>(tile + 32 * HD + (16 * jj + j) * 64 + 16 * g);
+            vs[jj] = load<u32x4_t>(tile + 66 * HD + jj * 64 + 16 * g);
         }
     }
 };
@@ -461,19 +481,23 @@ __global__ void __launch_bounds__(64, 2) kv4_attn_kernel(AttnArgs a) {
     Plan<SMALL, 64> plan(a, small);
     const int64_t blk = run_of_block((int)gridDim.x), end = edge_of(a, plan, blk + 1);
     int2 note = make_int2(0, 0);
+    User user;
+    user.to = -1;
     for (int64_t at = edge_of(a, plan, blk); at < end;) {
-        const Piece c = piece_at(a, plan, at, end, blk);
+        const Piece c = piece_at(a, plan, user, at, end, blk);
         if (c.n) note = make_int2(c.n, min(a.R, c.x.n_rows - c.tile * a.R));
         at += c.p1 - c.p0;
         Pages pages;   // the table's entry is on its way while the queries are found
         pages.open(a, c, TILE);
         Queries<HD, NT, 16> q;
         // The d order of K and Q: lane group g takes the g-th quarter of a head, one piece of a K row.
-        q.load(a, plan, c.x, c.h, c.tile * 16 * NT, j, g * (HD / 4), 8);
+        q.find(a, plan, c.x, c.h, c.tile * 16 * NT, j);
+        q.load(a, c.x, g * (HD / 4), 8);
+        q.start();
         const int p1 = min(c.p1, (q.most + kPage - 1) / kPage);   // no row sees further pages
         PageRegs<HD> pg;
         for (int p = c.p0; p < p1; ++p) {
-            const char *tile = pages.at(p);
+            const global_bytes tile = pages.at(p);
             pg.load_k(tile, g, j);
             pg.load_v(tile, g, j);
             f32x4_t S[4][NT];
@@ -527,7 +551,7 @@ __global__ void __launch_bounds__(64, 2) kv4_attn_kernel(AttnArgs a) {
             const int in_unit = 16 * n + j, r = c.tile * 16 * NT + in_unit;
             if (r >= c.x.n_rows) continue;
             const float l = q.lsum[n][0];
-            const int64_t o_at = out_at(a, plan, c, r);
+            const int64_t o_at = q.to[n];
             if (c.n && g == 0) a.note_o[blk * a.R + in_unit] = o_at;
             if (c.whole) {
                 const float inv = inverse_of(l);
@@ -562,13 +586,13 @@ __global__ void __launch_bounds__(64, 2) kv4_attn_kernel(AttnArgs a) {
 
 // ---- the wide kernel -----------------------------------------------------------------------
 
-// Four page buffers in LDS: K rows [64 tokens][HD] and V^T rows [HD][64 tokens], bf16.  The 16-byte
-// chunks of a row stand permuted by an XOR with a number of the row.  A 16-byte read of a wave is served 16
-// lanes at a time, and not in their order: lanes 0-3, 12-15, 20-23 and 24-27, then 4-11, 16-19 and 28-31, and so
-// on (measured with pairs of patterns).  With lane 16 g + j that is every j once, some with g and the others with
-// g ^ 1.  Where a row is 256 bytes (all 64 banks) the XOR with j serves both; where it is 128, two neighbouring
-// rows make up the banks, and half of j is taken, turned by the difference of g's two chunks for the j of the
-// second kind (2 .. 5 of 8): without conflicts a wave's read takes 4 cycles instead of 8.
+// Four page buffers in LDS: K rows [64 tokens][HD] and V^T rows [HD][64 tokens], bf16.  The 16-byte chunks of a row
+// stand permuted by an XOR with a number of the row.  A 16-byte access of a wave is served 16 lanes at a time, and not
+// in their order: lanes 0-3, 12-15, 20-23 and 24-27, then 4-11, 16-19 and 28-31, and so on (measured with pairs of
+// patterns).  Those of the first set and those of the second hold each value of j % 16 once among j = lane % 32, and
+// their g is the same: the 16 rows' chunks fall on 16 places of 256 bytes if the numbers are j % 16 for rows of 256
+// bytes, (j / 2) % 8 for rows of 128, where neighbouring rows are the two halves.  Without conflicts a wave's read
+// takes 4 cycles instead of 8 and more.
 template <int HD>
 struct WideLds {
     static constexpr int KBYTES = kPage * HD * 2, PAGE = 2 * KBYTES;
@@ -600,9 +624,10 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
     static_assert(BOTH || 2 * PIECES == THREADS, "every thread takes K, V or both");
     extern __shared__ __align__(16) char lds[];
     __shared__ PlanLds<false> in_workspace;
-    __shared__ int s_most[WAVES];
+    __shared__ int s_most[2][WAVES];
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = tid >> 6, g = lane >> 5, j = lane & 31;
     Plan<false, THREADS> plan(a, in_workspace);
+    int odd_piece = 0;
     const int64_t blk = run_of_block((int)gridDim.x), end = edge_of(a, plan, blk + 1);
     int2 note = make_int2(0, 0);
     // This thread's operand reads (K tile t: + 4 t rows; V tile x: + 16 x rows), and where its pieces come from and
@@ -625,72 +650,94 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
             v_to[y][x] = L::v_at(2 * pair + x, i & 7);
         }
     }
+    User user;
+    user.to = -1;
     for (int64_t at = edge_of(a, plan, blk); at < end;) {
-        const Piece c = piece_at(a, plan, at, end, blk);
+        const Piece c = piece_at(a, plan, user, at, end, blk);
         if (c.n) note = make_int2(c.n, min(a.R, c.x.n_rows - c.tile * a.R));
         at += c.p1 - c.p0;
         Pages pages;
         pages.open(a, c, TILE);
         Queries<HD, 1, 32> q;
-        q.load(a, plan, c.x, c.h, c.tile * ROWS + wv * 32, j, 8 * g, 16);
-        if (lane == 0) s_most[wv] = q.most;
-        __syncthreads();   // also: the block's last reads of the previous piece's pages are done
+        q.find(a, plan, c.x, c.h, c.tile * ROWS + wv * 32, j);
+        const int p0 = c.p0;
+        u32x2_t kc[2][JOBS], vc[2][JOBS], vs[2][JOBS];
+        uint32_t ks[2][JOBS];
+        auto fetch = [&](int p, int w) {
+            const global_bytes tile = pages.at(p);
+#pragma unroll
+            for (int y = 0; y < JOBS; ++y) {
+                if (has_k) {
+                    kc[w][y] = load<u32x2_t>(tile + code_at[y]);
+                    ks[w][y] = load<uint8_t>(tile + ks_at[y]);
+                }
+                if (has_v) {
+                    vc[w][y] = load<u32x2_t>(tile + code_at[y] + 32 * HD);
+                    vs[w][y] = load<u32x2_t>(tile + vs_at[y]);
+                }
+            }
+        };
+        auto tail = [&](int p, int w) {
+            const int left = c.x.len - min(p, pages.last) * kPage;   // tokens of the page that exist
+            if (left < kPage) {
+                asm volatile("");
+#pragma unroll
+                for (int y = 0; y < JOBS; ++y)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) vs[w][y][x] = existing(vs[w][y][x], left - (8 * (tid & 7) + 4 * x));
+            }
+        };
+        auto convert = [&](int p, int w) {
+            char *to = lds + (p & (kBuffers - 1)) * L::PAGE;
+#pragma unroll
+            for (int y = 0; y < JOBS; ++y) {
+                if (has_k) {
+                    const float s = scale_of(ks[w][y], 0);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) *reinterpret_cast<u32x4_t *>(to + k_to[y][x]) = values8(kc[w][y][x], s);
+                }
+                if (has_v) {
+                    u32x4_t even, odd;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t e0, e1, o0, o1;
+                        values_v(vc[w][y][x], vs[w][y][x], e0, e1, o0, o1);
+                        even[2 * x] = e0;
+                        even[2 * x + 1] = e1;
+                        odd[2 * x] = o0;
+                        odd[2 * x + 1] = o1;
+                    }
+                    *reinterpret_cast<u32x4_t *>(to + v_to[y][0]) = even;
+                    *reinterpret_cast<u32x4_t *>(to + v_to[y][1]) = odd;
+                }
+            }
+        };
+        // The first pages' codes are on their way before the queries' are waited for, and converted before the barrier
+        // below (the previous piece's last reads were before its last).
+        const bool any = p0 <= pages.last;
+        if (any) {
+            fetch(p0, 0);
+            fetch(p0 + 1, 1);
+        }
+        q.load(a, c.x, 8 * g, 16);
+        q.start();
+        int *ends = s_most[odd_piece];   // two, for a wave may be a barrier ahead of one that still reads
+        odd_piece ^= 1;
+        if (lane == 0) ends[wv] = q.most;
+        if (any) {
+            tail(p0, 0);
+            convert(p0, 0);
+            fetch(p0 + 2, 0);
+            tail(p0 + 1, 1);
+            convert(p0 + 1, 1);
+            fetch(p0 + 3, 1);
+        }
+        lds_barrier();
         int most = 0;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) most = max(most, s_most[w]);
-        const int p0 = c.p0, p1 = min(c.p1, (most + kPage - 1) / kPage);   // no row sees further pages
+        for (int w = 0; w < WAVES; ++w) most = max(most, ends[w]);
+        const int p1 = min(c.p1, (most + kPage - 1) / kPage);   // no row sees further pages
         if (p0 < p1) {
-            u32x2_t kc[JOBS], vc[JOBS], vs[JOBS];
-            uint32_t ks[JOBS];
-            auto fetch = [&](int p) {
-                const char *tile = pages.at(p);
-#pragma unroll
-                for (int y = 0; y < JOBS; ++y) {
-                    if (has_k) {
-                        kc[y] = *reinterpret_cast<const u32x2_t *>(tile + code_at[y]);
-                        ks[y] = (uint8_t)tile[ks_at[y]];
-                    }
-                    if (has_v) {
-                        vc[y] = *reinterpret_cast<const u32x2_t *>(tile + code_at[y] + 32 * HD);
-                        vs[y] = *reinterpret_cast<const u32x2_t *>(tile + vs_at[y]);
-                    }
-                }
-            };
-            auto tail = [&](int p) {
-                const int left = c.x.len - min(p, pages.last) * kPage;   // tokens of the page that exist
-                if (left < kPage) {
-                    asm volatile("");
-#pragma unroll
-                    for (int y = 0; y < JOBS; ++y)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) vs[y][x] = existing(vs[y][x], left - (8 * (tid & 7) + 4 * x));
-                }
-            };
-            auto convert = [&](int p) {
-                char *to = lds + (p & (kBuffers - 1)) * L::PAGE;
-#pragma unroll
-                for (int y = 0; y < JOBS; ++y) {
-                    if (has_k) {
-                        const float s = scale_of(ks[y], 0);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) *reinterpret_cast<u32x4_t *>(to + k_to[y][x]) = values8(kc[y][x], s);
-                    }
-                    if (has_v) {
-                        u32x4_t even, odd;
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            uint32_t e0, e1, o0, o1;
-                            values_v(vc[y][x], vs[y][x], e0, e1, o0, o1);
-                            even[2 * x] = e0;
-                            even[2 * x + 1] = e1;
-                            odd[2 * x] = o0;
-                            odd[2 * x + 1] = o1;
-                        }
-                        *reinterpret_cast<u32x4_t *>(to + v_to[y][0]) = even;
-                        *reinterpret_cast<u32x4_t *>(to + v_to[y][1]) = odd;
-                    }
-                }
-            };
             auto scores = [&](int p, f32x16_t (&S)[2][1]) {
                 const char *from = lds + (p & (kBuffers - 1)) * L::PAGE;
                 S[0][0] = S[1][0] = (f32x16_t)(0.f);
@@ -720,40 +767,32 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
                 product(p, 3, pf);
             };
             f32x16_t S[2][1];
-            fetch(p0);
-            tail(p0);
-            convert(p0);
-            fetch(p0 + 1);
-            tail(p0 + 1);
-            convert(p0 + 1);
-            fetch(p0 + 2);
-            lds_barrier();
             // Two pages a barrier: a page's buffer takes the one four pages on, two turns after the barrier behind
             // its last reads.  Pages behind the last are taken again from the last one (into buffers that nothing
             // reads), which keeps the turns free of branches.  The conversion stands behind the scores' matrix
             // instructions, which it can overlap (in front of them: 6% slower).  Waves without a row that sees
             // the page do the same work on masked scores: a branch around it cost the others a tenth.
-            auto turn = [&](int p) {
-                tail(p + 2);
+            auto turn = [&](int p, int w) {
+                tail(p + 2, w);
                 scores(p, S);
-                convert(p + 2);
-                fetch(p + 3);
+                convert(p + 2, w);
+                fetch(p + 4, w);
                 q.raise(S, p, g, a.scale_log2);
                 accumulate(p, S);
             };
             for (int p = p0; p < p1; p += 2) {
-                turn(p);
-                if (p + 1 < p1) turn(p + 1);
+                turn(p, 0);
+                if (p + 1 < p1) turn(p + 1, 1);
                 lds_barrier();
             }
             if (pages.bad && tid == 0) atomicOr(a.status, kStPage);
         }
 
         // Lane (g, j) holds of query j the elements 32 x + 8 y + 4 g + i.
-        const int in_unit = wv * 32 + j, r = c.tile * ROWS + in_unit;
-        if (r < c.x.n_rows) {
+        const int in_unit = wv * 32 + j;
+        if (q.live[0]) {
             const float l = q.lsum[0][0];
-            const int64_t o_at = out_at(a, plan, c, r);
+            const int64_t o_at = q.to[0];
             if (c.n && g == 0) a.note_o[blk * a.R + in_unit] = o_at;
             if (c.whole) {
                 const float inv = inverse_of(l);

@@ -6,9 +6,9 @@
 // even whatever the lengths are, and a unit is cut only where a run ends.  Neighbouring units share
 // their K and V.
 //
-// A run's end that falls within an eighth of a run of a unit's edge moves to that edge: runs then differ by a
-// quarter at most, and many short units (1080 units of 15 pages in 256 runs) are hardly cut at all, which costs
-// less than writing and joining their pieces.
+// A run's end that falls within a sixteenth of a run of a unit's edge moves to that edge: a cut costs writing and
+// joining two pieces (260 KB at 256 rows of head 128), a move makes runs uneven, by an eighth at most.  1080 units of
+// 13 to 16 pages in 256 runs, us with the join: 222 where a 512th moves, 215 with a sixteenth, 220 with an eighth.
 //
 // A block leaves at most two partial results: one of the unit that its run begins inside (slot 2 b),
 // one of a unit that begins in its run and goes on after it (slot 2 b + 1).  So the pieces of a unit
@@ -63,6 +63,13 @@ __device__ __forceinline__ int64_t share_of(int64_t work, int log_blocks) {
     return s > 1 ? s : 1;
 }
 
+// Runs' ends move by this much at most.
+__device__ __forceinline__ int64_t near_of(int64_t share) { return share >> 4; }
+// x / y for 0 <= x, 0 < y: in 32 bits where they do (a quotient in 64 takes 150 instructions).
+__device__ __forceinline__ int64_t over(int64_t x, int64_t y) {
+    return (x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
+}
+
 // Exclusive scan over a wave.
 template <class T>
 __device__ __forceinline__ T wave_before(T v, T *total) {
@@ -104,7 +111,7 @@ using PlanLds = typename std::conditional<SMALL, SmallPlan, int>::type;
 
 struct User {
     int u, len, pages, n_rows, tiles, cand0;
-    int64_t from;                     // its first page in the line
+    int64_t from, to;                 // its pages in the line
 };
 
 template <bool SMALL, int NTH>
@@ -186,6 +193,7 @@ struct Plan {
         User x;
         x.u = u;
         x.from = work[u];
+        x.to = work[u + 1];
         x.len = clamp_len(a.lens[u], a.max_pages);
         x.pages = max(1, pages_of(x.len));
         if constexpr (SMALL) {
