@@ -395,11 +395,12 @@ __device__ __forceinline__ int64_t run_of_block(int blocks) {
 }
 
 // Bytes in device memory, said to the compiler: an address put together from integers is a flat one to it otherwise,
-// and the wait for an LDS read then waits for every such load in flight as well.
+// and the wait for an LDS read then waits for every such load in flight as well.  ONCE: not to be kept in the caches.
 typedef const __attribute__((address_space(1))) char *global_bytes;
-template <class T>
+template <class T, bool ONCE = false>
 __device__ __forceinline__ T load(global_bytes p) {
-    return *(const __attribute__((address_space(1))) T *)p;
+    const auto x = (const __attribute__((address_space(1))) T *)p;
+    return ONCE ? __builtin_nontemporal_load(x) : *x;
 }
 
 // The tiles of a run of pages: lane i keeps the page number of page base + i, so that a tile's address
@@ -448,32 +449,34 @@ struct PageRegs {
     uint32_t k[4][KW];
     uint32_t ks;
     u32x4_t v[VJ], vs[VJ];
+    template <bool ONCE>
     __device__ __forceinline__ void load_k(global_bytes tile, int g, int j) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const global_bytes p = tile + (16 * (j >> 2) + 4 * t + (j & 3)) * (HD / 2) + g * (HD / 8);
             if constexpr (HD == 128) {
-                const u32x4_t w = load<u32x4_t>(p);
+                const u32x4_t w = load<u32x4_t, ONCE>(p);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) k[t][i] = w[i];
             } else {
-                const u32x2_t w = load<u32x2_t>(p);
+                const u32x2_t w = load<u32x2_t, ONCE>(p);
                 k[t][0] = w[0];
                 k[t][1] = w[1];
             }
         }
-        ks = load<uint32_t>(tile + 64 * HD + (HD == 128 ? g : g >> 1) * 64 + 4 * j);
+        ks = load<uint32_t, ONCE>(tile + 64 * HD + (HD == 128 ? g : g >> 1) * 64 + 4 * j);
     }
+    template <bool ONCE>
     __device__ __forceinline__ void load_v(global_bytes tile, int g, int j) {
 #pragma unroll
         for (int jj = 0; jj < VJ; ++jj) {
-            v[jj] = load<u32x4_t>(tile + 32 * HD + (16 * jj + j) * 64 + 16 * g);
-            vs[jj] = load<u32x4_t>(tile + 66 * HD + jj * 64 + 16 * g);
+            v[jj] = load<u32x4_t, ONCE>(tile + 32 * HD + (16 * jj + j) * 64 + 16 * g);
+            vs[jj] = load<u32x4_t, ONCE>(tile + 66 * HD + jj * 64 + 16 * g);
         }
     }
 };
 
-template <int HD, int NT, bool SMALL>
+template <int HD, int NT, bool SMALL, bool ONCE>
 __global__ void __launch_bounds__(64, 2) kv4_attn_kernel(AttnArgs a) {
     constexpr int VJ = HD / 32, TILE = 68 * HD;
     __shared__ PlanLds<SMALL> small;
@@ -498,8 +501,8 @@ __global__ void __launch_bounds__(64, 2) kv4_attn_kernel(AttnArgs a) {
         PageRegs<HD> pg;
         for (int p = c.p0; p < p1; ++p) {
             const global_bytes tile = pages.at(p);
-            pg.load_k(tile, g, j);
-            pg.load_v(tile, g, j);
+            pg.template load_k<ONCE>(tile, g, j);
+            pg.template load_v<ONCE>(tile, g, j);
             f32x4_t S[4][NT];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -788,7 +791,7 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
             if (pages.bad && tid == 0) atomicOr(a.status, kStPage);
         }
 
-        // Lane (g, j) holds of query j the elements 32 x + 8 y + 4 g + i.
+        // Lane (g, j) holds of query j the elements 32 x + 8 y + 4 g + i.  Both lanes of a query are live, or neither is.
         const int in_unit = wv * 32 + j;
         if (q.live[0]) {
             const float l = q.lsum[0][0];
@@ -799,10 +802,18 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
 #pragma unroll
                 for (int x = 0; x < DT; ++x)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
+                    for (int y = 0; y < 4; y += 2) {
+                        // The lanes 32 away have each other's neighbours: g = 0 takes the 8 elements of y, g = 1 those of y + 1.
                         const f32x16_t &o = q.o[x][0];
-                        *reinterpret_cast<u32x2_t *>(a.O + o_at + 32 * x + 8 * y + 4 * g) =
-                            (u32x2_t){pack_bf16x2(o[4 * y] * inv, o[4 * y + 1] * inv), pack_bf16x2(o[4 * y + 2] * inv, o[4 * y + 3] * inv)};
+                        u32x4_t w;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const auto p = __builtin_amdgcn_permlane32_swap(pack_bf16x2(o[4 * y + 2 * i] * inv, o[4 * y + 2 * i + 1] * inv),
+                                                                            pack_bf16x2(o[4 * y + 4 + 2 * i] * inv, o[4 * y + 5 + 2 * i] * inv), false, false);
+                            w[i] = p[0];
+                            w[2 + i] = p[1];
+                        }
+                        *reinterpret_cast<u32x4_t *>(a.O + o_at + 32 * x + 8 * (y + g)) = w;
                     }
             } else {
                 const int64_t to = c.slot * ROWS + in_unit;
@@ -900,8 +911,12 @@ hipError_t launch(const AttnArgs &a, int64_t line_most, hipStream_t s) {
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(k, grid, dim3(512), kBuffers * WideLds<HD>::PAGE, s, a);
     } else {
-        const auto k = a.R == 16 ? (small ? kv4_attn_kernel<HD, 1, true> : kv4_attn_kernel<HD, 1, false>)
-                                 : (small ? kv4_attn_kernel<HD, 2, true> : kv4_attn_kernel<HD, 2, false>);
+        // With 16 rows to a unit hardly any two units share a tile, and a cache larger than the 256 MB of the last level
+        // is read past it: 97 -> 87 us for 0.46 GB; 0.1 GB, which stays there from call to call, would take 35 for 34.
+        const bool once = a.R == 16 && (int64_t)a.B_u * a.max_pages * a.H_kv * (68 * HD) > (256ll << 20);
+        const auto k = a.R != 16 ? (small ? kv4_attn_kernel<HD, 2, true, false> : kv4_attn_kernel<HD, 2, false, false>)
+                       : once    ? (small ? kv4_attn_kernel<HD, 1, true, true> : kv4_attn_kernel<HD, 1, false, true>)
+                                 : (small ? kv4_attn_kernel<HD, 1, true, false> : kv4_attn_kernel<HD, 1, false, false>);
         hipLaunchKernelGGL(k, grid, dim3(64), 0, s, a);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;

@@ -609,6 +609,36 @@ def test_attend_plans(B_u, B_c, Hq, Hkv, Lq, dim, longest, mapping, positions):
     assert (got[users < 0] == 5).all() and np.isfinite(got).all()
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("B_u, Hkv, width", [(5, 2, 16500), (300, 1, 220)])
+def test_attend_tables_for_more_than_the_last_cache_level(B_u, Hkv, width, dim):
+    """Tables whose histories could take more than 256 MB: tiles are read past the caches then."""
+    assert B_u * width * Hkv * 68 * dim > 256 << 20
+    lens = list(np.random.default_rng(width).integers(0, 200, B_u))
+    attend_case(5, lens, B_u, 2 * Hkv, Hkv, 2, dim, mapping="none", width=width)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_units_that_see_nothing(dim):
+    """Many rows of one page each, several units to a block; whole units and parts of them see no token."""
+    t = torch()
+    rng = np.random.default_rng(dim)
+    B_c, Hkv, lens = 40000, 4, np.array([50])
+    tiles, d_table, table, k, v = history(rng, lens, 1, Hkv, dim)
+    pos = np.where(np.arange(B_c) // 256 % 3 < 2, -1, rng.integers(-1, 60, B_c)).astype(np.int32)[:, None]
+    pos[300:310] = 20
+    Q = dev(rng.standard_normal((B_c, Hkv, 1, dim)), t.bfloat16)
+    st = word()
+    out = t.full_like(Q, 5.0)
+    H().kv4_attention(Q, tiles, d_table, dev(lens.astype(np.int32)), dev(np.zeros(B_c, np.int32)), st, positions=dev(pos), out=out)
+    assert H().kv_status(st) == bga.IKBO_OK
+    got = f64(out)
+    pick = np.unique(np.concatenate([np.arange(290, 320), rng.integers(0, B_c, 60)]))
+    want, bound = ref.attend(f64(Q)[pick], k, v, table, lens, np.zeros(len(pick), int), pos[pick])
+    bounded(got[pick], want, bound, t.bfloat16, "sampled candidates")
+    assert (got[pos[:, 0] < 0] == 0).all()
+
+
 def test_attend_scale_and_wide_table():
     attend_case(1, [100, 700], 2, 4, 2, 1, 128, mapping="none", scale=0.31, width=50)
     attend_case(2, [100, 700], 2, 4, 2, 1, 64, mapping="none", scale=3.0)
