@@ -25,9 +25,13 @@
 //
 // Two kernels.  In the narrow one a block is one wave with 16 or 32 rows, which converts the codes it
 // reads for itself, registers to registers: with few rows the cache's bytes are what counts, and 8 waves
-// on a CU keep 5 TB/s of them coming.  Every wave repeats the conversion, so with many rows per user and
-// head a block of 8 waves, 32 rows each, converts a page once into LDS (bf16) and each wave reads its
-// operands there.
+// on a CU keep 5 TB/s and more of them coming (0.46 GB of histories, one token each: 79 us, 5.8 TB/s).
+// Every wave repeats the conversion, so with many rows per user and head a block of 8 waves, 32 rows each,
+// converts a page once into LDS (bf16) and each wave reads its operands there.  What bounds it is the sum of
+// its parts, which two waves on a SIMD overlap only in part: of 2.14 us per page of 256 rows at head 128 the
+// matrix instructions take 1.1 (at full rate), the softmax's and the conversion's vector work 1.1, LDS 0.7; around
+// every piece of a unit all blocks read their queries and write their rows at once (9 us).  1024 candidates of
+// 64 rows (121 GFLOP): 186 us, 650 TFLOP/s.
 //
 // How the work is dealt to the blocks, and what joins their partial results: hist_plan.h.
 #include <algorithm>
@@ -930,11 +934,11 @@ hipError_t launch(const AttnArgs &a, int64_t line_most, hipStream_t s) {
 Kv4AttnLayout kv4_attn_layout(int B_u, int B_c, int H_q, int H_kv, int L_q, int head_dim, int max_pages) {
     Kv4AttnLayout w{};
     const int64_t rows = (int64_t)B_c * L_q * (H_q / H_kv);
-    // By the rows of the average user.  32 users of 3000 tokens and 8 heads, in us, narrow against wide:
-    // head 128: 116, 193, 386 against 145, 192, 323 at 128, 256, 512 rows; head 64: 69, 102, 168 against 86, 100,
-    // 140 at 64, 128, 256 rows.
+    // By the rows of the average user.  32 users of 3000 tokens and 8 heads, in us, narrow against wide: head 128:
+    // 106, 143, 181, 320 against 138, 145, 158, 273 at 128, 192, 256, 512 rows; head 64: 80, 104, 129, 220 against
+    // 99, 106, 112, 189.
     const int64_t mean = rows / B_u;
-    w.R = mean <= 16 ? 16 : mean <= (head_dim == 128 ? 256 : 128) ? 32 : 256;
+    w.R = mean <= 16 ? 16 : mean <= 192 ? 32 : 256;
     w.log_blocks = w.R == 256 ? kLogWide : kLogNarrow;
     const int64_t tiles = (rows / w.R + std::min(B_u, B_c)) * H_kv;   // at most
     w.line_most = std::max<int64_t>(1, tiles * max_pages);
