@@ -127,7 +127,9 @@ class RopeFunction(torch.autograd.Function):
 class IkboRope(torch.nn.Module):
     """Rotary positions of q and k [T, H, head_dim] (k may be None), with gradients.
 
-    ``rot_dim``, ``theta`` and ``scaling`` as in ``history.rope_frequencies``; the frequencies are a buffer."""
+    ``rot_dim``, ``theta`` and ``scaling`` as in ``history.rope_frequencies``; the frequencies are a buffer.  Forward
+    and backward may be captured into a graph together, while no eager graph of the same leaves is alive (torch
+    would accumulate their gradients on that one's stream)."""
 
     def __init__(self, head_dim: int, rot_dim: int = 0, theta: float = 10000.0, scaling=None, layout: str = "half"):
         super().__init__()

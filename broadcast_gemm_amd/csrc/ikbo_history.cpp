@@ -138,6 +138,9 @@ int ikbo_kv4_attention(const ikbo_kv4_attention_args *a, void *stream) {
         return IKBO_ERR_ALIGNMENT;
     for (int64_t s : {a->q_cand, a->q_head, a->q_query, a->o_cand, a->o_head, a->o_query})
         if (s % 8 != 0) return IKBO_ERR_ALIGNMENT;
+    if (a->Q == a->O && ((a->B_c > 1 && a->q_cand != a->o_cand) || (a->H_q > 1 && a->q_head != a->o_head) ||
+                         (a->L_q > 1 && a->q_query != a->o_query)))
+        return IKBO_ERR_INVALID_ARG;   // rows would be written before others are read
     const Kv4AttnLayout w = kv4_attn_layout(a->B_u, a->B_c, a->H_q, a->H_kv, a->L_q, a->head_dim, a->max_pages);
     const float scale = a->scale > 0.0f ? a->scale : 1.0f / std::sqrt((float)a->head_dim);
     const hipError_t e = launch_kv4_attention(*a, w, scale, static_cast<hipStream_t>(stream));

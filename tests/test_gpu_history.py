@@ -335,6 +335,34 @@ def test_rope_gradient(layout):
     bounded(f64(gg), back, bound, t.float32, "gradient of the gradient")
 
 
+def test_rope_gradient_replays_in_a_graph():
+    """Forward and backward captured together, with leaves that no eager graph holds; every replay against an eager pass."""
+    t = torch()
+    from broadcast_gemm_amd.autograd import IkboRope
+    rng = np.random.default_rng(26)
+    m = IkboRope(64, 32).cuda()
+    pos = t.zeros(33, dtype=t.int32, device="cuda")
+    q, up = (t.zeros(33, 3, 64, device="cuda") for _ in range(2))
+    q.requires_grad_()
+    graph = t.cuda.CUDAGraph()
+    t.cuda.synchronize()
+    with t.cuda.graph(graph):
+        turned = m(q, None, pos)[0]
+        grad, = t.autograd.grad(turned, q, up)
+    for rep in range(4):
+        eager = dev(rng.standard_normal((33, 3, 64)), t.float32).requires_grad_()
+        with t.no_grad():
+            q.copy_(eager)
+        up.copy_(dev(rng.standard_normal((33, 3, 64)), t.float32))
+        pos.copy_(dev(rng.integers(0, 5000, 33).astype(np.int32)))
+        want = m(eager, None, pos)[0]
+        want_grad, = t.autograd.grad(want, eager, up)
+        t.cuda.synchronize()
+        graph.replay()
+        t.cuda.synchronize()
+        assert t.equal(turned, want) and t.equal(grad, want_grad), rep
+
+
 # ---- the cache: write and read -------------------------------------------------------------
 
 

@@ -132,6 +132,12 @@ def test_attention_refusals(L, change, want):
     assert L.ikbo_kv4_attention(None, None) == INVALID
 
 
+@pytest.mark.parametrize("change", [dict(o_cand=64 * 128), dict(o_head=256), dict(L_q=2, q_query=128, o_query=256)])
+def test_attention_refuses_its_queries_in_another_order(L, change):
+    """O may be Q only with Q's strides: a row written elsewhere would be a query not yet read."""
+    assert call(L.ikbo_kv4_attention, fill(_AttentionArgs, **{**ATTEND, "O": P, "Q": P, **change})) == INVALID
+
+
 def test_attention_workspace(L):
     f = L.ikbo_kv4_attention_workspace
     assert f(15, 15, 4, 4, 1, 128, 16) > 0
