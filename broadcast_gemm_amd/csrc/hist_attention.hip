@@ -414,23 +414,26 @@ struct Pages {
     const int32_t *row;
     const char *tiles;                // head h of page 0
     int64_t stride;                   // bytes from page to page
-    int base, last, num_pages, ids;
+    int user = -1, base, end, last, num_pages, ids;
     bool bad;
     __device__ __forceinline__ void open(const AttnArgs &a, const Piece &c, int tile_bytes) {
-        row = a.table + (int64_t)c.x.u * a.table_stride;
         tiles = a.tiles + (int64_t)c.h * tile_bytes;
         stride = (int64_t)a.H_kv * tile_bytes;
         num_pages = a.num_pages;
         // Entries behind the history may hold anything; an empty one has none.
-        last = min(c.p1, pages_of(c.x.len)) - 1;
+        end = pages_of(c.x.len) - 1;
+        last = min(c.p1 - 1, end);
         bad = false;
+        if (c.x.u == user && c.p0 >= base && c.p0 - base < 64) return;   // a unit of the same user: the numbers are here
+        user = c.x.u;
+        row = a.table + (int64_t)user * a.table_stride;
         base = 0;
         ids = 0;
         if (c.p0 <= last) read(c.p0);
     }
     __device__ __forceinline__ void read(int p) {
         base = p;
-        ids = row[min(p + ((int)threadIdx.x & 63), last)];
+        ids = row[min(p + ((int)threadIdx.x & 63), end)];
     }
     // The tile of page p (of the last page if p is behind it); p never decreases by more than the caller's look-ahead.
     __device__ __forceinline__ global_bytes at(int p) {
@@ -490,12 +493,12 @@ __global__ void __launch_bounds__(64, 2) kv4_attn_kernel(AttnArgs a) {
     int2 note = make_int2(0, 0);
     User user;
     user.to = -1;
+    Pages pages;
     for (int64_t at = edge_of(a, plan, blk); at < end;) {
         const Piece c = piece_at(a, plan, user, at, end, blk);
         if (c.n) note = make_int2(c.n, min(a.R, c.x.n_rows - c.tile * a.R));
         at += c.p1 - c.p0;
-        Pages pages;   // the table's entry is on its way while the queries are found
-        pages.open(a, c, TILE);
+        pages.open(a, c, TILE);   // the table's entries are on their way while the queries are found
         Queries<HD, NT, 16> q;
         // The d order of K and Q: lane group g takes the g-th quarter of a head, one piece of a K row.
         q.find(a, plan, c.x, c.h, c.tile * 16 * NT, j);
@@ -659,11 +662,11 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
     }
     User user;
     user.to = -1;
+    Pages pages;
     for (int64_t at = edge_of(a, plan, blk); at < end;) {
         const Piece c = piece_at(a, plan, user, at, end, blk);
         if (c.n) note = make_int2(c.n, min(a.R, c.x.n_rows - c.tile * a.R));
         at += c.p1 - c.p0;
-        Pages pages;
         pages.open(a, c, TILE);
         Queries<HD, 1, 32> q;
         q.find(a, plan, c.x, c.h, c.tile * ROWS + wv * 32, j);
