@@ -28,10 +28,9 @@
 // on a CU keep 5 TB/s and more of them coming (0.46 GB of histories, one token each: 79 us, 5.8 TB/s).
 // Every wave repeats the conversion, so with many rows per user and head a block of 8 waves, 32 rows each,
 // converts a page once into LDS (bf16) and each wave reads its operands there.  What bounds it is the sum of
-// its parts, which two waves on a SIMD overlap only in part: of 2.14 us per page of 256 rows at head 128 the
-// matrix instructions take 1.1 (at full rate), the softmax's and the conversion's vector work 1.1, LDS 0.7; around
-// every piece of a unit all blocks read their queries and write their rows at once (9 us).  1024 candidates of
-// 64 rows (121 GFLOP): 186 us, 650 TFLOP/s.
+// its parts, which two waves on a SIMD overlap only in part: of 2.14 us per page of 256 rows at head 128 (1.0
+// PFLOP/s) the matrix instructions take 1.1 at full rate, the softmax's and the conversion's vector work 1.1, LDS
+// 0.7; to begin and end a piece of a unit takes 6.6 us.  1024 candidates of 64 rows (121 GFLOP): 184 us, 656 TFLOP/s.
 //
 // How the work is dealt to the blocks, and what joins their partial results: hist_plan.h.
 #include <algorithm>

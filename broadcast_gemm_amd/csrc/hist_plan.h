@@ -8,7 +8,7 @@
 //
 // A run's end that falls within a sixteenth of a run of a unit's edge moves to that edge: a cut costs writing and
 // joining two pieces (260 KB at 256 rows of head 128), a move makes runs uneven, by an eighth at most.  1080 units of
-// 13 to 16 pages in 256 runs, us with the join: 222 where a 512th moves, 215 with a sixteenth, 220 with an eighth.
+// 13 to 16 pages in 256 runs, us with the join: 212 where a 128th moves, 204 with a sixteenth, 209 with an eighth.
 //
 // A block leaves at most two partial results: one of the unit that its run begins inside (slot 2 b),
 // one of a unit that begins in its run and goes on after it (slot 2 b + 1).  So the pieces of a unit
