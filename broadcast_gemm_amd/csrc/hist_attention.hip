@@ -223,6 +223,15 @@ __device__ __forceinline__ f32x16_t mfma_bf16(const u32x4_t &a, const u32x4_t &b
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
 }
 
+// Bytes in device memory, said to the compiler: an address put together from integers is a flat one to it otherwise,
+// and the wait for an LDS read then waits for every such load in flight as well.  ONCE: not to be kept in the caches.
+typedef const __attribute__((address_space(1))) char *global_bytes;
+template <class T, bool ONCE = false>
+__device__ __forceinline__ T load_global(global_bytes p) {
+    const auto x = (const __attribute__((address_space(1))) T *)p;
+    return ONCE ? __builtin_nontemporal_load(x) : *x;
+}
+
 // A wave's query rows, W n + j from `first`, and their softmax: NT tiles of W rows, on the W x W matrix instruction;
 // lane = W g + j.  Of a page's scores a lane holds EACH per query, element e (S[e / ACC][n][e % ACC]) being that of
 // token W/2 (e / 8) + 8 g + e % 8 with W = 32, 16 g + e with W = 16.
@@ -253,7 +262,7 @@ struct Queries {
             plan.row(x, h, live[n] ? r : 0, cnd, l, hq);
             from[n] = a.Q + cnd * a.q_cand + hq * a.q_head + l * a.q_query;
             to[n] = cnd * a.o_cand + hq * a.o_head + l * a.o_query;
-            if (a.positions) pos[n] = a.positions[(int64_t)cnd * a.L_q + l];
+            if (a.positions) pos[n] = load_global<int32_t>((global_bytes)a.positions + 4 * ((int64_t)cnd * a.L_q + l));
         }
     }
     // Step s of a row's elements: lane group g holds the 8 from `base` + s * `step`.
@@ -397,20 +406,11 @@ __device__ __forceinline__ int64_t run_of_block(int blocks) {
     return (blocks & 7) ? blockIdx.x : (int64_t)(blockIdx.x & 7) * (blocks >> 3) + (blockIdx.x >> 3);
 }
 
-// Bytes in device memory, said to the compiler: an address put together from integers is a flat one to it otherwise,
-// and the wait for an LDS read then waits for every such load in flight as well.  ONCE: not to be kept in the caches.
-typedef const __attribute__((address_space(1))) char *global_bytes;
-template <class T, bool ONCE = false>
-__device__ __forceinline__ T load(global_bytes p) {
-    const auto x = (const __attribute__((address_space(1))) T *)p;
-    return ONCE ? __builtin_nontemporal_load(x) : *x;
-}
-
 // The tiles of a run of pages: lane i keeps the page number of page base + i, so that a tile's address
 // needs no load of its own (64 pages at a time; a wait on the table in every turn cost the wide kernel
 // a third of its time).
 struct Pages {
-    const int32_t *row;
+    global_bytes row;
     const char *tiles;                // head h of page 0
     int64_t stride;                   // bytes from page to page
     int user = -1, base, end, last, num_pages, ids;
@@ -425,14 +425,14 @@ struct Pages {
         bad = false;
         if (c.x.u == user && c.p0 >= base && c.p0 - base < 64) return;   // a unit of the same user: the numbers are here
         user = c.x.u;
-        row = a.table + (int64_t)user * a.table_stride;
+        row = (global_bytes)(a.table + (int64_t)user * a.table_stride);
         base = 0;
         ids = 0;
         if (c.p0 <= last) read(c.p0);
     }
     __device__ __forceinline__ void read(int p) {
         base = p;
-        ids = row[min(p + ((int)threadIdx.x & 63), end)];
+        ids = load_global<int32_t>(row + 4 * (int64_t)min(p + ((int)threadIdx.x & 63), end));
     }
     // The tile of page p (of the last page if p is behind it); p never decreases by more than the caller's look-ahead.
     __device__ __forceinline__ global_bytes at(int p) {
@@ -461,23 +461,23 @@ struct PageRegs {
         for (int t = 0; t < 4; ++t) {
             const global_bytes p = tile + (16 * (j >> 2) + 4 * t + (j & 3)) * (HD / 2) + g * (HD / 8);
             if constexpr (HD == 128) {
-                const u32x4_t w = load<u32x4_t, ONCE>(p);
+                const u32x4_t w = load_global<u32x4_t, ONCE>(p);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) k[t][i] = w[i];
             } else {
-                const u32x2_t w = load<u32x2_t, ONCE>(p);
+                const u32x2_t w = load_global<u32x2_t, ONCE>(p);
                 k[t][0] = w[0];
                 k[t][1] = w[1];
             }
         }
-        ks = load<uint32_t, ONCE>(tile + 64 * HD + (HD == 128 ? g : g >> 1) * 64 + 4 * j);
+        ks = load_global<uint32_t, ONCE>(tile + 64 * HD + (HD == 128 ? g : g >> 1) * 64 + 4 * j);
     }
     template <bool ONCE>
     __device__ __forceinline__ void load_v(global_bytes tile, int g, int j) {
 #pragma unroll
         for (int jj = 0; jj < VJ; ++jj) {
-            v[jj] = load<u32x4_t, ONCE>(tile + 32 * HD + (16 * jj + j) * 64 + 16 * g);
-            vs[jj] = load<u32x4_t, ONCE>(tile + 66 * HD + jj * 64 + 16 * g);
+            v[jj] = load_global<u32x4_t, ONCE>(tile + 32 * HD + (16 * jj + j) * 64 + 16 * g);
+            vs[jj] = load_global<u32x4_t, ONCE>(tile + 66 * HD + jj * 64 + 16 * g);
         }
     }
 };
@@ -677,12 +677,12 @@ __global__ void __launch_bounds__(512, 1) kv4_wide_kernel(AttnArgs a) {
 #pragma unroll
             for (int y = 0; y < JOBS; ++y) {
                 if (has_k) {
-                    kc[w][y] = load<u32x2_t>(tile + code_at[y]);
-                    ks[w][y] = load<uint8_t>(tile + ks_at[y]);
+                    kc[w][y] = load_global<u32x2_t>(tile + code_at[y]);
+                    ks[w][y] = load_global<uint8_t>(tile + ks_at[y]);
                 }
                 if (has_v) {
-                    vc[w][y] = load<u32x2_t>(tile + code_at[y] + 32 * HD);
-                    vs[w][y] = load<u32x2_t>(tile + vs_at[y]);
+                    vc[w][y] = load_global<u32x2_t>(tile + code_at[y] + 32 * HD);
+                    vs[w][y] = load_global<u32x2_t>(tile + vs_at[y]);
                 }
             }
         };
