@@ -336,13 +336,16 @@ class UserHistories:
         ``causal`` see tokens up to it only."""
         if positions is None and (causal or self.freq is not None):
             raise ValueError("positions are needed for causal attention and for rotary queries")
+        if stream is not None:   # the copies below are torch's, on its current stream: make that the call's
+            with _on(self.tiles.device, stream):
+                return self.attend(Q, mp, positions=positions, causal=causal, scale=scale, out=out)
         if self.freq is not None:
             q = Q.transpose(1, 2) if Q.dim() == 4 else Q          # [.., heads, head_dim], tokens first
             turned = rope(q.reshape(-1, *q.shape[-2:]), None, positions.reshape(-1), self.freq, layout=self.layout,
-                          factor=self.factor, stream=stream)[0].view(q.shape)
+                          factor=self.factor)[0].view(q.shape)
             Q = turned.transpose(1, 2) if Q.dim() == 4 else turned
         return kv4_attention(Q, self.tiles, self.table, self.lens, mp, self.status, positions=positions if causal else None,
-                             scale=scale, out=out, stream=stream)
+                             scale=scale, out=out)
 
     def check(self, stream=None) -> int:
         """Wait, then return and clear the condition that a step recorded."""

@@ -948,6 +948,37 @@ def test_captured_steps_and_two_graphs_and_streams():
         assert all(t.equal(w, x) for x in o)
 
 
+def test_attend_on_a_given_stream_behind_a_busy_current_one():
+    """Rotary queries of several heads and tokens, and positions that are not contiguous, produced on the stream that the
+    call is given while the current stream is busy: the result is that of a call on one stream alone."""
+    t = torch()
+    h = H()
+    rng = np.random.default_rng(23)
+    hist = h.UserHistories(5, 256, 20, 2, 64, rot_dim=64)
+    k, v = (dev(rng.standard_normal((5 * 150, 2, 64)), t.bfloat16) for _ in range(2))
+    hist.append(k, v, t.full((5,), 150, dtype=t.int32, device="cuda"))
+    mp = dev((np.arange(70) % 5).astype(np.int32))
+    pos = dev(rng.integers(0, 150, (33, 70)).astype(np.int32)).t()
+    qs = [dev(rng.standard_normal((70, 4, 33, 64)), t.bfloat16) for _ in range(6)]
+    wants = [hist.attend(q, mp, positions=pos) for q in qs]
+    big = t.randn(8192, 8192, dtype=t.bfloat16, device="cuda")
+    side = t.cuda.Stream()
+    t.cuda.synchronize()
+    outs = []
+    for stream in (side, side.cuda_stream):
+        for q, want in zip(qs, wants):
+            for _ in range(3):
+                big @ big                     # the current stream is busy
+            with t.cuda.stream(side):
+                mine = q + 0
+                at = pos + 0
+            outs.append((hist.attend(mine, mp, positions=at, stream=stream), want, mine, at))
+            t.full((70 * 33 * 4 * 64,), 7.0, dtype=t.bfloat16, device="cuda")   # takes memory that the current stream has free
+    t.cuda.synchronize()
+    assert all(t.equal(got, want) for got, want, _, _ in outs)
+    assert hist.check() == bga.IKBO_OK
+
+
 def test_cached_attention_agrees_with_dense_target_attention():
     """FaPlan over the dequantised values and the cached attention over the codes compute the same weights and sums."""
     t = torch()

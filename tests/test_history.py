@@ -183,6 +183,50 @@ def test_heads_of_one_tensor_are_told_from_overlap():
     history._distinct("out", qkv.transpose(0, 1))
 
 
+def test_attend_stays_on_the_stream_it_is_given(monkeypatch):
+    """With rotary queries of several heads and tokens, Q has to be copied: the copy, the rotation and the attention all
+    belong on the call's stream.  Told on the CPU by a stand-in for entering that stream."""
+    import contextlib
+
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    on, seen = [], []
+
+    @contextlib.contextmanager
+    def enter(device, stream):
+        on.append(stream)
+        yield 0
+        on.pop()
+
+    class Watch(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            out = func(*args, **(kwargs or {}))
+            if isinstance(out, torch.Tensor) and out.untyped_storage().data_ptr() not in {a.untyped_storage().data_ptr() for a in args if isinstance(a, torch.Tensor)}:
+                seen.append((func.__name__, bool(on)))
+            return out
+
+    def rope(q, k, positions, freq, stream=None, **kw):
+        seen.append(("rope", bool(on) or stream is not None))
+        return q.contiguous(), None
+
+    def attention(Q, *rest, stream=None, **kw):
+        seen.append(("attention", bool(on) or stream is not None))
+        return Q
+
+    monkeypatch.setattr(history, "_on", enter)
+    monkeypatch.setattr(history, "rope", rope)
+    monkeypatch.setattr(history, "kv4_attention", attention)
+    hist = history.UserHistories(3, 64, 3, 2, 64, rot_dim=64, device="cpu")
+    Q = torch.zeros(11, 4, 3, 64, dtype=torch.bfloat16)
+    mp, positions = torch.zeros(11, dtype=torch.int32), torch.zeros(3, 11, dtype=torch.int32).t()
+    with Watch():
+        out = hist.attend(Q, mp, positions=positions, stream="the call's stream")
+    assert out.shape == Q.shape and not on
+    names = [n for n, _ in seen]
+    assert "rope" in names and "attention" in names and len(names) > 2      # the copies were seen
+    assert all(there for _, there in seen), seen
+
+
 # ---- frequencies ---------------------------------------------------------------------------
 
 
