@@ -13,7 +13,7 @@
 // In-place lengths and ring state may only change once every block has read them: a block counts
 // itself in state[2] when it is done, and the last one writes lens_out and state_out and sets the
 // count back to 0 (out of place the first block writes them at once).  The ring's popped and pushed
-// places are disjoint (their sum is at most the ring), and so are the table entries read (the page a
+// places are disjoint (a step whose returned pages and free ones are more than the ring is refused), and so are the table entries read (the page a
 // request's next token falls into) and written (the ones behind it): those are updated where they are.
 //
 // The sums saturate at 2^32 - 1: that is more than any capacity or ring, so a step that reaches it is
@@ -100,7 +100,9 @@ __global__ void __launch_bounds__(kMost) kv_tables_kernel(ikbo_kv_tables_args a)
         err |= werr[w];
     }
     if (all.tok > (uint32_t)a.capacity || all.take > (uint32_t)nfree) err |= kStNoPages;
-    else if ((long long)nfree - all.take + all.give > N) err |= kStPage;
+    // Free pages and those that lengths hold are N at most.  With more (a page returned twice, a length overstated) the
+    // pushed places would reach round the ring into the popped ones.
+    if ((long long)nfree + all.give > N) err |= kStPage;
     if (!err) {   // then no sum has saturated
         Sums run{before.tok + inc.tok - mine.tok, before.take + inc.take - mine.take, before.give + inc.give - mine.give};
 #pragma unroll

@@ -293,8 +293,8 @@ int ikbo_kv_status(uint32_t *status, void *stream);
  * (0 for a leaving request); lens_out may be lens or counts, and state_out may be state (updated in
  * place: one step after the other, also on replays of a captured graph).  No other buffers overlap.
  * A step that does not fit (free pages, table columns or capacity: IKBO_ERR_NO_PAGES; a
- * negative or overlong length, a count below -1, a ring state out of range:
- * IKBO_ERR_PAGE_RANGE) is refused as a whole: slots, positions and rows become -1, starts 0,
+ * negative or overlong length, a count below -1, a ring state out of range, more free and
+ * returned pages than num_pages: IKBO_ERR_PAGE_RANGE) is refused as a whole: slots, positions and rows become -1, starts 0,
  * lens_out = lens, state_out = state, and the table and the ring keep their contents.  A page
  * number outside [0, num_pages) that the table or the ring holds is recorded as PAGE_RANGE and
  * gives slot -1.

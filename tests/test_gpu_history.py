@@ -135,6 +135,25 @@ def test_tables_refuse_a_step_as_a_whole(what, status):
     assert state.tolist() == [head, free, 0, 0]
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("counts, lens, free, N", [
+    ([-1, 1], [64, 0], 4, 4),                    # a page returned though all are free: its place is the one that is taken
+    ([-1, 64], [65, 0], 3, 4), ([-1, 64, 64], [192, 0, 0], 2, 4), ([-1] * 700 + [64] * 700, [64] * 700 + [0] * 700, 1300, 1999)])
+def test_tables_refuse_more_free_pages_than_the_ring(counts, lens, free, N, in_place):
+    """Returned pages that would reach round the ring into the places of the taken ones, whatever the step leaves free."""
+    counts, lens = np.array(counts, np.int32), np.array(lens, np.int32)
+    need = (-(-(lens + np.maximum(counts, 0)) // 64) - -(-lens // 64))[counts >= 0].sum()
+    give = (-(-lens // 64))[counts < 0].sum()
+    assert need <= free and free - need + give <= N < free + give
+    table, ring = np.full((len(lens), 3), 1, np.int32), np.arange(N, dtype=np.int32)
+    got, d, state, st = run_tables((counts, lens, table, ring, 1, free), 64 * len(lens), 64, in_place)
+    assert st == bga.IKBO_ERR_PAGE_RANGE
+    assert (got.slots == -1).all() and (got.rows == -1).all() and (got.starts == 0).all()
+    assert np.array_equal(got.lens.cpu().numpy(), lens) and got.state.tolist()[:2] == [1, free]
+    for x, y in zip(d, (counts, lens, table, ring)):
+        assert np.array_equal(x.cpu().numpy(), y)
+
+
 def test_tables_bad_page_numbers_give_no_slot():
     t = torch()
     step = (np.array([3, 3], np.int32), np.array([10, 64], np.int32), np.array([[77, -1], [1, -1]], np.int32), np.array([0, 99, 2, 3], np.int32), 1, 2)
