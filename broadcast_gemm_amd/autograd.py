@@ -127,15 +127,23 @@ class RopeFunction(torch.autograd.Function):
 class IkboRope(torch.nn.Module):
     """Rotary positions of q and k [T, H, head_dim] (k may be None), with gradients.
 
-    ``rot_dim``, ``theta`` and ``scaling`` as in ``history.rope_frequencies``; the frequencies are a buffer.  Forward
-    and backward may be captured into a graph together, while no eager graph of the same leaves is alive (torch
-    would accumulate their gradients on that one's stream)."""
+    ``rot_dim``, ``theta`` and ``scaling`` as in ``history.rope_frequencies``; the frequencies are a buffer that casts of
+    the module (``bfloat16()``, ``to(dtype)``) leave in float64.  Forward and backward may be captured into a graph
+    together, while no eager graph of the same leaves is alive (torch would accumulate their gradients on that one's
+    stream)."""
 
     def __init__(self, head_dim: int, rot_dim: int = 0, theta: float = 10000.0, scaling=None, layout: str = "half"):
         super().__init__()
         self.layout = layout
         freq, self.factor = history.rope_frequencies(rot_dim or head_dim, theta, scaling, device="cpu")
         self.register_buffer("freq", freq, persistent=False)
+
+    def _apply(self, fn, *args, **kwargs):
+        freq = self.freq
+        super()._apply(fn, *args, **kwargs)
+        if self.freq.dtype != freq.dtype:   # moved and rounded: only the move is kept
+            self.freq = freq.to(self.freq.device)
+        return self
 
     def forward(self, q, k, positions):
         return RopeFunction.apply(q, k, positions, self.freq, self.layout, self.factor)

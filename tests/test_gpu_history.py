@@ -354,6 +354,18 @@ def test_rope_gradient(layout):
     bounded(f64(gg), back, bound, t.float32, "gradient of the gradient")
 
 
+def test_rope_module_after_casts():
+    """A cast of the module, before or after it moves to the GPU, changes no rotation."""
+    t = torch()
+    from broadcast_gemm_amd.autograd import IkboRope
+    rng = np.random.default_rng(27)
+    q = dev(rng.standard_normal((9, 3, 64)), t.bfloat16)
+    pos = dev(rng.integers(0, 10 ** 6, 9).astype(np.int32))
+    want = IkboRope(64, 32).cuda()(q, None, pos)[0]
+    for m in (IkboRope(64, 32).bfloat16().cuda(), IkboRope(64, 32).cuda().half(), IkboRope(64, 32).to("cuda", t.bfloat16).float()):
+        assert t.equal(m(q, None, pos)[0], want)
+
+
 def test_rope_gradient_replays_in_a_graph():
     """Forward and backward captured together, with leaves that no eager graph holds; every replay against an eager pass."""
     t = torch()

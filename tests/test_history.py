@@ -267,6 +267,29 @@ def test_frequencies_refusals(rot, scaling):
         history.rope_frequencies(rot, 1e4, scaling, device="cpu")
 
 
+@pytest.mark.parametrize("cast", ["bfloat16", "half", "float", "double", "to", "type", "meta"])
+def test_rope_frequencies_survive_casts_of_their_module(cast):
+    """A model that holds IkboRope is cast as any other: its parameters change, the frequencies stay float64 to the bit."""
+    from broadcast_gemm_amd.autograd import IkboRope
+    want, _ = history.rope_frequencies(64, 500.0, device="cpu")
+    rope = IkboRope(64, theta=500.0)
+    model = torch.nn.Sequential(torch.nn.Linear(2, 2), rope)
+    if cast == "to":
+        model.to(torch.bfloat16)
+    elif cast == "type":
+        model.type(torch.float16)
+    elif cast == "meta":
+        model.to("meta", torch.bfloat16)
+        assert rope.freq.dtype == torch.float64 and rope.freq.device.type == "meta" and model[0].weight.dtype == torch.bfloat16
+        return
+    else:
+        getattr(model, cast)()
+    assert model[0].weight.dtype == {"float": torch.float32, "double": torch.float64, "half": torch.float16, "type": torch.float16}.get(cast, torch.bfloat16)
+    model.double()
+    assert rope.freq.dtype == torch.float64 and torch.equal(rope.freq, want)
+    assert dict(rope.named_buffers())["freq"] is rope.freq and not rope.state_dict()
+
+
 # ---- the plain forms -----------------------------------------------------------------------
 
 
