@@ -227,22 +227,41 @@ def _rope_out(q, k, q_out, k_out) -> None:
 
 
 def _meet(a, b) -> bool:
-    """Whether elements of two tensors [T, H, dim] may share memory (different heads of one tensor do not)."""
+    """Whether two tensors may share memory (different heads, rows or columns of one tensor do not)."""
     x, y = _spans(a), _spans(b)
     return x[0] <= y[1] and y[0] <= x[1] and not _interleaved(a, b)
 
 
 def _interleaved(a, b) -> bool:
-    """Whether two tensors [T, H, dim] are different heads of one tensor: same token stride, and the heads of a token
-    lie within it without meeting."""
-    st = a.stride(0)
-    if b.stride(0) != st or a.shape[0] <= 1 or st <= 0:
-        return False
-    size = a.element_size()
-    lo, hi = (a, b) if a.data_ptr() <= b.data_ptr() else (b, a)
-    within = [(t.shape[1] - 1) * t.stride(1) + t.shape[2] for t in (lo, hi)]
-    gap = hi.data_ptr() - lo.data_ptr()
-    return gap % size == 0 and within[0] <= gap // size and gap // size + within[1] <= st
+    """Whether two tensors share no element although their spans may cross.
+
+    Looks for places i in a and j in b with gap + sum_k j_k t_k - sum_k i_k s_k = 0, in bytes, the largest strides first
+    and only where the rest can still get there: strides that nest, as those of tensors do, leave two choices each."""
+    steps = {}
+    for t, sign in ((a, -1), (b, 1)):
+        for n, stride in zip(t.shape, t.stride()):
+            if n > 1 and stride:
+                lo, hi = steps.get(stride * t.element_size(), (0, 0))
+                steps[stride * t.element_size()] = (lo - (n - 1), hi) if sign < 0 else (lo, hi + n - 1)
+    steps = [(s, *steps[s]) for s in sorted(steps, reverse=True)]
+    least, most = [0], [0]                                   # what the smaller strides can add
+    for s, lo, hi in reversed(steps):
+        least.append(least[-1] + lo * s)
+        most.append(most[-1] + hi * s)
+    below, above = -b.element_size(), a.element_size()       # elements meet if their distance lies between
+    left = 10000                                             # strides that do not nest: give up, they may meet
+
+    def reach(k, at):
+        nonlocal left
+        left -= 1
+        if k == len(steps) or left < 0:
+            return left < 0 or below < at < above
+        s, lo, hi = steps[k]
+        lo = max(lo, -((at + most[-2 - k] - below - 1) // s))
+        hi = min(hi, (above - 1 - at - least[-2 - k]) // s)
+        return any(reach(k + 1, at + d * s) for d in range(lo, hi + 1))
+
+    return not reach(0, b.data_ptr() - a.data_ptr())
 
 
 def kv4_write(k, v, slots, tiles, status, stream=None) -> None:
@@ -272,9 +291,12 @@ def kv4_attention(Q, tiles, block_table, lens, mp, status, positions=None, scale
     Q [B_c, H_q, L_q, head_dim] bf16 (or [B_c, H_q, head_dim]: one query each), any strides that are multiples of 8;
     ``mp`` [B_c] int32, or None where candidate b belongs to user b; -1 entries are padding.  ``positions`` [B_c, L_q]
     (or [B_c]) int32 limits each query to tokens up to its position.  O has Q's shape; the rows of padding are left as
-    they were (unspecified without ``out``).  ``out`` may be Q."""
+    they were (unspecified without ``out``).  ``out`` may be Q, or else must not overlap it."""
     if out is not None:
         _distinct("out", out)
+        same = out.data_ptr() == Q.data_ptr() and out.shape == Q.shape and all(x == y or n == 1 for x, y, n in zip(out.stride(), Q.stride(), Q.shape))
+        if not same and _meet(out, Q):
+            raise ValueError("out overlaps Q")
     return _status_of(_run(_device(Q), stream, _binding().kv4_attention, Q, tiles, block_table, lens, mp, status, positions, scale, out),
                       "ikbo_kv4_attention")
 

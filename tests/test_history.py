@@ -183,6 +183,51 @@ def test_heads_of_one_tensor_are_told_from_overlap():
     history._distinct("out", qkv.transpose(0, 1))
 
 
+def test_attention_refuses_an_output_that_meets_its_queries():
+    """O may be Q or stand apart from it, also within one tensor; rows of O over other rows of Q are refused."""
+    i, st = torch.zeros(4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    tiles, table = torch.zeros(3, 2, 68 * 64, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.int32)
+    buf = torch.zeros(5, 8, 6, 64, dtype=torch.bfloat16)
+    flat = torch.zeros(5 * 8 * 6 * 64 + 8, dtype=torch.bfloat16)
+    wide = torch.zeros(4, 2, 4 * 3 * 64, dtype=torch.bfloat16)
+
+    def attend(Q, out):
+        history.kv4_attention(Q, tiles, table, i, None, st, out=out)
+
+    q = buf[:4, :4, :3]
+    for out in (buf[1:, :4, :3], buf[:4, 2:6, :3], buf[:4, :4, 2:5], buf[:4, 1:5, 1:4], buf[1:, 3:7, 2:5]):
+        with pytest.raises(ValueError, match="overlap"):
+            attend(q, out)
+    with pytest.raises(ValueError, match="overlap"):
+        attend(flat[:4 * 768].view(4, 4, 3, 64), flat[8:8 + 4 * 768].view(4, 4, 3, 64))
+    with pytest.raises(ValueError, match="overlap"):
+        attend(wide[:, 0].view(4, 4, 3, 64), wide[:, 0].view(4, 3, 4, 64).transpose(1, 2))
+    # What stands apart gets as far as the check of the device.
+    for a, out in ((q, q), (q, buf[:4, 4:, :3]), (q, buf[:4, :4, 3:]), (buf[:4, 4:, 3:], q), (q, buf[:4, 4:, 2:5]), (q, q.clone()),
+                   (wide[:, 0].view(4, 4, 3, 64), wide[:, 1].view(4, 3, 4, 64).transpose(1, 2)), (q[:1], q[:1].as_strided((1, 4, 3, 64), (8, 384, 64, 1)))):
+        with pytest.raises(ValueError, match="GPU"):
+            attend(a, out)
+
+
+def test_meeting_tensors_against_their_elements():
+    """_meet against the sets of elements: exact, whatever the strides are."""
+    rng = np.random.default_rng(4)
+    flat = torch.zeros(4000)
+    crossed = 0
+    for _ in range(3000):
+        shapes = rng.integers(1, 5, (2, 3))
+        strides = np.cumprod(rng.integers(1, 6, 3))[::-1].copy()
+        other = strides if rng.random() < 0.6 else rng.integers(0, 30, 3)
+        ta = flat.as_strided(tuple(map(int, shapes[0])), tuple(map(int, strides)), int(rng.integers(0, 200)))
+        tb = flat.as_strided(tuple(map(int, shapes[1])), tuple(map(int, other)), int(rng.integers(0, 200)))
+        at = [set((x.storage_offset() + sum(np.indices(x.shape)[d] * x.stride(d) for d in range(3))).ravel().tolist()) for x in (ta, tb)]
+        meet = bool(at[0] & at[1])
+        assert history._meet(ta, tb) == history._meet(tb, ta)
+        assert history._meet(ta, tb) == meet
+        crossed += not meet and history._spans(ta)[0] < history._spans(tb)[1] and history._spans(tb)[0] < history._spans(ta)[1]
+    assert crossed > 200
+
+
 def test_attend_stays_on_the_stream_it_is_given(monkeypatch):
     """With rotary queries of several heads and tokens, Q has to be copied: the copy, the rotation and the attention all
     belong on the call's stream.  Told on the CPU by a stand-in for entering that stream."""
