@@ -1,5 +1,6 @@
 """Build libikbo.so (HIP C++ for gfx950) in-tree with hipcc, and _ikbo_torch.so, the host-side binding
-of the cached user histories to torch tensors, with the host compiler.
+of the cached user histories to torch tensors, with the host compiler.  The library does not need torch: where torch
+cannot be imported, it is built alone.
 
     python -m broadcast_gemm_amd.build
 """
@@ -45,7 +46,7 @@ def torch_command(out: str) -> list:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP/C++ source and link libikbo.so (always rebuilds)."""
+    """Compile every HIP/C++ source and link libikbo.so, then the torch binding if torch is there (always rebuilds)."""
     out_dir = os.path.join(ROOT, "_build")
     os.makedirs(out_dir, exist_ok=True)
     common = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", os.path.join(ROOT, "include"),
@@ -60,10 +61,14 @@ def build(verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         jobs.append((src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
     torch_tmp = TORCH_LIB + ".tmp"
-    cmd = torch_command(torch_tmp)
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    torch_proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+    torch_proc = trouble = None   # the library is linked before any trouble with the binding is raised
+    try:
+        cmd = torch_command(torch_tmp)
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        torch_proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+    except Exception as e:
+        trouble = e
     objs = []
     for src, obj, proc in jobs:
         _, err = proc.communicate()
@@ -73,16 +78,21 @@ def build(verbose: bool = False) -> str:
         if verbose and msgs.strip():
             print(msgs)
         objs.append(obj)
-    _, err = torch_proc.communicate()
-    if torch_proc.returncode != 0:
-        raise RuntimeError(f"the host compiler failed on torch_history.cpp:\n{err}")
-    os.replace(torch_tmp, TORCH_LIB)
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp] + objs
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    if isinstance(trouble, ImportError):
+        print(f"torch cannot be imported ({trouble}): {os.path.basename(TORCH_LIB)} is not built", file=sys.stderr)
+        return LIB
+    if trouble is not None:
+        raise trouble
+    _, err = torch_proc.communicate()
+    if torch_proc.returncode != 0:
+        raise RuntimeError(f"the host compiler failed on torch_history.cpp:\n{err}")
+    os.replace(torch_tmp, TORCH_LIB)
     return LIB
 
 

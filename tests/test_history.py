@@ -145,6 +145,36 @@ def test_attention_workspace(L):
     assert f(15, 15, 4, 4, 1, 80, 16) == UNSUPPORTED
 
 
+def test_library_is_built_where_its_torch_binding_cannot_be(tmp_path, monkeypatch, capsys):
+    """The C ABI needs hipcc alone: without torch it is built and said to be alone, and a host compiler that fails is an
+    error that leaves the library linked."""
+    import sys
+
+    from broadcast_gemm_amd import build
+    try:
+        build.hipcc()
+    except RuntimeError:
+        pytest.skip("no hipcc")
+    (tmp_path / "one.cpp").write_text('extern "C" int one() { return 1; }\n')
+    monkeypatch.setattr(build, "ROOT", str(tmp_path))
+    monkeypatch.setattr(build, "CSRC", str(tmp_path))
+    monkeypatch.setattr(build, "SOURCES", ["one.cpp"])
+    monkeypatch.setattr(build, "TORCH_LIB", str(tmp_path / "_ikbo_torch.so"))
+    for name, fails in (("a.so", False), ("b.so", True)):
+        monkeypatch.setattr(build, "LIB", str(tmp_path / name))
+        with monkeypatch.context() as m:
+            if fails:
+                m.setattr(build, "torch_command", lambda out: [sys.executable, "-c", "import sys; sys.exit('no headers')"])
+                with pytest.raises(RuntimeError, match="no headers"):
+                    build.build()
+            else:
+                m.setitem(sys.modules, "torch", None)
+                assert build.build() == str(tmp_path / name)
+                assert "torch" in capsys.readouterr().err
+        assert ctypes.CDLL(str(tmp_path / name)).one() == 1
+        assert not (tmp_path / "_ikbo_torch.so").exists()
+
+
 def test_status_word_refusal(L):
     assert L.ikbo_kv_status(None, None) == INVALID
     for code in (bga.IKBO_ERR_PAGE_RANGE, bga.IKBO_ERR_NO_PAGES, bga.IKBO_ERR_NONFINITE):
