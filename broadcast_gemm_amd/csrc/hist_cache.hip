@@ -303,22 +303,43 @@ hipError_t launch_write(const ikbo_kv4_rows_args &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <int HD, bool F32>
+hipError_t launch_read(const ikbo_kv4_rows_args &a, hipStream_t s) {
+    const int64_t threads = ((int64_t)a.T + 3) / 4 * (HD / 2);
+    const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), (unsigned)a.H_kv);
+    hipLaunchKernelGGL((kv4_read_kernel<HD, F32>), grid, dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+// A launch counts its threads in 32 bits (more are dropped without an error): 2^27 rows at a time are 2^31 of the read.
+template <class Launch>
+hipError_t by_parts(const ikbo_kv4_rows_args &a, hipStream_t s, Launch launch) {
+    constexpr int64_t kMost = 1ll << 27;
+    const int size = a.dtype == IKBO_DTYPE_F32 ? 4 : 2;
+    for (int64_t r = 0; r < a.T; r += kMost) {
+        ikbo_kv4_rows_args part = a;
+        part.T = (int)(a.T - r < kMost ? a.T - r : kMost);
+        part.slots += r;
+        part.k = beyond(a.k, r * a.k_token, size);
+        part.v = beyond(a.v, r * a.v_token, size);
+        const hipError_t e = launch(part, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 }  // namespace
 
 hipError_t launch_kv4_write(const ikbo_kv4_rows_args &a, hipStream_t s) {
     const bool f = a.dtype == IKBO_DTYPE_F32;
-    if (a.head_dim == 128) return f ? launch_write<128, true>(a, s) : launch_write<128, false>(a, s);
-    return f ? launch_write<64, true>(a, s) : launch_write<64, false>(a, s);
+    if (a.head_dim == 128) return by_parts(a, s, f ? launch_write<128, true> : launch_write<128, false>);
+    return by_parts(a, s, f ? launch_write<64, true> : launch_write<64, false>);
 }
 
 hipError_t launch_kv4_read(const ikbo_kv4_rows_args &a, hipStream_t s) {
-    const int64_t threads = ((int64_t)a.T + 3) / 4 * (a.head_dim / 2);
-    const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), (unsigned)a.H_kv);
-    auto go = [&](auto k) { hipLaunchKernelGGL(k, grid, dim3(kThreads), 0, s, a); };
     const bool f = a.dtype == IKBO_DTYPE_F32;
-    if (a.head_dim == 128) f ? go(kv4_read_kernel<128, true>) : go(kv4_read_kernel<128, false>);
-    else f ? go(kv4_read_kernel<64, true>) : go(kv4_read_kernel<64, false>);
-    return hipGetLastError();
+    if (a.head_dim == 128) return by_parts(a, s, f ? launch_read<128, true> : launch_read<128, false>);
+    return by_parts(a, s, f ? launch_read<64, true> : launch_read<64, false>);
 }
 
 }  // namespace ikbo

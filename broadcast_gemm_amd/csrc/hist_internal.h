@@ -15,6 +15,12 @@ int hip_fail(hipError_t e, const char *what);
 // Record `what` for ikbo_last_error_message; returns status.
 int status_fail(int status, const char *what);
 
+// Element `at` of a tensor of the given element size; NULL stays NULL.
+template <class T>
+T *beyond(T *p, int64_t at, int size) {
+    return p ? reinterpret_cast<T *>(reinterpret_cast<uintptr_t>(p) + (uintptr_t)(at * size)) : p;
+}
+
 // Bits of the caller's status word.
 constexpr uint32_t kStMap = 1u, kStPage = 2u, kStNoPages = 4u, kStNonfinite = 8u;
 

@@ -150,10 +150,23 @@ hipError_t launch(const ikbo_rope_args &a, hipStream_t s) {
     // sines then fill the block's threads.
     const int half = a.rot_dim / 2;
     int tpb = std::max(1, std::min(kThreads / half, a.T / 2048));
-    const long long blocks = ((long long)a.T + tpb - 1) / tpb;
-    hipLaunchKernelGGL((rope_kernel<F32, VEC, HALF>), dim3((unsigned)blocks), dim3(kThreads),
-                       (size_t)tpb * half * sizeof(float2), s, a, tpb);
-    return hipGetLastError();
+    // A launch counts its threads in 32 bits (more are dropped without an error): 2^23 blocks at a time.
+    const long long most = (1ll << 23) * tpb;
+    for (long long t = 0; t < a.T; t += most) {
+        ikbo_rope_args part = a;
+        constexpr int SIZE = F32 ? 4 : 2;
+        part.T = (int)std::min(most, a.T - t);
+        part.positions += t;
+        part.q = beyond(a.q, t * a.q_token, SIZE);
+        part.k = beyond(a.k, t * a.k_token, SIZE);
+        part.q_out = beyond(a.q_out, t * a.q_out_token, SIZE);
+        part.k_out = beyond(a.k_out, t * a.k_out_token, SIZE);
+        hipLaunchKernelGGL((rope_kernel<F32, VEC, HALF>), dim3((unsigned)((part.T + (long long)tpb - 1) / tpb)), dim3(kThreads),
+                           (size_t)tpb * half * sizeof(float2), s, part, tpb);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 template <bool F32, bool HALF>

@@ -394,6 +394,24 @@ def test_rope_gradient_replays_in_a_graph():
         assert t.equal(turned, want) and t.equal(grad, want_grad), rep
 
 
+def test_rope_more_tokens_than_one_launch_counts():
+    """2^24 tokens and a few, heads that leave one token to a block: over 2^32 threads."""
+    t = torch()
+    T = (1 << 24) + 5
+    log(f"rope T={T}")
+    x = t.linspace(-2, 2, 258, device="cuda").to(t.bfloat16).view(1, 1, 258)
+    pos = t.zeros(T, dtype=t.int32, device="cuda")
+    pos[0], pos[-3], pos[-1] = 1, 2, 3
+    freq = H().rope_frequencies(258)[0]
+    out = t.zeros(T, 1, 258, dtype=t.bfloat16, device="cuda")
+    H().rope(x.expand(T, 1, 258), None, pos, freq, out=(out, None))
+    turned = H().rope(x.expand(4, 1, 258), None, t.arange(4, dtype=t.int32, device="cuda"), freq)[0]
+    assert t.equal(turned[0], x[0])
+    assert t.equal(out[0], turned[1]) and t.equal(out[-3], turned[2]) and t.equal(out[-1], turned[3])
+    out[0] = out[-3] = out[-1] = x[0]
+    assert all(bool((part == x).all()) for part in out.split(1 << 21))
+
+
 # ---- the cache: write and read -------------------------------------------------------------
 
 
@@ -527,6 +545,35 @@ def test_rows_refusals():
         h.kv4_read(slots, tiles[..., :-1], st)
     h.kv4_write(k[:0], k[:0], slots[:0], tiles, st)
     assert h.kv4_read(slots[:0], tiles, st)[0].shape == (0, 2, 64) and not tiles.any()
+
+
+@pytest.mark.parametrize("T, op", [((1 << 30) + 70, "write"), ((1 << 29) + 70, "read")])
+def test_more_rows_than_one_launch_counts(T, op):
+    """Rows whose launch would have over 2^32 threads, all padding but a few at both ends, each the same row in memory
+    (strides of 0; a read's rows hold equal values)."""
+    import ctypes
+    from test_history import _RowsArgs, fill
+    t = torch()
+    log(f"{op} T={T}")
+    slots = t.full((T,), -1, dtype=t.int32, device="cuda")
+    first = t.tensor([5, 6, 7, 8, 9], dtype=t.int32, device="cuda")
+    slots[:5], slots[-3:] = first, t.tensor([70, 71, 3], dtype=t.int32, device="cuda")
+    kv = t.linspace(-6, 6, 128, device="cuda").view(2, 1, 1, 64)
+    tiles, st = cache(2, 1, 64), word()
+    few = t.cat([first, slots[-3:]])
+    H().kv4_write(*(x.expand(8, 1, 64) for x in kv), few, tiles, st)
+    want_k, want_v = H().kv4_read(few, tiles, st, dtype=t.float32)
+    got_tiles = tiles if op == "read" else t.zeros_like(tiles)
+    rows = t.zeros_like(kv) if op == "read" else kv
+    if op == "read":                      # the last row alone decides what is left
+        slots[:5] = -1
+    args = fill(_RowsArgs, k=rows[0].data_ptr(), v=rows[1].data_ptr(), slots=slots.data_ptr(), tiles=got_tiles.data_ptr(), status=st.data_ptr(),
+                k_token=0, k_head=64, v_token=0, v_head=64, T=T, H_kv=1, head_dim=64, num_pages=2, dtype=1)
+    t.cuda.synchronize()
+    assert getattr(bga.lib(), "ikbo_kv4_" + op)(ctypes.byref(args), None) == bga.IKBO_OK
+    assert H().kv_status(st) == bga.IKBO_OK
+    assert t.equal(got_tiles, tiles)
+    assert t.equal(rows[0, 0], want_k[0] if op == "read" else kv[0, 0]) and t.equal(rows[1, 0], want_v[0] if op == "read" else kv[1, 0])
 
 
 def test_slots_past_32_bits_of_bytes():
