@@ -7,6 +7,8 @@
 // strides raise ValueError; a status that the library returns comes back as an int.
 #include <torch/extension.h>
 
+#include <cfloat>
+
 #include "ikbo.h"
 
 namespace {
@@ -262,6 +264,7 @@ py::object kv4_attention(uintptr_t stream, const Tensor &Q, const Tensor &tiles,
     a.max_pages = size32("the block table", table.size(1));
     a.num_pages = size32("tiles", tiles.size(0));
     a.scale = (float)scale;
+    if (scale > 0 && a.scale < FLT_MIN) a.scale = FLT_MIN;   // not 0, which is the default; the scores are 0 to float32 either way
     a.workspace_bytes = ik.workspace(a.B_u, a.B_c, a.H_q, a.H_kv, a.L_q, a.head_dim, a.max_pages);
     if (a.workspace_bytes < 0) return status_of((int)a.workspace_bytes);
     const Tensor O = given ? *given : at::empty(Q.sizes(), Q.options());

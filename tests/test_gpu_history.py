@@ -750,6 +750,12 @@ def test_attend_scale_and_wide_table():
     attend_case(2, [100, 700], 2, 4, 2, 1, 64, mapping="none", scale=3.0)
 
 
+@pytest.mark.parametrize("scale", [1e-38, 1e-42, 1e-50, 5e-324])
+def test_attend_scales_below_float32(scale):
+    """A positive scale too small for float32 is no scale of 0, which means the default: all weights are equal."""
+    attend_case(91, [150, 64], 6, 2, 1, 1, 64, mapping="random", scale=scale)
+
+
 def test_attend_layouts_padding_and_untouched_rows():
     """Q and O as views of token-major buffers; padding candidates and everything around O keep their bytes."""
     t = torch()
