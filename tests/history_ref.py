@@ -55,6 +55,21 @@ def put(tiles, k, v, slots):
             w[66 * dim:].reshape(dim // 32, 64)[:, t] = vs[h]
 
 
+def put_all(tiles, k, v, slots):
+    """``put`` for distinct slots, all rows at once."""
+    n, H, size = tiles.shape
+    dim = size // 68
+    live = slots >= 0
+    page, t = np.divmod(slots[live].astype(int), PAGE)
+    for x, codes, scales, place in ((k, tiles[..., :32 * dim].reshape(n, H, 64, dim // 2).swapaxes(2, 3), tiles[..., 64 * dim:66 * dim], scale_place(t)),
+                                    (v, tiles[..., 32 * dim:64 * dim].reshape(n, H, dim // 2, 64), tiles[..., 66 * dim:], t)):
+        scales = scales.reshape(n, H, dim // 32, 64)
+        assert np.shares_memory(codes, tiles) and np.shares_memory(scales, tiles)
+        c, s = encode(x[live])
+        codes[page, :, :, t] = c[..., 0::2] | (c[..., 1::2] << 4)
+        scales[page, :, :, place] = s
+
+
 def rows_of(tiles):
     """K and V values [pages, H, 64, dim] float64 that tiles hold."""
     n, H, size = tiles.shape

@@ -459,6 +459,47 @@ def test_write_and_read(T, heads, dim, order, dtype):
     check_write(kv[0], kv[1], slots, pages, heads, dim)
 
 
+@pytest.mark.parametrize("T, heads, dim, order", [
+    (4032, 8, 128, "offset"),      # 504 blocks of 64 rows: the last step that takes 16 rows a block
+    (4033, 8, 128, "offset"), (4033, 8, 64, "run"), (4160, 8, 128, "run"), (4103, 8, 64, "offset"), (4103, 8, 128, "random"), (4103, 8, 64, "random"),
+    (4219, 8, 128, "runs"), (4219, 8, 64, "runs"), (4103, 8, 128, "reverse"), (4103, 8, 64, "reverse"), (1, 512, 64, "run"), (70, 257, 128, "offset")])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_write_and_read_blocks_of_64_rows(T, heads, dim, order, dtype):
+    """Steps of many rows, on both sides of the rule that takes 64 rows to a block: whole runs, runs that start and end
+    inside a page and inside a block, and rows without neighbours; every byte, then the values read back."""
+    t = torch()
+    rng = np.random.default_rng(T + dim)
+    pages = T // 64 + 3
+    x = dev(rng.standard_normal((2, T, heads, dim)) * np.exp(2 * rng.standard_normal((2, T, heads, 1))), getattr(t, dtype))
+    slots = {"run": np.arange(T), "offset": np.arange(T) + 37, "reverse": np.arange(T)[::-1] + 5, "random": rng.permutation(pages * 64)[:T],
+             "runs": None}[order]
+    if order == "runs":            # pieces of 1 to 40 slots in random order
+        cuts = np.cumsum(rng.integers(1, 41, pages * 64))
+        pieces = np.split(np.arange(pages * 64), cuts[cuts < pages * 64])
+        slots = np.concatenate([pieces[i] for i in rng.permutation(len(pieces))])[:T]
+    slots = slots.astype(np.int32)
+    if T > 20:
+        slots[[3, 17, T // 2, T - 1]] = -1
+    log(f"write in blocks of 64: T={T} heads={heads} dim={dim} {order} {dtype}")
+    tiles, st = cache(pages, heads, dim, 0x5A), word()
+    want = tiles.cpu().numpy()
+    d_slots = dev(slots)
+    H().kv4_write(x[0], x[1], d_slots, tiles, st)
+    ref.put_all(want, f64(x[0]), f64(x[1]), slots)
+    assert H().kv_status(st) == bga.IKBO_OK
+    got = tiles.cpu().numpy()
+    assert np.array_equal(got, want), f"{(got != want).sum()} bytes differ"
+    live = slots >= 0
+    values = ref.rows_of(want)
+    for dt in (t.bfloat16, t.float32):
+        out = tuple(t.full((T, heads, dim), 9.0, dtype=dt, device="cuda") for _ in range(2))
+        H().kv4_read(d_slots, tiles, st, out=out)
+        for o, y in zip(out, values):
+            o = f64(o)
+            assert np.array_equal(o[live], y[slots[live] // 64, :, slots[live] % 64]) and (o[~live] == 9).all()
+    assert H().kv_status(st) == bga.IKBO_OK
+
+
 def test_write_strided_rows():
     t = torch()
     rng = np.random.default_rng(8)

@@ -9,7 +9,7 @@ import torch
 
 import broadcast_gemm_amd as bga
 from broadcast_gemm_amd import history
-from history_ref import LEVELS, decode, encode, tables, turn
+from history_ref import LEVELS, decode, encode, put, put_all, rows_of, tables, turn
 
 
 # The structures of the C ABI.
@@ -383,6 +383,21 @@ def test_plain_codes():
     top = np.abs(y.reshape(50, 2, 32)).max(-1, keepdims=True)
     assert (np.abs(z - y).reshape(50, 2, 32) <= top / 3 * 1.0000001).all()
     assert len(LEVELS) == 8
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_plain_rows_at_once(dim):
+    rng = np.random.default_rng(2)
+    k, v = rng.standard_normal((2, 150, 3, dim)) * np.exp(rng.standard_normal((2, 150, 3, 1)))
+    slots = rng.permutation(256)[:150].astype(np.int32)
+    slots[[4, 90]] = -1
+    one, all_ = (np.full((4, 3, 68 * dim), 0x5A, np.uint8) for _ in range(2))
+    put(one, k, v, slots)
+    put_all(all_, k, v, slots)
+    assert np.array_equal(one, all_)
+    live = slots >= 0
+    for x, y in zip((k, v), rows_of(all_)):
+        assert np.array_equal(y[slots[live] // 64, :, slots[live] % 64], decode(*encode(x[live])))
 
 
 def test_plain_turn_keeps_lengths_and_inverts():
