@@ -12,8 +12,6 @@ namespace ikbo {
 
 // Record "what: <HIP error text>" for ikbo_last_error_message (ikbo_api.cpp); returns IKBO_ERR_HIP.
 int hip_fail(hipError_t e, const char *what);
-// Record `what` for ikbo_last_error_message; returns status.
-int status_fail(int status, const char *what);
 
 // Element `at` of a tensor of the given element size; NULL stays NULL.
 template <class T>
