@@ -25,12 +25,14 @@
 //
 // Two kernels.  In the narrow one a block is one wave with 16 or 32 rows, which converts the codes it
 // reads for itself, registers to registers: with few rows the cache's bytes are what counts, and 8 waves
-// on a CU keep 5 TB/s and more of them coming (0.46 GB of histories, one token each: 79 us, 5.8 TB/s).
+// on a CU keep 5 TB/s and more of them coming (0.46 GB of histories, one token each: 78-81 us, 5.7 TB/s).
 // Every wave repeats the conversion, so with many rows per user and head a block of 8 waves, 32 rows each,
 // converts a page once into LDS (bf16) and each wave reads its operands there.  What bounds it is the sum of
-// its parts, which two waves on a SIMD overlap only in part: of 2.14 us per page of 256 rows at head 128 (1.0
-// PFLOP/s) the matrix instructions take 1.1 at full rate, the softmax's and the conversion's vector work 1.1, LDS
-// 0.7; to begin and end a piece of a unit takes 6.6 us.  1024 candidates of 64 rows (121 GFLOP): 184 us, 656 TFLOP/s.
+// its parts, which two waves on a SIMD overlap only in part: of 1.83 us per page of 256 rows at head 128 (1.2
+// PFLOP/s) the matrix instructions take 0.95 at full rate, the softmax's and the conversion's vector work 0.95, LDS
+// 0.6; to begin and end a piece of a unit takes 5.9 us.  1024 candidates of 64 rows (123 GFLOP): 158 us, 775 TFLOP/s.
+// These are of a device whose clock is up, which takes some hundred passes; where two variants are compared below and in
+// hist_plan.h, both were timed over the first 20, in which this launch takes 184 us.
 //
 // How the work is dealt to the blocks, and what joins their partial results: hist_plan.h.
 #include <algorithm>
@@ -957,7 +959,8 @@ hipError_t launch(const AttnArgs &a, int64_t line_most, hipStream_t s) {
         hipLaunchKernelGGL(k, grid, dim3(512), kBuffers * WideLds<HD>::PAGE, s, a);
     } else {
         // With 16 rows to a unit hardly any two units share a tile, and a cache larger than the 256 MB of the last level
-        // is read past it: 97 -> 87 us for 0.46 GB; 0.1 GB, which stays there from call to call, would take 35 for 34.
+        // is read past it: 97 -> 87 us for 0.46 GB; 0.1 GB, which stays there from call to call, would take 35 for 34.  The
+        // table's capacity stands for the cache's size: a wide table over few pages is read past the caches too.
         const bool once = a.R == 16 && (int64_t)a.B_u * a.max_pages * a.H_kv * (68 * HD) > (256ll << 20);
         const auto k = a.R != 16 ? (small ? kv4_attn_kernel<HD, 2, true, false> : kv4_attn_kernel<HD, 2, false, false>)
                        : once    ? (small ? kv4_attn_kernel<HD, 1, true, true> : kv4_attn_kernel<HD, 1, false, true>)
@@ -979,7 +982,11 @@ Kv4AttnLayout kv4_attn_layout(int B_u, int B_c, int H_q, int H_kv, int L_q, int 
     const int64_t rows = (int64_t)B_c * L_q * (H_q / H_kv);
     // By the rows of the average user.  32 users of 3000 tokens and 8 heads, in us, narrow against wide: head 128:
     // 106, 143, 181, 320 against 138, 145, 158, 273 at 128, 192, 256, 512 rows; head 64: 80, 104, 129, 220 against
-    // 99, 106, 112, 189.
+    // 99, 106, 112, 189.  Units of 16 rows against 32: head 128: 36, 43, 50 against 46, 48, 56 at 16, 17, 32 rows, head
+    // 64: 31, 39, 45 against 33, 34, 41: between 17 and 32 rows head 128 would rather keep 16.
+    // A user is a row of the table, with candidates or without, for the host does not see the map.  15 users with 4352
+    // rows each take 159 us in a table of their own, 178 in one of 400 (units of 32 rows) and 334 in one of 4096 (of 16);
+    // with one token each 12, 22 and 28 us, most of it the launch that forms the plan.
     const int64_t mean = rows / B_u;
     w.R = mean <= 16 ? 16 : mean <= 192 ? 32 : 256;
     w.log_blocks = w.R == 256 ? kLogWide : kLogNarrow;

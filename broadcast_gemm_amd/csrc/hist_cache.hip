@@ -14,7 +14,7 @@
 // slots are neighbours, and the lanes of a wave, neighbouring pairs, write whole rows.
 //
 // Both are bound by their bytes once there are enough rows, and by a launch and two dependent reads where there are
-// few.  16381 tokens of 8 heads of 128, bf16: write 20.4 us (67 MB in, 18 out: 4.2 TB/s), read 22 us (3.8 TB/s);
+// few.  16381 tokens of 8 heads of 128, bf16: write 20 us (67 MB in, 18 out: 4.3 TB/s), read 22 us (3.9 TB/s);
 // 59 tokens of 4 heads: 3.5 and 3.8 us.
 #include "hist_internal.h"
 

@@ -5,8 +5,8 @@
 // rounded to float32: at p = 10^6 and freq = 1 a float32 angle would be off by 0.03 radians, this one
 // is off by 2^-25 turns.  Sine and cosine depend on the token and the pair only, so a block computes
 // them once for its tokens into LDS and all heads of q and k read them from there: the kernel is bound
-// by reading and writing q and k once: 16381 tokens of 32 + 8 heads of 128 in bf16 take 64 us (335 MB, 5.2 TB/s), 15
-// tokens of 4 + 4 heads 2.9 us (launch, sines, one access).
+// by reading and writing q and k once: 16381 tokens of 32 + 8 heads of 128 in bf16 take 62 us (335 MB, 5.4 TB/s), 15
+// tokens of 4 + 4 heads 2.7 us (launch, sines, one access).
 //
 // VEC elements (16 bytes) per thread and access where the heads allow it (rot_dim, head_dim and the
 // strides whole multiples of VEC, 16-byte aligned bases); VEC = 1 otherwise.

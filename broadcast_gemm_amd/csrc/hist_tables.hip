@@ -7,7 +7,7 @@
 // whose range of the third sum holds p.  So no block needs another's result: each block forms the
 // three sums itself (at most 4096 requests, 4 per thread, one block-wide scan) and then takes its share
 // of the rows and pages, found by binary search in LDS.  One launch, no waiting between blocks; what it
-// costs is the chain of a few dependent reads (4.2 us for a step of 59 requests, 10.4 us for 4096 requests with 65000
+// costs is the chain of a few dependent reads (3.9 us for a step of 59 requests, 10.4 us for 4096 requests with 65000
 // tokens, of which the scan of the counts and the searches are most).
 //
 // In-place lengths and ring state may only change once every block has read them: a block counts
