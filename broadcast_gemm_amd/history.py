@@ -97,7 +97,9 @@ def _device(t):
 
 
 def kv_status(status, stream=None) -> int:
-    """Wait for the stream, then return and clear the condition recorded in ``status`` (an IKBO_* code)."""
+    """Wait for the stream, then return and clear the condition recorded in ``status`` (an IKBO_* code).
+
+    Calls on other streams that share ``status`` must be over."""
     device = _device(status)
     if status.dtype != torch.int32 or status.numel() != 1:
         raise ValueError("status must be an int32 tensor of one element")

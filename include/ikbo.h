@@ -275,7 +275,8 @@ int ikbo_fa_plan_destroy(ikbo_fa_plan_t plan);
 
 /* Wait for `stream`, then return and clear the condition recorded in *status (device memory):
  * IKBO_OK, IKBO_ERR_MAP_RANGE, IKBO_ERR_PAGE_RANGE, IKBO_ERR_NO_PAGES or IKBO_ERR_NONFINITE
- * (the first of these that was set). */
+ * (the first of these that was set).  Calls on other streams that share the word must be over: what they
+ * record meanwhile may be cleared with it. */
 int ikbo_kv_status(uint32_t *status, void *stream);
 
 /*
