@@ -20,6 +20,7 @@ if the library is not built, every call raises.
     O = fa.forward(Q, K, V, map)
 
     from broadcast_gemm_amd.history import UserHistories    # target attention over cached 4-bit histories
+    from broadcast_gemm_amd.autograd import IkboAttention   # target attention's training, with dropout
 """
 from __future__ import annotations
 
@@ -54,7 +55,8 @@ EXPORTED = ("ikbo_lce_plan", "ikbo_lce_forward", "ikbo_lce_forward_noalloc", "ik
             "ikbo_fa_plan", "ikbo_fa_forward", "ikbo_fa_forward_fused", "ikbo_fa_check", "ikbo_fa_plan_destroy", "ikbo_lce_plan_info",
             "ikbo_lce_plan_set_spin_limit", "ikbo_lce_plan_destroy", "ikbo_status_str",
             "ikbo_last_error_message", "ikbo_kv_status", "ikbo_kv_tables", "ikbo_rope", "ikbo_kv4_write", "ikbo_kv4_read",
-            "ikbo_kv4_attention_workspace", "ikbo_kv4_attention")
+            "ikbo_kv4_attention_workspace", "ikbo_kv4_attention", "ikbo_attention_workspace", "ikbo_attention_forward",
+            "ikbo_attention_backward", "ikbo_dropout")
 
 
 class IkboError(RuntimeError):
@@ -108,11 +110,14 @@ def lib() -> ctypes.CDLL:
         L.ikbo_status_str.restype = ctypes.c_char_p
         L.ikbo_last_error_message.argtypes = []
         L.ikbo_last_error_message.restype = ctypes.c_char_p
-        for name in ("ikbo_kv_status", "ikbo_kv_tables", "ikbo_rope", "ikbo_kv4_write", "ikbo_kv4_read", "ikbo_kv4_attention"):
+        for name in ("ikbo_kv_status", "ikbo_kv_tables", "ikbo_rope", "ikbo_kv4_write", "ikbo_kv4_read", "ikbo_kv4_attention",
+                     "ikbo_attention_forward", "ikbo_attention_backward", "ikbo_dropout"):
             getattr(L, name).argtypes = [vp, vp]     # a structure (or the status word) and a stream
             getattr(L, name).restype = ip
         L.ikbo_kv4_attention_workspace.argtypes = [i] * 7
         L.ikbo_kv4_attention_workspace.restype = ctypes.c_int64
+        L.ikbo_attention_workspace.argtypes = [i] * 8
+        L.ikbo_attention_workspace.restype = ctypes.c_int64
         _lib = L
     return _lib
 

@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libikbo.so")
 TORCH_LIB = os.path.join(HERE, "_ikbo_torch.so")
 SOURCES = ["ikbo_api.cpp", "lce_kernels.hip", "lce_fused.hip", "lce_rows.hip", "lce_stream.hip", "lce_noalloc.hip", "lce_backward.hip", "ikbo_fa.cpp",
-           "fa_kernels.hip", "ikbo_history.cpp", "hist_tables.hip", "hist_rope.hip", "hist_cache.hip", "hist_attention.hip"]
+           "fa_kernels.hip", "ikbo_history.cpp", "hist_tables.hip", "hist_rope.hip", "hist_cache.hip", "hist_attention.hip",
+           "ikbo_training.cpp", "train_prep.hip", "train_forward.hip", "train_backward.hip", "dropout.hip"]
 ARCH = os.environ.get("IKBO_OFFLOAD_ARCH", "gfx950")
 
 

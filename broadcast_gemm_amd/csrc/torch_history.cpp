@@ -1,4 +1,5 @@
-// torch_history.cpp -- the binding of the cached user histories (history.py): argument checks, outputs and
+// torch_history.cpp -- the binding of the cached user histories (history.py) and of attention's training (training.py,
+// torch_training.h): argument checks, outputs and
 // workspaces from torch's allocator, and one call of the C ABI each.  A small call is bound by the host,
 // and these steps cost about 10 us in Python; here 3.  Host code only; the library's entry points
 // are handed over as addresses (bind), so that there is one libikbo.so in the process.
@@ -290,6 +291,8 @@ py::object kv4_attention(uintptr_t stream, const Tensor &Q, const Tensor &tiles,
     return py::cast(O);
 }
 
+#include "torch_training.h"
+
 }  // namespace
 
 PYBIND11_MODULE(_ikbo_torch, m) {
@@ -299,4 +302,8 @@ PYBIND11_MODULE(_ikbo_torch, m) {
     m.def("kv4_write", &kv4_write);
     m.def("kv4_read", &kv4_read);
     m.def("kv4_attention", &kv4_attention);
+    m.def("bind_training", &bind_training);
+    m.def("attention_forward", &attention_forward);
+    m.def("attention_backward", &attention_backward);
+    m.def("dropout", &dropout);
 }

@@ -1,0 +1,198 @@
+// train_device.h -- what the training kernels of target attention share: operands, staging, random numbers, rows.
+//
+// All products are v_mfma_f32_32x32x16_bf16; lane = 32 g + j.  A holds row j, contraction 8 g .. + 7; B column j,
+// likewise; element i of the result is row 8 (i / 4) + 4 g + i % 4 of column j.  A result that becomes the B operand of
+// the next product (weights, or their gradients) is used as it stands: step s of 16 takes elements 8 s .. 8 s + 7, that
+// is rows 16 s + 4 g + {0..3} and 16 s + 8 + 4 g + {0..3}, and the A operand of that product holds the same rows of a
+// staged matrix, transposed: two ds_read_b64_tr_b16, each 4 rows of column j.
+#pragma once
+
+#include "lce_device.h"
+#include "lce_sync.h"
+#include "train_internal.h"
+
+namespace ikbo {
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x16_t mfma32(const u32x4_t &a, const u32x4_t &b, f32x16_t acc) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+}
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+// x with that of the lane 32 away.
+__device__ __forceinline__ float sum_halves(float x) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, x);
+    const auto p = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return __builtin_bit_cast(float, (uint32_t)p[0]) + __builtin_bit_cast(float, (uint32_t)p[1]);
+}
+__device__ __forceinline__ float max_halves(float x) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, x);
+    const auto p = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
+}
+
+// ---- staged matrices -----------------------------------------------------------------------
+//
+// Rows of HD bf16 elements, their 16-byte chunks permuted by an XOR with a number of the row.  A 16-byte read of a wave
+// is served in sets of 16 lanes that hold each j % 16 once: the numbers of 16 rows (8 pairs of rows at HD 64, which share
+// 256 bytes) differ.  A transposed read takes 64 bytes of each of 4 neighbouring rows: their numbers differ in the bits
+// above those of 4 chunks.
+template <int HD>
+struct Rows {
+    static constexpr int BYTES = HD * 2, CHUNKS = HD / 8;
+    static __device__ __forceinline__ int number(int row) {
+        return HD == 128 ? (row & 3) << 2 | ((row >> 2) & 3) : ((row >> 1) & 1) << 2 | ((row >> 2) & 3);
+    }
+    static __device__ __forceinline__ int at(int row, int chunk) { return row * BYTES + ((chunk ^ number(row)) << 4); }
+};
+
+// A lane's reads of a staged matrix.  Rows 32 t + j of step s: direct(s) + 32 t rows.  Rows 16 s + 4 g + {0..3} (and
+// 8 behind) of column 32 d + j: turned(d) + 16 s rows, + 8 rows; the rows' numbers repeat after 16.
+template <int HD>
+struct Reader {
+    int row[HD / 16], col[2][HD / 32];
+    __device__ __forceinline__ void init(int lane) {
+        const int g = lane >> 5, j = lane & 31, i = lane & 15;
+#pragma unroll
+        for (int s = 0; s < HD / 16; ++s) row[s] = Rows<HD>::at(j, 2 * s + g);
+#pragma unroll
+        for (int d = 0; d < HD / 32; ++d)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {   // 16 lanes read 4 rows of 16 columns, 8 bytes each
+                const int c = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (i & 3);
+                col[y][d] = Rows<HD>::at(8 * y + 4 * g + (i >> 2), c >> 3) + 2 * (c & 7);
+            }
+    }
+    __device__ __forceinline__ u32x4_t direct(const char *m, int t, int s) const {
+        return *reinterpret_cast<const u32x4_t *>(m + row[s] + 32 * t * Rows<HD>::BYTES);
+    }
+    __device__ __forceinline__ u32x4_t turned(const char *m, int s, int d) const {
+        u32x2_t w[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+            w[y] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) i16x4_t *)(m + col[y][d] + 16 * s * Rows<HD>::BYTES)));
+        return (u32x4_t){w[0][0], w[0][1], w[1][0], w[1][1]};
+    }
+};
+
+// 16 bytes per lane from device memory straight into LDS, lane l's at `to` + 16 l.  Inline because the compiler would
+// make every LDS read wait for the builtin's loads; `landed` waits for them, and a barrier publishes them.  Nothing else in
+// these kernels uses m0.
+__device__ __forceinline__ void load_to_lds(const void *from, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(from) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) { return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)p; }
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// A block's LDS: two buffers of two matrices of 64 rows first, so that what is loaded straight into them stands in the
+// first 64 KB, which the loads' 16-bit base reaches.
+template <int HD, class T>
+struct Staged {
+    __align__(16) char buffer[2][2][64 * HD * 2];
+    __align__(16) T rest;
+};
+
+// What stands for a row that does not exist.
+__device__ const uint32_t kZeroRow[64] __attribute__((aligned(16))) = {};
+
+// A block's staging of 64 keys (or values) of one user and head.
+template <int HD, int WAVES>
+struct KeyLoads {
+    static constexpr int N = 64 * HD / 8 / (64 * WAVES), STAGE = 64 * HD * 2;
+    const char *from[N];
+    int key[N];
+    uint32_t chunk[N];
+    int64_t step;
+    __device__ __forceinline__ void init(const uint16_t *base, int64_t token, int first, int lane, int wv) {
+        step = token * 128;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int p = (i * WAVES + wv) * 64 + lane, row = p / Rows<HD>::CHUNKS;
+            chunk[i] = ((p % Rows<HD>::CHUNKS) ^ Rows<HD>::number(row)) * 16;
+            key[i] = first + row;
+            from[i] = reinterpret_cast<const char *>(base + key[i] * token) + chunk[i];
+        }
+    }
+    // The next 64; keys from `len` on are zeros.
+    __device__ __forceinline__ void next(uint32_t to, int wv, int len) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            load_to_lds(key[i] < len ? from[i] : reinterpret_cast<const char *>(kZeroRow) + chunk[i], to + (i * WAVES + wv) * 1024);
+            key[i] += 64;
+            from[i] += step;
+        }
+    }
+};
+
+// ---- random numbers ------------------------------------------------------------------------
+//
+// Philox4x32 with 7 rounds (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011): the
+// fewest with which it passes their batteries of tests.
+__device__ __forceinline__ u32x4_t philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0, uint32_t k1) {
+#pragma unroll
+    for (int r = 0; r < 7; ++r) {
+        const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c1 = (uint32_t)b;
+        c3 = (uint32_t)a;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return (u32x4_t){c0, c1, c2, c3};
+}
+
+struct Random {
+    uint32_t k0, k1, offset;
+    __device__ __forceinline__ void init(const int64_t *rng) {
+        const uint64_t seed = (uint64_t)rng[0];
+        k0 = __builtin_amdgcn_readfirstlane((uint32_t)seed);
+        k1 = __builtin_amdgcn_readfirstlane((uint32_t)(seed >> 32));
+        offset = __builtin_amdgcn_readfirstlane((uint32_t)rng[1]);
+    }
+    // The bytes of the 16 tokens 32 `block` + 8 w + 4 g + e: byte e of word w.
+    __device__ __forceinline__ u32x4_t weights(int block, int g, uint32_t row, uint32_t head) const {
+        return philox(2 * block + g, row, head, offset, k0, k1);
+    }
+};
+
+// ---- places --------------------------------------------------------------------------------
+
+__device__ __forceinline__ int user_len(const TrainArgs &a, int u) { return a.lens ? min(max(a.lens[u], 0), a.L_kv) : a.L_kv; }
+
+struct Place {
+    int cand, head, query;
+};
+// Row r of user u's rows of shared head hk; first = off[u].
+__device__ __forceinline__ Place place_of(const TrainArgs &a, int first, int hk, int r) {
+    const uint32_t per = (uint32_t)(a.G * a.L_q), slot = (uint32_t)r / per, rest = (uint32_t)r - slot * per, gr = rest / (uint32_t)a.L_q;
+    return Place{a.perm[first + (int)slot], hk * a.G + (int)gr, (int)(rest - gr * (uint32_t)a.L_q)};
+}
+// Tokens that a query sees.
+__device__ __forceinline__ int limit_of(const TrainArgs &a, const Place &p, int len) {
+    if (!a.positions) return len;
+    const int pos = a.positions[(int64_t)p.cand * a.L_q + p.query];
+    return pos < 0 ? 0 : pos < len ? pos + 1 : len;
+}
+
+// Blocks go round the 8 dies in turn; neighbouring units, which share K and V, go to one die.  Unit of this block
+// among n, or -1.
+__device__ __forceinline__ int unit_of(int block, int n) {
+    const int per = (n + 7) >> 3, at = (block & 7) * per + (block >> 3);
+    return (block >> 3) < per && at < n ? at : -1;
+}
+
+// Element quads 2 p and 2 p + 1 of a result column, rounded: 8 consecutive rows 16 p + 8 g .. of it for this lane.
+__device__ __forceinline__ u32x4_t eight_rows(const f32x16_t &x, int p, float by) {
+    const uint32_t a0 = pack_bf16x2(x[8 * p] * by, x[8 * p + 1] * by), a1 = pack_bf16x2(x[8 * p + 2] * by, x[8 * p + 3] * by);
+    const uint32_t b0 = pack_bf16x2(x[8 * p + 4] * by, x[8 * p + 5] * by), b1 = pack_bf16x2(x[8 * p + 6] * by, x[8 * p + 7] * by);
+    const auto s0 = __builtin_amdgcn_permlane32_swap(a0, b0, false, false), s1 = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+    return (u32x4_t){s0[0], s1[0], s0[1], s1[1]};
+}
+
+}  // namespace ikbo

@@ -1,0 +1,65 @@
+// train_internal.h -- host-side interface between the ABI of attention's training and dropout
+// (ikbo_training.cpp) and its kernels (train_*.hip).  Not installed; not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "ikbo.h"
+
+namespace ikbo {
+
+// Record "what: <HIP error text>" for ikbo_last_error_message (ikbo_api.cpp); returns IKBO_ERR_HIP.
+int hip_fail(hipError_t e, const char *what);
+
+// Bits of the caller's status word, as in the cached histories.
+constexpr uint32_t kTrainStMap = 1u, kTrainStLens = 2u;
+
+// How the work is cut, and the byte offsets of the workspace's parts.  A user's rows of one shared head are its
+// candidates' queries of all heads of the group: slot * G * L_q + g * L_q + l, with the candidates in order.
+struct TrainLayout {
+    int tile_rows;                     // rows to a block of the forward and of dQ
+    int tiles;                         // blocks of them per shared head, at most
+    int splits, split_keys;            // parts of the keys, each a multiple of 64
+    int chunk_rows;                    // rows to a block of dK and dV, at most
+    int chunks, slots;                 // blocks of them per shared head and range of keys, at most; those with partial results
+    int64_t o_perm, o_off, o_tile, o_chunk, o_user_chunk, o_count, o_delta, o_part, o_ml, o_dk, o_dv, total;
+};
+TrainLayout train_layout(int B_u, int B_c, int H_q, int H_kv, int L_q, int L_kv, int head_dim, bool backward);
+
+struct TrainArgs {
+    const uint16_t *Q, *K, *V;
+    uint16_t *O;
+    float *lse;
+    const uint16_t *dO;
+    uint16_t *dQ, *dK, *dV;
+    const int32_t *map, *lens, *positions;
+    const int64_t *rng;
+    uint32_t *status;
+    int32_t *perm, *off;               // [B_c] candidates by user, [B_u + 1]
+    int2 *tile;                        // [tiles]: user, first row
+    int4 *chunk;                       // [chunks]: user, first row, row behind the last, place of its partial result or -1
+    int2 *user_chunk;                  // [B_u]: the user's first place among the partial results, and how many
+    int32_t *count;                    // [2]: tiles, chunks
+    float *delta;                      // [B_c][H_q][L_q]: rowsum(dO O)
+    float *part;                       // partial O or dQ [splits][tiles][H_kv][tile_rows][head_dim]
+    float2 *ml;                        // maximum and sum of a partial row of O, likewise
+    float *part_dk, *part_dv;          // [slots][H_kv][L_kv rounded up][head_dim]
+    int64_t q_cand, q_head, q_query, k_user, k_head, k_token, v_user, v_head, v_token, o_cand, o_head, o_query;
+    int64_t do_cand, do_head, do_query, dq_cand, dq_head, dq_query, dk_user, dk_head, dk_token, dv_user, dv_head, dv_token;
+    int B_u, B_c, H_q, H_kv, G, L_q, L_kv;
+    int splits, split_keys, tiles, chunk_rows, chunks, slots;
+    float scale, scale_log2;
+    uint32_t edge;                     // weights whose byte is below it are dropped
+    float keep;                        // 256 / (256 - edge)
+};
+
+// What a launch of the grouping fills in for padding: O and lse, or dQ.
+hipError_t launch_train_prep(const TrainArgs &a, int tile_rows, bool backward, int head_dim, hipStream_t s);
+hipError_t launch_train_forward(const TrainArgs &a, const TrainLayout &w, int head_dim, hipStream_t s);
+hipError_t launch_train_backward(const TrainArgs &a, const TrainLayout &w, int head_dim, hipStream_t s);
+// Elements whose 16 bits are below edge are dropped.
+hipError_t launch_dropout(const ikbo_dropout_args &a, uint32_t edge, hipStream_t s);
+
+}  // namespace ikbo

@@ -1,7 +1,7 @@
 /*
  * ikbo.h -- C ABI of libikbo: the IKBO Linear Compression Embedding forward (and its
- * backward) on AMD Instinct MI355X (gfx950), target attention, and target attention over
- * cached user histories.
+ * backward) on AMD Instinct MI355X (gfx950), target attention, target attention over
+ * cached user histories, and target attention's training.
  *
  * The operation (IKBO recsys blog, "Deep Dive: Linear Compression"; aibriefing
  * article, "kernel deep-dive case 1"):
@@ -409,6 +409,83 @@ typedef struct ikbo_kv4_attention_args {
 /* Bytes of workspace for these dimensions, or a negative status. */
 int64_t ikbo_kv4_attention_workspace(int B_u, int B_c, int H_q, int H_kv, int L_q, int head_dim, int max_pages);
 int ikbo_kv4_attention(const ikbo_kv4_attention_args *args, void *stream);
+
+/*
+ * ---- Training target attention ----------------------------------------------------------
+ *
+ * Target attention over dense K and V that keeps the statistics its gradient needs, and the gradient; and dropout from a
+ * counter-based generator.  As for the cached histories there is no plan: every buffer is the caller's, calls are
+ * asynchronous on `stream`, may be captured, and record conditions in device data in the caller's status word
+ * (ikbo_kv_status).  Strides count elements.  The device that owns the buffers must be current.
+ *
+ * Query l of head h of candidate b, with u = map[b] and the shared head h / (H_q / H_kv), sees the tokens t of user u with
+ *     t < lens[u] (L_kv if lens is NULL)   and, if positions are given,   t <= positions[b][l]:
+ *
+ *     S = scale Q K^T,   lse = ln sum_t exp S,   P = exp(S - lse),   O = (P Z) V
+ *
+ * with Z the dropout's factors (1 without dropout), and the gradients, for an upstream gradient dO,
+ *
+ *     dV = (P Z)^T dO,   dP = (dO V^T) Z,   dS = P (dP - rowsum(dO O)),   dQ = scale dS K,   dK = scale dS^T Q
+ *
+ * dK and dV summed over the user's candidates and queries and the heads that share the head.  A query that sees nothing has
+ * O = 0 and lse = -inf, its gradient is 0 and its dO is not read; so are those of candidates whose map entry is -1 (padding) or, recorded
+ * as MAP_RANGE, outside [0, B_u).  Tokens from lens[u] on are not read and have dK = dV = 0; lengths outside [0, L_kv] are
+ * clamped and recorded as PAGE_RANGE.  A token that some of its user's queries see and others do not has to be finite.
+ *
+ * Dropout keeps each weight with probability 1 - r / 256, r = round(256 dropout), and divides it by that; r has to be
+ * between 1 and 255, or dropout 0.  rng[0] is the seed, the low 32 bits of rng[1] the offset: with the generator Philox4x32
+ * of 7 rounds (Salmon, Moraes, Dror, Shaw, 2011), key = the seed's low and high word, the 16 bytes of the counter
+ * (2 (t / 32) + (t / 4) % 2, b L_q + l, h, offset) are those of 16 tokens, byte t % 4 of word (t % 32) / 8 that of token t; a
+ * weight stays if its byte is at least r.  The backward takes the forward's dropout and rng.
+ *
+ * Layouts: Q, O, dO, dQ [B_c][H_q][L_q][head_dim], K, V, dK, dV [B_u][H_kv][L_kv][head_dim], bf16 with three strides
+ * (multiples of 8, not negative; those of inputs may be 0) and contiguous heads, 16-byte aligned; lse [B_c][H_q][L_q] float32,
+ * dense.  Outputs overlap nothing.  Scores, statistics and sums are float32; P and dS reach the matrix cores as bf16; outputs are rounded
+ * once.  The same call gives the same bits.  scale = 0 means 1/sqrt(head_dim); negative, NaN and infinite scales are
+ * INVALID_ARG.  head_dim 64 or 128, H_q a multiple of H_kv, 1 <= B_u <= IKBO_KV_MAX_USERS.
+ * workspace: ikbo_attention_workspace bytes, 16-byte aligned, not shared with a call that may overlap; nothing in it has
+ * to be kept between calls.
+ */
+typedef struct ikbo_attention_args {
+    const void *Q, *K, *V;
+    void *O;                    /* written by the forward, read by the backward, as lse is */
+    float *lse;
+    const void *dO;             /* from here to dV: the backward only */
+    void *dQ, *dK, *dV;
+    const int32_t *map;         /* [B_c] */
+    const int32_t *lens;        /* [B_u] or NULL */
+    const int32_t *positions;   /* [B_c][L_q] or NULL */
+    const int64_t *rng;         /* [2] seed, offset; may be NULL without dropout */
+    uint32_t *status;
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t q_cand, q_head, q_query, k_user, k_head, k_token, v_user, v_head, v_token, o_cand, o_head, o_query;
+    int64_t do_cand, do_head, do_query, dq_cand, dq_head, dq_query, dk_user, dk_head, dk_token, dv_user, dv_head, dv_token;
+    double dropout;
+    int32_t B_u, B_c, H_q, H_kv, L_q, L_kv, head_dim;
+    float scale;
+} ikbo_attention_args;
+/* Bytes of workspace for these dimensions (of the backward if it is not 0), or a negative status. */
+int64_t ikbo_attention_workspace(int B_u, int B_c, int H_q, int H_kv, int L_q, int L_kv, int head_dim, int backward);
+int ikbo_attention_forward(const ikbo_attention_args *args, void *stream);
+int ikbo_attention_backward(const ikbo_attention_args *args, void *stream);
+
+/*
+ * Dropout of n elements: y = residual + x / (1 - r / 65536) where an element stays, and residual (0 if NULL) where it does
+ * not, with r = round(65536 p) between 1 and 65535, or p = 0.  Element i has the 16 bits i % 8, in order, of the counter
+ * (i / 8 low, i / 8 high, 2^32 - 1, offset) of the generator above, and stays if they are at least r.  The gradient of x is
+ * the same call on the gradient of y, without residual.  An element that does not stay is not multiplied: NaN and infinity go with it.
+ * bf16 or float32 (IKBO_DTYPE_*), dense; y may be x or residual, and overlaps neither otherwise.
+ */
+typedef struct ikbo_dropout_args {
+    const void *x, *residual;
+    void *y;
+    const int64_t *rng;         /* [2] seed, offset */
+    int64_t n;
+    double p;
+    int32_t dtype;
+} ikbo_dropout_args;
+int ikbo_dropout(const ikbo_dropout_args *args, void *stream);
 
 /* Static text for a status code. */
 const char *ikbo_status_str(int status);
