@@ -21,6 +21,13 @@ angle with the same factor, the same kernel.
 
     rope = IkboRope(head_dim).cuda()
     q, k = rope(q, k, positions)                     # [T, H, head_dim] each
+
+Target attention trains through ``IkboAttention``, with dropout of its weights, and ``IkboDropout`` drops activations;
+``IkboLce`` takes a ``dropout`` of its output.  Their masks are never stored: the backward forms them again from the
+module's counter (``training``).
+
+    attend = IkboAttention(dropout=0.1).cuda()
+    O = attend(Q, K, V, map, lens=lens)              # Q, K, V may require grad; dK, dV at the user batch
 """
 from __future__ import annotations
 
@@ -29,7 +36,7 @@ from typing import Dict, Tuple
 import torch
 
 from . import FLAG_BACKWARD, LcePlan
-from . import history
+from . import history, training
 from .rewrite import bucket_b_c, bucket_b_u
 
 
@@ -88,18 +95,20 @@ class IkboLce(torch.nn.Module):
     """The LCE layer with trainable projections W_u [M, K_u] and W_c [M, K_c] (bf16).
 
     Initialised with standard deviation 1/sqrt(K_u + K_c), so that Y has about unit variance for
-    unit-variance inputs."""
+    unit-variance inputs.  While training, ``dropout`` of the output's elements are dropped (``IkboDropout``)."""
 
-    def __init__(self, K_u: int, K_c: int, M: int, D: int, generator=None):
+    def __init__(self, K_u: int, K_c: int, M: int, D: int, generator=None, dropout: float = 0.0):
         super().__init__()
         std = (K_u + K_c) ** -0.5
         self.W_u = torch.nn.Parameter((torch.randn(M, K_u, generator=generator) * std).to(torch.bfloat16))
         self.W_c = torch.nn.Parameter((torch.randn(M, K_c, generator=generator) * std).to(torch.bfloat16))
         self.D = D
+        self.drop = IkboDropout(dropout) if dropout else None
         self._plans = _BackwardPlans()
 
     def forward(self, U, C, mp):
-        return LceFunction.apply(U, C, mp, self.W_u, self.W_c, self._plans)
+        Y = LceFunction.apply(U, C, mp, self.W_u, self.W_c, self._plans)
+        return Y if self.drop is None else self.drop(Y)
 
 
 class RopeFunction(torch.autograd.Function):
@@ -147,3 +156,107 @@ class IkboRope(torch.nn.Module):
 
     def forward(self, q, k, positions):
         return RopeFunction.apply(q, k, positions, self.freq, self.layout, self.factor)
+
+
+class _Counter(torch.nn.Module):
+    """A module with random numbers of its own: ``rng`` (seed, offset), whose offset moves on with every call that uses them,
+    on the device, so that replays of a captured step draw new ones.  It is saved with the module's state."""
+
+    def __init__(self, seed):
+        super().__init__()
+        if seed is None:   # from torch's generator: other modules have others
+            seed = int(torch.randint(0, 1 << 62, ()))
+        self.register_buffer("rng", torch.tensor([seed, 0], dtype=torch.int64))
+
+    def _draw(self):
+        rng = self.rng.clone()
+        self.rng[1:].add_(1)
+        return rng
+
+
+def _probability(p: float, of: int) -> float:
+    if not (p == 0.0 or (0.0 < p < 1.0 and 0 < round(p * of) < of)):
+        raise ValueError(f"dropout must be 0, or a probability that is not 0 or 1 in whole {of}ths")
+    return float(p)
+
+
+class DropoutFunction(torch.autograd.Function):
+    """residual + dropout(x) in the library; the gradient of x is the same dropout of the gradient."""
+
+    @staticmethod
+    def forward(ctx, x, residual, p, rng):
+        ctx.save_for_backward(rng)
+        ctx.p = p
+        return training.dropout(x.contiguous(), p, rng, residual=None if residual is None else residual.contiguous())
+
+    @staticmethod
+    def backward(ctx, dy):
+        dx = DropoutFunction.apply(dy, None, ctx.p, *ctx.saved_tensors) if ctx.needs_input_grad[0] else None
+        return dx, dy if ctx.needs_input_grad[1] else None, None, None
+
+
+class IkboDropout(_Counter):
+    """x with ``p`` of its elements dropped and the others divided by 1 - p, added to ``residual`` if that is given.
+
+    bf16 or float32 on the GPU; p in whole 65536ths (the nearest).  In evaluation nothing is dropped."""
+
+    def __init__(self, p: float, seed=None):
+        super().__init__(seed)
+        self.p = _probability(p, 65536)
+
+    def forward(self, x, residual=None):
+        if self.training and self.p:
+            return DropoutFunction.apply(x, residual, self.p, self._draw())
+        return x if residual is None else residual + x
+
+
+class AttentionFunction(torch.autograd.Function):
+    """O = softmax(scale Q K[map]^T) V[map] over the tokens that each query sees, both directions in the library."""
+
+    @staticmethod
+    def forward(ctx, Q, K, V, mp, lens, positions, scale, dropout, rng, status):
+        Q, K, V = (_rows(t) for t in (Q, K, V))
+        how = dict(lens=lens, positions=positions, scale=scale, dropout=dropout, rng=rng)
+        O, lse = training.attention(Q, K, V, mp, status, **how)
+        ctx.save_for_backward(Q, K, V, O, lse, mp, lens, positions, rng, status)
+        ctx.how = scale, dropout
+        return O
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dO):
+        Q, K, V, O, lse, mp, lens, positions, rng, status = ctx.saved_tensors
+        scale, dropout = ctx.how
+        grads = training.attention_backward(_rows(dO), Q, K, V, O, lse, mp, status, lens=lens, positions=positions, scale=scale,
+                                            dropout=dropout, rng=rng)
+        return tuple(g if need else None for g, need in zip(grads, ctx.needs_input_grad)) + (None,) * 7
+
+
+def _rows(t):
+    """t, or a copy of it where its rows are not contiguous and 16-byte aligned."""
+    whole = t.dim() == 4 and (t.shape[3] == 1 or t.stride(3) == 1) and t.data_ptr() % 16 == 0
+    return t if whole and all(s % 8 == 0 for s, n in zip(t.stride()[:3], t.shape) if n > 1) else t.clone(memory_format=torch.contiguous_format)
+
+
+class IkboAttention(_Counter):
+    """Target attention with gradients: Q [B_c, H_q, L_q, head_dim] over the K, V [B_u, H_kv, L_kv, head_dim] of the candidates'
+    users, bf16.
+
+    ``map`` [B_c] names the users, -1 is padding; ``lens`` [B_u] are the users' numbers of tokens, ``positions`` [B_c, L_q]
+    limits each query to tokens up to its position (``training.attention``).  While training, ``dropout`` of the weights
+    (in whole 256ths, the nearest) are dropped.  ``check`` waits, returns and clears what calls recorded about their
+    device data.  Forward and backward may be captured into a graph together, while no eager graph of the same leaves is
+    alive (torch would accumulate their gradients on that one's stream)."""
+
+    def __init__(self, dropout: float = 0.0, scale: float = 0.0, seed=None):
+        super().__init__(seed)
+        self.dropout, self.scale = _probability(dropout, 256), float(scale)
+        self.register_buffer("status", torch.zeros(1, dtype=torch.int32), persistent=False)
+
+    def forward(self, Q, K, V, mp, lens=None, positions=None):
+        i32 = [None if t is None else t.to(torch.int32).contiguous() for t in (mp, lens, positions)]
+        drop = self.dropout if self.training else 0.0
+        return AttentionFunction.apply(Q, K, V, *i32, self.scale, drop, self._draw() if drop else None, self.status)
+
+    def check(self, stream=None) -> int:
+        return history.kv_status(self.status, stream)

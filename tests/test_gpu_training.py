@@ -1,0 +1,532 @@
+"""Attention's training and dropout on the GPU against their plain 64-bit forms (training_ref), with the bounds derived there."""
+import numpy as np
+import pytest
+
+import broadcast_gemm_amd as bga
+import training_ref as ref
+from gpu_util import log, torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def need_gpu():
+    if not torch().cuda.is_available():
+        pytest.skip("no GPU")
+    bga.lib()
+
+
+def T():
+    from broadcast_gemm_amd import training
+    return training
+
+
+def dev(a, dtype=None):
+    x = torch().from_numpy(np.ascontiguousarray(a))
+    return (x if dtype is None else x.to(dtype)).cuda()
+
+
+def f64(x):
+    return x.detach().double().cpu().numpy()
+
+
+def word():
+    return torch().zeros(1, dtype=torch().int32, device="cuda")
+
+
+def status(st):
+    from broadcast_gemm_amd import history
+    return history.kv_status(st)
+
+
+def bf16(g, *shape, size=1.0):
+    """Normal values that bf16 holds, as a tensor and in float64."""
+    t = torch()
+    x = t.from_numpy(g.normal(size=shape) * size).to(t.bfloat16)
+    return x, x.double().numpy()
+
+
+class Inputs:
+    def __init__(self, seed, B_u, B_c, H_q, H_kv, L_q, L_kv, dim, ragged=True, causal=False, dropout=0.0, padding=0, empty_users=False, size=1.0, scale=0.0):
+        g = np.random.default_rng(seed)
+        self.q, self.Q = bf16(g, B_c, H_q, L_q, dim, size=size)
+        self.k, self.K = bf16(g, B_u, H_kv, L_kv, dim, size=size)
+        self.v, self.V = bf16(g, B_u, H_kv, L_kv, dim)
+        self.do, self.dO = bf16(g, B_c, H_q, L_q, dim)
+        self.mp = g.integers(0, max(1, B_u // 2) if empty_users else B_u, B_c).astype(np.int32)
+        if padding:
+            self.mp[g.permutation(B_c)[:padding]] = -1
+        self.lens = g.integers(0, L_kv + 1, B_u).astype(np.int32) if ragged else None
+        self.positions = g.integers(-1, L_kv + 3, (B_c, L_q)).astype(np.int32) if causal else None
+        self.rng = (int(g.integers(0, 1 << 62)), int(g.integers(0, 1 << 32)))
+        self.dropout, self.scale = dropout, scale
+
+    def how(self, device=True):
+        t = torch()
+        d = dict(dropout=self.dropout, scale=self.scale, lens=self.lens, positions=self.positions, rng=self.rng)
+        if device:
+            for n in ("lens", "positions"):
+                d[n] = None if d[n] is None else dev(d[n])
+            d["rng"] = t.tensor(self.rng, dtype=t.int64, device="cuda")
+        return d
+
+    def want(self):
+        return ref.attention(self.Q, self.K, self.V, self.mp, dO=self.dO, **self.how(False))
+
+    def run(self, q=None, k=None, v=None, do=None, st=None, **kw):
+        st = word() if st is None else st
+        q, k, v, do = (b.cuda() if a is None else a for a, b in ((q, self.q), (k, self.k), (v, self.v), (do, self.do)))
+        mp = dev(self.mp)
+        O, lse = T().attention(q, k, v, mp, st, **self.how(), **kw)
+        dQ, dK, dV = T().attention_backward(do, q, k, v, O, lse, mp, st, **self.how(), **kw)
+        return dict(O=O, lse=lse, dQ=dQ, dK=dK, dV=dV)
+
+
+def compare(got, want, what):
+    for name in ("O", "lse", "dQ", "dK", "dV"):
+        x, y = f64(got[name]), want[name]
+        gone = np.isneginf(y)
+        assert np.array_equal(gone, np.isneginf(x)) and np.isfinite(x[~gone]).all(), f"{what}: {name}"
+        h = 0.0 if name == "lse" else ref.B8
+        ok, share = ref.within(np.where(gone, 0, x), np.where(gone, 0, y), want["off"][name], h)
+        log(f"  {what} {name}: {share:.2f} of the bound")
+        assert ok, f"{what}: {name} outside, {share:.3g} of its bound"
+
+
+SHAPES = [
+    # B_u, B_c, H_q, H_kv, L_q, L_kv, dim
+    (1, 1, 1, 1, 1, 1, 64), (1, 1, 1, 1, 1, 1, 128), (3, 7, 2, 1, 1, 64, 64), (2, 9, 2, 2, 3, 65, 128), (5, 40, 4, 2, 16, 130, 64), (4, 33, 3, 3, 33, 63, 128),
+    (2, 65, 8, 2, 1, 257, 128), (7, 5, 1, 1, 64, 300, 64), (1, 300, 2, 1, 2, 96, 64), (30, 64, 6, 2, 1, 31, 128), (2, 3, 2, 2, 1, 4500, 64),
+    (1, 2, 4, 1, 5, 2000, 128), (130, 257, 1, 1, 1, 20, 64)]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("kind", ["whole", "ragged", "causal", "dropout"])
+def test_attention_and_its_gradients(shape, kind):
+    log(f"attention {shape} {kind}")
+    x = Inputs(sum(shape), *shape, ragged=kind != "whole", causal=kind in ("causal", "dropout"), dropout=0.3 if kind == "dropout" else 0.0,
+               padding=shape[1] // 5 if kind != "whole" else 0, empty_users=kind == "ragged")
+    st = word()
+    compare(x.run(st=st), x.want(), f"{shape} {kind}")
+    assert status(st) == bga.IKBO_OK
+
+
+@pytest.mark.parametrize("dropout", [1 / 256, 0.5, 255 / 256])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_every_dropout_at_one_key_and_many(dropout, dim):
+    for L_kv in (1, 70):
+        x = Inputs(8, 2, 12, 2, 1, 3, L_kv, dim, ragged=False, dropout=dropout)
+        log(f"dropout {dropout} dim={dim} L_kv={L_kv}")
+        compare(x.run(), x.want(), f"dropout {dropout}")
+
+
+@pytest.mark.parametrize("L_kv", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257])
+def test_lengths_at_the_edges_of_tiles(L_kv):
+    x = Inputs(L_kv, 3, 6, 2, 1, 5, L_kv, 64, dropout=0.25)
+    x.lens = np.array([L_kv, max(0, L_kv - 1), 0], np.int32)
+    log(f"edges L_kv={L_kv}")
+    compare(x.run(), x.want(), f"L_kv {L_kv}")
+
+
+@pytest.mark.parametrize("rows", [1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 513, 1100])
+def test_rows_at_the_edges_of_tiles(rows):
+    """One user with many rows beside one with a single row and one without."""
+    x = Inputs(rows, 3, rows + 1, 1, 1, 1, 70, 128, ragged=False, causal=True)
+    x.mp = np.where(np.arange(rows + 1) == rows // 2, 2, 0).astype(np.int32)
+    log(f"edges rows={rows}")
+    compare(x.run(), x.want(), f"rows {rows}")
+
+
+def test_large_scores():
+    """Scores of several hundred: one weight is 1 and the others vanish."""
+    x = Inputs(5, 3, 20, 2, 1, 4, 200, 64, size=7.0)
+    log("large scores")
+    compare(x.run(), x.want(), "large scores")
+    x = Inputs(6, 3, 20, 2, 1, 4, 200, 128, size=3.0, scale=1.5, dropout=0.1)
+    compare(x.run(), x.want(), "a scale")
+
+
+def test_many_users_and_candidates():
+    """More users than threads of the grouping, and a map that names them in no order."""
+    x = Inputs(4, 2000, 3001, 1, 1, 1, 9, 64, padding=50, empty_users=True)
+    log("many users")
+    compare(x.run(), x.want(), "many users")
+    x = Inputs(5, 4096, 60, 1, 1, 1, 5, 64)
+    compare(x.run(), x.want(), "most users")
+
+
+def test_strided_tensors():
+    """Queries and gradients with tokens before heads, K and V out of one projection, K shared by all users, an
+    expanded upstream gradient."""
+    t = torch()
+    x = Inputs(9, 3, 10, 4, 2, 6, 100, 64, causal=True)
+    log("strides")
+    want = x.want()
+    q = x.q.transpose(1, 2).contiguous().cuda().transpose(1, 2)
+    do = x.do.transpose(1, 2).contiguous().cuda().transpose(1, 2)
+    kv = t.stack([x.k, x.v], 3).cuda()                       # [B_u, H, L, 2, dim]
+    k, v = kv[:, :, :, 0], kv[:, :, :, 1]
+    assert not q.is_contiguous() and k.stride(2) == 128
+    compare(x.run(q=q, k=k, v=v, do=do), want, "strides")
+    x.K[:], x.dO[:] = x.K[:1], x.dO[:, :, :1]
+    k = k[:1].expand(3, -1, -1, -1)
+    do = do[:, :, :1].expand(-1, -1, 6, -1)
+    compare(x.run(k=k, v=v, do=do), x.want(), "expanded")
+
+
+def test_wide_offsets():
+    """Users and candidates more than 2^32 bytes apart."""
+    t = torch()
+    x = Inputs(10, 3, 4, 1, 1, 2, 70, 64)
+    x.mp = np.array([2, 0, 1, 2], np.int32)
+    log("wide offsets")
+    step = (1 << 31) + 4096                                  # elements: 4.3 GB
+    big = t.empty(3 * step + 2 * 4 * 64, dtype=t.bfloat16, device="cuda")
+
+    def far(y):
+        z = big.as_strided((y.shape[0], 1, y.shape[2], 64), (step if y.shape[0] == 3 else step * 3 // 4, 64 * y.shape[2], 64, 1))
+        return z.copy_(y.cuda())
+
+    want = x.want()
+    compare(x.run(k=far(x.k)), want, "far keys")
+    compare(x.run(q=far(x.q)), want, "far queries")
+    compare(x.run(do=far(x.do)), want, "far gradients")
+
+
+def test_what_is_masked_is_not_read():
+    """NaN and infinity behind the histories, in the rows of padding and in the gradients of queries that see nothing."""
+    t = torch()
+    x = Inputs(11, 4, 20, 2, 1, 3, 90, 64, causal=True, padding=4, dropout=0.2)
+    x.lens[0] = 0
+    x.mp[:3] = 0, 1, 1
+    x.positions[1, 0] = -1
+    want = x.want()
+    k, v, q, do = x.k.cuda(), x.v.cuda(), x.q.cuda(), x.do.cuda()
+    for u, n in enumerate(x.lens):
+        k[u, :, n:] = float("nan")
+        v[u, :, n:] = float("inf")
+    for b, u in enumerate(x.mp):
+        for l in range(3):
+            if u < 0 or x.lens[u] == 0 or x.positions[b, l] < 0:
+                q[b, :, l], do[b, :, l] = float("nan"), float("inf")
+    log("masked places")
+    compare(x.run(q=q, k=k, v=v, do=do), want, "masked")
+
+
+def test_nonfinite_values_reach_their_own_rows_only():
+    t = torch()
+    x = Inputs(12, 2, 8, 2, 2, 4, 50, 64, ragged=False)
+    x.mp = (np.arange(8) % 2).astype(np.int32)
+    v, q = x.v.cuda(), x.q.cuda()
+    v[0, 0, 7, 3] = float("nan")
+    q[5, 1, 2, 0] = float("nan")
+    log("nonfinite")
+    got, want = x.run(q=q, v=v), x.want()
+    O = f64(got["O"])
+    bad = np.isnan(O)
+    assert bad[0::2, 0, :, 3].all() and bad[5, 1, 2].all()
+    bad[0::2, 0, :, 3] = False
+    bad[5, 1, 2] = False
+    assert not bad.any()
+    assert np.isfinite(f64(got["dK"])[0, 1]).all() and np.isfinite(f64(got["dV"])[1, 0]).all() and np.isnan(f64(got["dK"])[1, 1]).any()
+    assert np.isfinite(f64(got["dQ"])[1::2, 0]).all()
+
+
+def test_conditions_are_recorded():
+    t = torch()
+    x = Inputs(13, 3, 9, 2, 1, 2, 40, 64)
+    x.mp[:] = np.arange(9) % 3
+    want = {}
+    st = word()
+    x.lens[:] = 100, -3, 20
+    got = x.run(st=st)
+    assert status(st) == bga.IKBO_ERR_PAGE_RANGE and status(st) == bga.IKBO_OK
+    x.lens[:] = 40, 0, 20
+    compare(got, x.want(), "clamped lengths")
+    x.mp[2], x.mp[5] = 3, -7
+    got = x.run(st=st)
+    assert status(st) == bga.IKBO_ERR_MAP_RANGE
+    x.mp[[2, 5]] = -1
+    compare(got, x.want(), "map out of range")
+
+
+def test_no_candidates_and_padding_alone():
+    t = torch()
+    x = Inputs(14, 2, 3, 2, 1, 2, 40, 64)
+    q = t.empty(0, 2, 2, 64, dtype=t.bfloat16, device="cuda")
+    none = t.empty(0, dtype=t.int32, device="cuda")
+    k, v = x.k.cuda(), x.v.cuda()
+    O, lse = T().attention(q, k, v, none, word())
+    assert O.shape == q.shape and lse.shape == (0, 2, 2)
+    dQ, dK, dV = T().attention_backward(q, q, k, v, O, lse, none, word())
+    assert dQ.shape == q.shape and not dK.any() and not dV.any()
+    x.mp[:] = -1
+    compare(x.run(), x.want(), "padding alone")
+
+
+def test_same_call_same_bits_and_other_numbers():
+    t = torch()
+    x = Inputs(15, 5, 120, 8, 2, 3, 700, 64, causal=True, dropout=0.4)
+    a, b = x.run(), x.run()
+    assert all(t.equal(a[n], b[n]) for n in a)
+    x.rng = (x.rng[0], x.rng[1] + (1 << 32))
+    assert t.equal(x.run()["O"], a["O"])                     # offsets count modulo 2^32
+    x.rng = (x.rng[0], x.rng[1] + 1)
+    c = x.run()
+    assert not t.equal(c["O"], a["O"]) and t.equal(c["lse"], a["lse"])
+
+
+def test_streams_and_replayed_graphs():
+    """Two captured steps that share nothing but their inputs, replayed between eager work on two streams, with other
+    numbers and lengths for every replay."""
+    t = torch()
+    xs = [Inputs(16, 4, 50, 4, 2, 3, 200, 64, dropout=0.2), Inputs(17, 2, 31, 2, 2, 2, 900, 128, causal=True, dropout=0.1)]
+    steps = []
+    for x in xs:
+        st, mp, how = word(), dev(x.mp), x.how()
+        ten = [y.cuda() for y in (x.q, x.k, x.v, x.do)]
+
+        def step(ten=ten, mp=mp, st=st, how=how):
+            O, lse = T().attention(*ten[:3], mp, st, **how)
+            return O, lse, *T().attention_backward(ten[3], *ten[:3], O, lse, mp, st, **how)
+        steps.append((step, how))
+    side = t.cuda.Stream()
+    t.cuda.synchronize()
+    with t.cuda.stream(side):
+        for step, _ in steps:
+            step()
+    t.cuda.synchronize()
+    graphs = []
+    for step, how in steps:
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g):
+            out = step()
+        graphs.append((g, out))
+    for turn in range(4):
+        for step, how in steps:
+            how["rng"][1] += 1
+            how["lens"] += (-1 if turn % 2 else 1) * (how["lens"] > 5)
+        t.cuda.synchronize()
+        with t.cuda.stream(side):
+            eager = [step() for step, _ in steps]
+        for g, _ in graphs:
+            g.replay()
+        t.cuda.synchronize()
+        for (_, out), want in zip(graphs, eager):
+            assert all(t.equal(a, b) for a, b in zip(out, want)), turn
+    step, how = steps[0]
+    handle = side.cuda_stream
+    x = xs[0]
+    O, lse = T().attention(x.q.cuda(), x.k.cuda(), x.v.cuda(), dev(x.mp), word(), stream=handle, **how)
+    t.cuda.synchronize()
+    assert t.equal(O, eager[0][0]) and t.equal(lse, eager[0][1])
+
+
+def test_refusals_of_the_binding():
+    t = torch()
+    x = Inputs(18, 2, 4, 2, 1, 3, 40, 64, dropout=0.5)
+    q, k, v, mp, st, how = x.q.cuda(), x.k.cuda(), x.v.cuda(), dev(x.mp), word(), x.how()
+    bad = [(q.float(), k, v, mp, st), (q, k.float(), v, mp, st), (q[0], k, v, mp, st), (q.transpose(2, 3), k, v, mp, st), (q, k, v, mp.long(), st),
+           (q, k, v.cpu(), mp, st), (q, k, v, mp, st.long()), (q, k, v, mp.cpu(), st)]
+    for args in bad:
+        with pytest.raises(ValueError):
+            T().attention(*args, **how)
+    for change in (dict(rng=None), dict(rng=how["rng"].int()), dict(rng=how["rng"][:1]), dict(lens=how["lens"].long())):
+        with pytest.raises(ValueError):
+            T().attention(q, k, v, mp, st, **{**how, **change})
+    for args in ((q, k, v[:1], mp, st), (q, k, v, mp[:3], st), (q[..., :32], k[..., :32], v[..., :32], mp, st), (q[:, :, :, :], k[:, :, :0], v[:, :, :0], mp, st)):
+        with pytest.raises(bga.IkboError):
+            T().attention(*args, **how)
+    for change in (dict(lens=how["lens"][:1]), dict(dropout=1.0), dict(dropout=0.0001), dict(scale=-1.0), dict(positions=dev(np.zeros((4, 2), np.int32)))):
+        with pytest.raises(bga.IkboError):
+            T().attention(q, k, v, mp, st, **{**how, **change})
+    odd = t.empty(q.numel() + 8, dtype=q.dtype, device="cuda")[4:4 + q.numel()].view(q.shape)
+    with pytest.raises(bga.IkboError) as e:
+        T().attention(odd, k, v, mp, st, **how)
+    assert e.value.status == bga.IKBO_ERR_ALIGNMENT
+    O, lse = T().attention(q, k, v, mp, st, **how)
+    with pytest.raises(bga.IkboError):
+        T().attention_backward(O[:3], q, k, v, O, lse, mp, st, **how)
+    with pytest.raises(ValueError):
+        T().attention_backward(O, q, k, v, O, lse.double(), mp, st, **how)
+    with pytest.raises(ValueError):
+        T().attention_backward(O.float(), q, k, v, O, lse, mp, st, **how)
+
+
+# ---- dropout -------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("n", [1, 7, 8, 9, 63, 2047, 2048, 2049, 70001])
+@pytest.mark.parametrize("residual", [False, True])
+def test_dropout(dtype, n, residual):
+    t = torch()
+    g = np.random.default_rng(n)
+    dtype = getattr(t, dtype)
+    x, r = (t.from_numpy(g.normal(size=n)).to(dtype) for _ in range(2))
+    h = t.finfo(dtype).eps / 2
+    for p in (0.0, 1 / 65536, 0.1, 0.9, 65535 / 65536):
+        rng = (int(g.integers(0, 1 << 62)), int(g.integers(0, 1 << 32)))
+        log(f"dropout {dtype} n={n} residual={residual} p={p}")
+        y = f64(T().dropout(x.cuda(), p, t.tensor(rng, device="cuda"), residual=r.cuda() if residual else None))
+        kept = np.where(ref.elements_kept(n, p, rng), f64(x) / (1 - round(65536 * p) / 65536), 0.0)
+        want = kept + (f64(r) if residual else 0.0)
+        # The factor, the product and the sum round in float32, and then the type.
+        off = 2 * ref.U24 * np.abs(kept) + ref.U24 * np.abs(want)
+        assert (np.abs(y - want) <= off * (1 + h) + h * np.abs(want)).all()
+        if not residual:
+            assert (y[kept == 0] == 0).all()
+
+
+def test_dropout_places():
+    """In place, over the residual, at odd addresses, with NaN and infinity in what goes."""
+    t = torch()
+    rng = t.tensor([3, 4], device="cuda")
+    g = t.Generator(device="cuda").manual_seed(1)
+    for dtype in (t.bfloat16, t.float32):
+        base = t.randn(5001, generator=g, device="cuda").to(dtype)
+        want = T().dropout(base, 0.3, rng)
+        add = t.randn(5001, generator=g, device="cuda").to(dtype)
+        both = T().dropout(base, 0.3, rng, residual=add)
+        room = t.empty(5010, dtype=dtype, device="cuda")
+        for at in (0, 1, 3, 8):
+            x = room[at:at + 5001]
+            x.copy_(base)
+            assert t.equal(T().dropout(x, 0.3, rng), want)
+            assert T().dropout(x, 0.3, rng, out=x) is x and t.equal(x, want)
+            x.copy_(add)
+            assert t.equal(T().dropout(base, 0.3, rng, residual=x, out=x), both)
+        kept = t.from_numpy(ref.elements_kept(5001, 0.3, (3, 4))).cuda()
+        x = t.where(kept, base, float("nan"))
+        x[~kept & (t.arange(5001, device="cuda") % 2 == 0)] = float("inf")
+        assert t.equal(T().dropout(x, 0.3, rng), want) and t.equal(T().dropout(x, 0.3, rng, residual=add), both)
+        with pytest.raises(ValueError):
+            T().dropout(room[:5000], 0.3, rng, out=room[1:5001])
+        with pytest.raises(ValueError):
+            T().dropout(base, 0.3, rng, residual=room[:5001], out=room[2:5003])
+        with pytest.raises(ValueError):
+            T().dropout(room[:5000].view(100, 50).t(), 0.3, rng)
+        with pytest.raises(ValueError):
+            T().dropout(base, 0.3, rng.int())
+        with pytest.raises(ValueError):
+            T().dropout(base, 0.3, rng, residual=add[:100])
+        with pytest.raises(bga.IkboError):
+            T().dropout(base, 1.0, rng)
+    with pytest.raises(ValueError):
+        T().dropout(t.zeros(8, dtype=t.float16, device="cuda"), 0.3, rng)
+    assert T().dropout(t.empty(0, device="cuda"), 0.3, rng).numel() == 0
+
+
+def test_dropout_of_more_than_2_to_32_elements():
+    """The last elements take the counters behind 2^29, whose generator words and places pass 32 bits."""
+    t = torch()
+    n = (1 << 32) + 77
+    x = t.ones(n, dtype=t.bfloat16, device="cuda")
+    rng = t.tensor([11, 12], device="cuda")
+    log("dropout of 2^32 elements")
+    y = T().dropout(x, 0.5, rng, out=x)[-4096 - 77:].cpu()
+    counter = np.zeros((-(-(4096 + 77) // 8), 4), np.uint64)
+    at = (1 << 32) - 4096
+    counter[:, 0] = at // 8 + np.arange(len(counter))
+    counter[:, 2], counter[:, 3] = 0xFFFFFFFF, 12
+    words = ref.philox(counter, 11)
+    kept = np.stack([words & np.uint64(0xFFFF), words >> np.uint64(16)], -1).reshape(-1)[:4096 + 77] >= 32768
+    assert np.array_equal(f64(y), np.where(kept, 2.0, 0.0))
+
+
+# ---- together ------------------------------------------------------------------------------
+
+
+def test_modules_run_together():
+    """Rotary positions, attention with dropout, dropout onto the residual stream, the LCE with dropout: a step's gradients
+    are those of the same calls made by hand, and evaluation drops nothing."""
+    t = torch()
+    from broadcast_gemm_amd.autograd import IkboAttention, IkboDropout, IkboLce, IkboRope
+    from broadcast_gemm_amd import history
+    x = Inputs(20, 3, 12, 4, 2, 8, 60, 64, causal=True, padding=2)
+    attend, drop = IkboAttention(dropout=0.2, seed=5).cuda(), IkboDropout(0.25, seed=6).cuda()
+    rope, lce = IkboRope(64).cuda(), IkboLce(10, 32, 8, 64, dropout=0.1).cuda()
+    q, k, v = (y.cuda().requires_grad_() for y in (x.q, x.k, x.v))
+    mp, lens, positions = dev(x.mp).long(), dev(x.lens), dev(np.maximum(x.positions, 0))
+    U = t.randn(3, 10, 64, device="cuda").to(t.bfloat16)
+
+    def forward():
+        flat = q.transpose(1, 2).reshape(-1, 4, 64)
+        turned = rope(flat, None, positions.reshape(-1))[0].view(12, 8, 4, 64).transpose(1, 2)
+        O = attend(turned, k, v, mp, lens=lens, positions=positions)
+        return turned, O, drop(O, q)
+
+    turned, O, y = forward()
+    Y = lce(U, y.reshape(12, 32, 64), mp.clamp(min=0))
+    dy = t.randn_like(y.float()).to(t.bfloat16)
+    log("together")
+    t.autograd.backward([y, Y], [dy, t.zeros_like(Y)])
+    t.cuda.synchronize()
+    assert attend.check() == bga.IKBO_OK
+    i32 = [z.to(t.int32) for z in (mp, lens, positions)]
+    st = word()
+    how = dict(lens=i32[1], positions=i32[2], dropout=0.2, rng=t.tensor([5, 0], device="cuda"))
+    O2, lse = T().attention(turned.detach(), k.detach(), v.detach(), i32[0], st, **how)
+    assert t.equal(O, O2) and t.equal(y, T().dropout(O2, 0.25, t.tensor([6, 0], device="cuda"), residual=q.detach()))
+    dO = T().dropout(dy, 0.25, t.tensor([6, 0], device="cuda"))
+    dt, dk, dv = T().attention_backward(dO, turned.detach(), k.detach(), v.detach(), O2, lse, i32[0], st, **how)
+    assert t.equal(k.grad, dk) and t.equal(v.grad, dv)
+    back = history.rope(dt.transpose(1, 2).reshape(-1, 4, 64), None, i32[2].reshape(-1), rope.freq, inverse=True)[0]
+    assert t.equal(q.grad, back.view(12, 8, 4, 64).transpose(1, 2) + dy)
+    assert attend.rng.tolist() == [5, 1] and drop.rng.tolist() == [6, 1]
+    assert abs(float((Y == 0).float().mean()) - 0.1) < 0.05
+    for m in (attend, drop, lce):
+        m.eval()
+    a, b = forward()[1:], forward()[1:]
+    assert t.equal(a[0], b[0]) and t.equal(a[1], b[1]) and attend.rng.tolist() == [5, 1]
+    lce._plans.close()
+
+
+def test_module_takes_any_strides_and_only_what_needs_gradients():
+    t = torch()
+    from broadcast_gemm_amd.autograd import IkboAttention
+    x = Inputs(21, 2, 5, 2, 2, 3, 40, 64, ragged=False)
+    attend = IkboAttention().cuda()
+    k, v = x.k.cuda(), x.v.cuda()
+    q = x.q.transpose(2, 3).contiguous().cuda().transpose(2, 3).requires_grad_()   # elements of a row far apart
+    O = attend(q, k, v, dev(x.mp))
+    O.sum().backward()                                                             # an upstream gradient without strides
+    x.dO[:] = 1.0
+    want = x.want()
+    ok, share = ref.within(f64(q.grad), want["dQ"], want["off"]["dQ"], ref.B8)
+    assert ok, share
+    ok, share = ref.within(f64(O), want["O"], want["off"]["O"], ref.B8)
+    assert ok, share
+
+
+def test_a_captured_training_step_draws_new_numbers():
+    t = torch()
+    from broadcast_gemm_amd.autograd import IkboAttention
+    x = Inputs(22, 3, 20, 2, 1, 2, 100, 64)
+    attend = IkboAttention(dropout=0.3, seed=9).cuda()
+    q, k, v = (y.cuda().requires_grad_() for y in (x.q, x.k, x.v))
+    mp, lens, do = dev(x.mp), dev(x.lens), x.do.cuda()
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        O = attend(q, k, v, mp, lens=lens)
+        t.autograd.grad(O, (q, k, v), do)
+    t.cuda.current_stream().wait_stream(side)
+    del O
+    t.cuda.synchronize()
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        O = attend(q, k, v, mp, lens=lens)
+        grads = t.autograd.grad(O, (q, k, v), do)
+    seen = []
+    for turn in range(3):
+        offset = int(attend.rng[1])
+        g.replay()
+        t.cuda.synchronize()
+        assert int(attend.rng[1]) == offset + 1
+        how = dict(lens=lens, dropout=0.3, rng=t.tensor([9, offset], device="cuda"))
+        O2, lse = T().attention(q.detach(), k.detach(), v.detach(), mp, word(), **how)
+        want = T().attention_backward(do, q.detach(), k.detach(), v.detach(), O2, lse, mp, word(), **how)
+        assert t.equal(O, O2) and all(t.equal(a, b) for a, b in zip(grads, want))
+        seen.append(O.clone())
+    assert not t.equal(seen[0], seen[1]) and not t.equal(seen[1], seen[2])
