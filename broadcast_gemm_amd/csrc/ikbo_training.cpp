@@ -16,7 +16,7 @@ namespace {
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 constexpr int64_t kInt = std::numeric_limits<int32_t>::max();
-constexpr int kMaxHeads = 4096, kTileRows = 256, kKeys = 256, kThreads = 512, kCus = 256;
+constexpr int kMaxHeads = 4096, kTileRows = 256, kThreads = 512, kCus = 256;
 
 // Probability as whole steps of 1 / of; 0 and `of` only for probabilities of 0 and 1.
 int steps(double p, int of) { return (int)std::nearbyint(p * of); }
@@ -69,11 +69,11 @@ TrainArgs args_of(const ikbo_attention_args &a, const TrainLayout &w) {
     t.map = a.map; t.lens = a.lens; t.positions = a.positions; t.rng = a.rng; t.status = a.status;
     t.perm = reinterpret_cast<int32_t *>(ws + w.o_perm);
     t.off = reinterpret_cast<int32_t *>(ws + w.o_off);
-    t.tile = reinterpret_cast<int2 *>(ws + w.o_tile);
+    t.tile = reinterpret_cast<int4 *>(ws + w.o_tile);
     t.chunk = reinterpret_cast<int4 *>(ws + w.o_chunk);
     t.user_chunk = reinterpret_cast<int2 *>(ws + w.o_user_chunk);
     t.count = reinterpret_cast<int32_t *>(ws + w.o_count);
-    t.delta = reinterpret_cast<float *>(ws + w.o_delta);
+    t.notes = reinterpret_cast<RowNotes *>(ws + w.o_notes);
     t.part = reinterpret_cast<float *>(ws + w.o_part);
     t.ml = reinterpret_cast<float2 *>(ws + w.o_ml);
     t.part_dk = reinterpret_cast<float *>(ws + w.o_dk);
@@ -88,7 +88,7 @@ TrainArgs args_of(const ikbo_attention_args &a, const TrainLayout &w) {
     t.dv_user = a.dv_user; t.dv_head = a.dv_head; t.dv_token = a.dv_token;
     t.B_u = a.B_u; t.B_c = a.B_c; t.H_q = a.H_q; t.H_kv = a.H_kv; t.G = a.H_q / a.H_kv; t.L_q = a.L_q; t.L_kv = a.L_kv;
     t.splits = w.splits; t.split_keys = w.split_keys; t.tiles = w.tiles;
-    t.chunk_rows = w.chunk_rows; t.chunks = w.chunks; t.slots = w.slots;
+    t.chunk_rows = w.chunk_rows; t.chunks = w.chunks; t.slots = w.slots; t.n_notes = w.notes;
     t.scale = a.scale > 0.0f ? a.scale : 1.0f / std::sqrt((float)a.head_dim);
     t.scale_log2 = (float)(t.scale * 1.4426950408889634);
     t.edge = (uint32_t)steps(a.dropout, 256);
@@ -119,7 +119,7 @@ TrainLayout train_layout(int B_u, int B_c, int H_q, int H_kv, int L_q, int L_kv,
     w.o_perm = take((int64_t)B_c * 4);
     w.o_off = take((int64_t)(B_u + 1) * 4);
     w.o_count = take(8);
-    w.o_tile = take((int64_t)w.tiles * 8);
+    w.o_tile = take((int64_t)w.tiles * 16);
     const int64_t parts = w.splits > 1 ? (int64_t)w.splits * w.tiles * H_kv * kTileRows : 0;
     w.o_part = take(parts * head_dim * 4);
     w.o_ml = take(backward ? 0 : parts * 8);
@@ -134,7 +134,8 @@ TrainLayout train_layout(int B_u, int B_c, int H_q, int H_kv, int L_q, int L_kv,
         w.slots = rows > w.chunk_rows ? (int)(2 * rows / w.chunk_rows + 1) : 0;   // n > 1 chunks of a user are more than n / 2 full ones
         w.o_chunk = take((int64_t)w.chunks * 16);
         w.o_user_chunk = take((int64_t)B_u * 8);
-        w.o_delta = take((int64_t)B_c * H_q * L_q * 4);
+        w.notes = (int)(rows / 64 + std::min(B_u, B_c));
+        w.o_notes = take((int64_t)w.notes * H_kv * (int64_t)sizeof(RowNotes));
         w.o_dk = take((int64_t)w.slots * H_kv * L_kv * head_dim * 4);
         w.o_dv = take((int64_t)w.slots * H_kv * L_kv * head_dim * 4);
     }

@@ -9,8 +9,7 @@
 // dK and dV: a wave keeps 32 keys' K and V and their gradients in registers, and the block goes over a chunk of the
 // user's rows, staged in LDS 64 at a time: S = Q K^T, dP = dO V^T, dV^T += dO^T P, dK^T += Q^T dS.  Rows stand in the
 // results' rows here, so P and dS are the B operands as they stand.  The weights that stay are decided with the rows
-// in the lanes, as in the other kernels (one generator call for 16 tokens of a row), and the bits turned round by
-// ballots.  Chunks of one user are joined by a third launch, in their order.
+// in the lanes, as in the other kernels (one generator call for 16 tokens of a row), and the bits turned round (Turn).  Chunks of one user are joined by a third launch, in their order.
 //
 // That is 7 products against the 5 that one pass needs; adding up dQ across key ranges instead would write and read 4
 // bytes an element for every range.  P and dS are rounded to bf16 for their products; all sums are float32.
@@ -23,10 +22,9 @@ namespace {
 
 template <int HD, int NT, int WAVES, bool DROP>
 __global__ void __launch_bounds__(64 * WAVES, 1) train_dq_kernel(TrainArgs a) {
-    constexpr int TK = HD / 16, DT = HD / 32, STAGE = 64 * HD * 2, ROWS = 32 * NT * WAVES;
-    __shared__ Staged<HD, int[WAVES]> sh;
-    char (&lds)[2][2][STAGE] = sh.buffer;
-    int (&s_most)[WAVES] = sh.rest;
+    constexpr int TK = HD / 16, DT = HD / 32, STAGE = Rows<HD>::matrix(64), ROWS = 32 * NT * WAVES;
+    __shared__ __align__(16) char lds[2][2][STAGE];
+    __shared__ int s_most[WAVES];
     const int n_tiles = a.count[0];
     const int unit = unit_of((int)blockIdx.x, n_tiles * a.H_kv * a.splits);
     if (unit < 0) return;   // the whole block: no barrier has run
@@ -185,8 +183,20 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_dq_kernel(TrainArgs a) {
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+        const int r = r0 + 32 * n + j;
+        if (split == 0 && g == 0 && r < ((n_rows + 63) & ~63)) {
+            RowNotes &x = a.notes[(int64_t)hk * a.n_notes + a.tile[tile].z + ((r - row0) >> 6)];
+            const int i = r & 63;
+            const bool sees = limit[n] > 0;
+            x.q[i] = sees ? (const void *)(a.Q + at[n].cand * a.q_cand + at[n].head * a.q_head + at[n].query * a.q_query) : kZeroRow;
+            x.dy[i] = sees ? (const void *)(a.dO + at[n].cand * a.do_cand + at[n].head * a.do_head + at[n].query * a.do_query) : kZeroRow;
+            x.shift[i] = sees ? shift[n] : neg_inf();
+            x.D[i] = D[n];
+            x.limit[i] = limit[n];
+            x.row[i] = at[n].cand * a.L_q + at[n].query;
+            x.head[i] = at[n].head;
+        }
         if (!live[n]) continue;
-        if (split == 0 && g == 0) a.delta[((int64_t)at[n].cand * a.H_q + at[n].head) * a.L_q + at[n].query] = D[n];
         if (a.splits == 1) {
             uint16_t *to = a.dQ + at[n].cand * a.dq_cand + at[n].head * a.dq_head + at[n].query * a.dq_query + 8 * g;
 #pragma unroll
@@ -223,95 +233,77 @@ __global__ void __launch_bounds__(256) train_dq_join_kernel(TrainArgs a, int til
         (u32x2_t){pack_bf16x2(o[0] * a.scale, o[1] * a.scale), pack_bf16x2(o[2] * a.scale, o[3] * a.scale)};
 }
 
-// What the dK and dV kernel keeps of 64 staged rows besides Q and dO.
-struct RowsMeta {
-    const char *q[64], *dy[64];       // where they stand; a row that does not exist or sees nothing is zeros
-    float shift[64], D[64];           // -lse in base 2 (-inf for such a row: no weights), rowsum(dO O)
-    int limit[64], row[64], head[64]; // tokens it sees, b L_q + l, h
-    int least, most;
-};
-
 template <int HD, int NK, int WAVES, bool DROP>
 __global__ void __launch_bounds__(64 * WAVES, 1) train_dkv_kernel(TrainArgs a) {
-    constexpr int TK = HD / 16, DT = HD / 32, STAGE = 64 * HD * 2, KEYS = 32 * NK * WAVES, N = 64 * HD / 8 / (64 * WAVES);
-    __shared__ Staged<HD, RowsMeta[3]> sh;
-    char (&lds)[2][2][STAGE] = sh.buffer;
-    RowsMeta (&meta)[3] = sh.rest;
+    constexpr int TK = HD / 16, DT = HD / 32, STAGE = Rows<HD>::matrix(64), KEYS = 32 * NK * WAVES, N = 64 * HD / 8 / (64 * WAVES);
+    constexpr bool V_LDS = HD == 128;   // V stays in LDS: 32 registers less, which lets two waves stand on a SIMD
+    __shared__ __align__(16) char lds[2][2][STAGE], v_lds[V_LDS ? Rows<HD>::matrix(KEYS) : 16];
+    __shared__ __align__(16) RowNotes notes[3];
     const int n_chunks = a.count[1], ranges = (a.L_kv + KEYS - 1) / KEYS;
     const int unit = unit_of((int)blockIdx.x, n_chunks * a.H_kv * ranges);
     if (unit < 0) return;   // the whole block: no barrier has run
     const int range = unit % ranges, hk = unit / ranges % a.H_kv, c = unit / ranges / a.H_kv;   // neighbours share rows
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5, j = lane & 31;
     const int4 ch = a.chunk[c];
-    const int u = __builtin_amdgcn_readfirstlane(ch.x), r0 = __builtin_amdgcn_readfirstlane(ch.y), r1 = __builtin_amdgcn_readfirstlane(ch.z);
-    const int first = a.off[u], len = user_len(a, u);
+    const int u = __builtin_amdgcn_readfirstlane(ch.x), len = user_len(a, u);
     const int key0 = range * KEYS + wv * 32 * NK;
 
+    const int token = Turn::token(j);   // of each 32 keys, the one in this lane
     Random rnd;
-    if constexpr (DROP) rnd.init(a.rng);
-    u32x4_t kf[TK][NK], vf[TK][NK];
+    Turn turn;
+    if constexpr (DROP) {
+        rnd.init(a.rng);
+        turn.init(lane);
+    }
+    u32x4_t kf[TK][NK], vf[V_LDS ? 1 : TK][NK];
     f32x16_t dk[DT][NK], dv[DT][NK];
 #pragma unroll
     for (int n = 0; n < NK; ++n) {
-        const int t = key0 + 32 * n + j;
+        const int t = key0 + 32 * n + token;
         const uint16_t *k = a.K + u * a.k_user + hk * a.k_head + t * a.k_token + 8 * g;
         const uint16_t *v = a.V + u * a.v_user + hk * a.v_head + t * a.v_token + 8 * g;
 #pragma unroll
         for (int s = 0; s < TK; ++s) {
             kf[s][n] = t < len ? *reinterpret_cast<const u32x4_t *>(k + 16 * s) : (u32x4_t){0, 0, 0, 0};
-            vf[s][n] = t < len ? *reinterpret_cast<const u32x4_t *>(v + 16 * s) : (u32x4_t){0, 0, 0, 0};
+            if constexpr (!V_LDS) vf[s][n] = t < len ? *reinterpret_cast<const u32x4_t *>(v + 16 * s) : (u32x4_t){0, 0, 0, 0};
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) dk[d][n] = dv[d][n] = (f32x16_t)(0.f);
     }
+    if constexpr (V_LDS) {   // each wave its own keys
+        const uint16_t *v = a.V + u * a.v_user + hk * a.v_head;
+#pragma unroll
+        for (int i = 0; i < 32 * NK * HD / 8 / 64; ++i) {
+            const int p = i * 64 + lane, row = p / Rows<HD>::CHUNKS, chunk = ((p % Rows<HD>::CHUNKS) ^ Rows<HD>::number(row)) * 16;
+            const int t = key0 + (row & ~31) + Turn::token(row & 31);
+            load_to_lds(t < len ? reinterpret_cast<const char *>(v + t * a.v_token) + chunk : reinterpret_cast<const char *>(kZeroRow) + chunk,
+                        lds_address(v_lds) + Rows<HD>::matrix(32 * NK) * wv + i * Rows<HD>::GROUP);
+        }
+    }
     Reader<HD> rd;
     rd.init(lane);
     const uint32_t lds0 = lds_address(lds);
-    const int stages = range * KEYS < len ? (r1 - r0 + 63) >> 6 : 0;   // keys behind the history: zeros
-    // One wave notes stage st's rows.
-    auto note = [&](int st) {
-        RowsMeta &x = meta[st % 3];
-        const int r = r0 + 64 * st + lane;
-        const bool exists = r < r1;
-        const Place p = place_of(a, first, hk, exists ? r : r0);
-        const int limit = exists ? limit_of(a, p, len) : 0;
-        const int64_t stat = ((int64_t)p.cand * a.H_q + p.head) * a.L_q + p.query;
-        const bool sees = limit > 0;
-        const float lse = a.lse[stat], D = a.delta[stat];
-        x.q[lane] = reinterpret_cast<const char *>(sees ? reinterpret_cast<const uint16_t *>(a.Q) + p.cand * a.q_cand + p.head * a.q_head + p.query * a.q_query
-                                                        : reinterpret_cast<const uint16_t *>(kZeroRow));
-        x.dy[lane] = reinterpret_cast<const char *>(sees ? a.dO + p.cand * a.do_cand + p.head * a.do_head + p.query * a.do_query
-                                                         : reinterpret_cast<const uint16_t *>(kZeroRow));
-        x.shift[lane] = sees ? -lse * kLog2e : neg_inf();
-        x.D[lane] = sees ? D : 0.f;
-        x.limit[lane] = limit;
-        x.row[lane] = p.cand * a.L_q + p.query;
-        x.head[lane] = p.head;
-        int least = exists ? limit : len, most = limit;
+    const int stages = range * KEYS < len ? __builtin_amdgcn_readfirstlane(ch.z) : 0;   // keys behind the history: zeros
+    const char *from_notes = reinterpret_cast<const char *>(a.notes + (int64_t)hk * a.n_notes + ch.y) + 16 * lane;
+    auto load_notes = [&](int st) {
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            least = min(least, __shfl_xor(least, d));
-            most = max(most, __shfl_xor(most, d));
-        }
-        if (lane == 0) {
-            x.least = least;
-            x.most = most;
-        }
+        for (int i = 0; i < 3; ++i) load_to_lds(from_notes + st * 3072 + 1024 * i, lds_address(&notes[st % 3]) + 1024 * i);
     };
     auto load = [&](int st) {
-        const RowsMeta &x = meta[st % 3];
+        const RowNotes &x = notes[st % 3];
         const uint32_t to = lds0 + (st & 1) * 2 * STAGE;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int p = (i * WAVES + wv) * 64 + lane, row = p / Rows<HD>::CHUNKS;
             const int chunk = ((p % Rows<HD>::CHUNKS) ^ Rows<HD>::number(row)) * 16;
-            load_to_lds(x.q[row] + chunk, to + (i * WAVES + wv) * 1024);
-            load_to_lds(x.dy[row] + chunk, to + STAGE + (i * WAVES + wv) * 1024);
+            load_to_lds(static_cast<const char *>(x.q[row]) + chunk, to + (i * WAVES + wv) * Rows<HD>::GROUP);
+            load_to_lds(static_cast<const char *>(x.dy[row]) + chunk, to + STAGE + (i * WAVES + wv) * Rows<HD>::GROUP);
         }
     };
     if (stages > 0) {
-        if (wv == 0) note(0);
-        if (wv == 1 % WAVES && stages > 1) note(1);
+        if (wv == 0) load_notes(0);
+        if (wv == 0 && stages > 1) load_notes(1);
+        landed();
         __syncthreads();
         load(0);
     }
@@ -319,12 +311,13 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_dkv_kernel(TrainArgs a) {
         landed();
         __syncthreads();   // stage st and the notes of the next are there, and the other buffer has been read
         if (st + 1 < stages) load(st + 1);
-        if (wv == (st & (WAVES - 1)) && st + 2 < stages) note(st + 2);
-        const RowsMeta &x = meta[st % 3];
-        const int least = __builtin_amdgcn_readfirstlane(x.least);
-        if (__builtin_amdgcn_readfirstlane(x.most) <= key0) continue;   // no row sees the wave's keys
+        if (wv == 0 && st + 2 < stages) load_notes(st + 2);
+        const RowNotes &x = notes[st % 3];
+        const int limit = x.limit[lane];
+        if (!__ballot(limit > key0)) continue;   // no row sees the wave's keys
+        const bool partly = __ballot(limit < key0 + 32 * NK) != 0;
         const char *Q = lds[st & 1][0], *Y = lds[st & 1][1];
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             f32x16_t S[NK], dP[NK];
 #pragma unroll
@@ -335,7 +328,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_dkv_kernel(TrainArgs a) {
 #pragma unroll
                 for (int n = 0; n < NK; ++n) {
                     S[n] = mfma32(qf, kf[s][n], S[n]);
-                    dP[n] = mfma32(yf, vf[s][n], dP[n]);
+                    dP[n] = mfma32(yf, V_LDS ? rd.direct(v_lds + Rows<HD>::matrix(32 * NK) * wv, n, s) : vf[V_LDS ? 0 : s][n], dP[n]);
                 }
             }
             f32x4_t shift[4], D[4];
@@ -350,25 +343,15 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_dkv_kernel(TrainArgs a) {
                 float p[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[n][i], a.scale_log2, shift[i >> 2][i & 3]));
-                if (key0 + 32 * n + 32 > least) {
+                if (partly) {
                     asm volatile("");
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (key0 + 32 * n + j >= x.limit[32 * h + 8 * (i >> 2) + 4 * g + (i & 3)]) p[i] = 0.f;
+                        if (key0 + 32 * n + token >= x.limit[32 * h + 8 * (i >> 2) + 4 * g + (i & 3)]) p[i] = 0.f;
                 }
-                uint32_t stays = 0xFFFFFFFFu;
-                if constexpr (DROP) {
-                    // Lane (g, j) decides row j's tokens 8 w + 4 g + e; bit j (of half g) of ballot 4 w + e is that token's row j.
-                    const u32x4_t w = rnd.weights((key0 >> 5) + n, g, (uint32_t)x.row[32 * h + j], (uint32_t)x.head[32 * h + j]);
-                    stays = 0;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint64_t b = __ballot(((w[i >> 2] >> (8 * (i & 3))) & 255u) >= a.edge);
-                        const int t = 8 * (i >> 2) + (i & 3);
-                        stays = j == t ? (uint32_t)b : j == t + 4 ? (uint32_t)(b >> 32) : stays;
-                    }
-                    stays >>= 4 * g;
-                }
+                uint32_t stays = 0;
+                if constexpr (DROP)
+                    stays = turn.rows(rnd.weights((key0 >> 5) + n, g, (uint32_t)x.row[32 * h + j], (uint32_t)x.head[32 * h + j]), a.edge) >> (4 * g);
                 float ds[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -400,7 +383,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_dkv_kernel(TrainArgs a) {
     }
 #pragma unroll
     for (int n = 0; n < NK; ++n) {
-        const int t = key0 + 32 * n + j;
+        const int t = key0 + 32 * n + token;
         if (t >= a.L_kv) continue;
         if (ch.w < 0) {
             const float by = t < len ? 1.f : 0.f;   // what a key behind the history has gathered is no gradient
@@ -453,9 +436,10 @@ __global__ void __launch_bounds__(256) train_dkv_join_kernel(TrainArgs a) {
     }
 }
 
-template <int HD, int NT, int NK, int WAVES>
+template <int HD, int NT, int WAVES, int NK, int KW>
 hipError_t launch(const TrainArgs &a, hipStream_t s) {
-    constexpr int ROWS = 32 * NT * WAVES, KEYS = 32 * NK * WAVES, EACH = 1024 / HD;
+    constexpr int ROWS = 32 * NT * WAVES, KEYS = 32 * NK * KW, EACH = 1024 / HD;
+    static_assert(KEYS == kKeys, "the layout's chunks");
     hipError_t e;
     if (a.tiles > 0) {
         const dim3 grid((unsigned)(((int64_t)a.tiles * a.H_kv * a.splits + 7) / 8 * 8));
@@ -468,8 +452,8 @@ hipError_t launch(const TrainArgs &a, hipStream_t s) {
         }
     }
     const dim3 grid((unsigned)(((int64_t)a.chunks * a.H_kv * ((a.L_kv + KEYS - 1) / KEYS) + 7) / 8 * 8));
-    if (a.edge) hipLaunchKernelGGL((train_dkv_kernel<HD, NK, WAVES, true>), grid, dim3(64 * WAVES), 0, s, a);
-    else hipLaunchKernelGGL((train_dkv_kernel<HD, NK, WAVES, false>), grid, dim3(64 * WAVES), 0, s, a);
+    if (a.edge) hipLaunchKernelGGL((train_dkv_kernel<HD, NK, KW, true>), grid, dim3(64 * KW), 0, s, a);
+    else hipLaunchKernelGGL((train_dkv_kernel<HD, NK, KW, false>), grid, dim3(64 * KW), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess || a.slots == 0) return e;
     hipLaunchKernelGGL((train_dkv_join_kernel<HD>), dim3((unsigned)std::min<int64_t>(((int64_t)a.B_u * a.H_kv * a.L_kv + EACH - 1) / EACH, 1 << 16)), dim3(256), 0, s, a);
     return hipGetLastError();
@@ -478,7 +462,7 @@ hipError_t launch(const TrainArgs &a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_train_backward(const TrainArgs &a, const TrainLayout &, int head_dim, hipStream_t s) {
-    return head_dim == 128 ? launch<128, 1, 1, 8>(a, s) : launch<64, 1, 1, 8>(a, s);
+    return head_dim == 128 ? launch<128, 1, 8, 1, 8>(a, s) : launch<64, 1, 8, 1, 8>(a, s);
 }
 
 }  // namespace ikbo

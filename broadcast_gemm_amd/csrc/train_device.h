@@ -37,45 +37,50 @@ __device__ __forceinline__ float max_halves(float x) {
 
 // ---- staged matrices -----------------------------------------------------------------------
 //
-// Rows of HD bf16 elements, their 16-byte chunks permuted by an XOR with a number of the row.  A 16-byte read of a wave
-// is served in sets of 16 lanes that hold each j % 16 once: the numbers of 16 rows (8 pairs of rows at HD 64, which share
-// 256 bytes) differ.  A transposed read takes 64 bytes of each of 4 neighbouring rows: their numbers differ in the bits
-// above those of 4 chunks.
+// Rows of HD bf16 elements in groups of 1 KB (what one load of a wave fills), each row's 16-byte chunks permuted by an
+// XOR with a number of the row.  A 16-byte read of a wave is served in sets of 16 lanes that hold each j % 16 once; a
+// transposed read takes 64 bytes of each of 4 neighbouring rows.  HD 128: the 4 rows of a group differ in the bits above
+// those of 4 chunks, and groups are set off by a chunk, so that the place of step s needs s / 2 alone (fewer registers).  HD 64:
+// pairs of rows share 256 bytes, and the number has 3 bits.  Measured without conflicts: 256 bytes a cycle for both reads.
 template <int HD>
 struct Rows {
-    static constexpr int BYTES = HD * 2, CHUNKS = HD / 8;
+    static constexpr int BYTES = HD * 2, CHUNKS = HD / 8, EACH = 1024 / BYTES, GROUP = HD == 128 ? 1040 : 1024;
+    static constexpr int matrix(int rows) { return rows / EACH * GROUP; }
     static __device__ __forceinline__ int number(int row) {
-        return HD == 128 ? (row & 3) << 2 | ((row >> 2) & 3) : ((row >> 1) & 1) << 2 | ((row >> 2) & 3);
+        return HD == 128 ? (row & 3) << 2 : ((row >> 1) & 1) << 2 | ((row >> 2) & 3);
     }
-    static __device__ __forceinline__ int at(int row, int chunk) { return row * BYTES + ((chunk ^ number(row)) << 4); }
+    static __device__ __forceinline__ int at(int row, int chunk) {
+        return row / EACH * GROUP + row % EACH * BYTES + ((chunk ^ number(row)) << 4);
+    }
 };
 
-// A lane's reads of a staged matrix.  Rows 32 t + j of step s: direct(s) + 32 t rows.  Rows 16 s + 4 g + {0..3} (and
-// 8 behind) of column 32 d + j: turned(d) + 16 s rows, + 8 rows; the rows' numbers repeat after 16.
+// A lane's reads of a staged matrix: row 32 t + j, step s of its elements; and rows 16 s + 4 g + {0..3} (and 8 behind) of
+// column 32 d + j.  What depends on t, and on s there, is a constant.
 template <int HD>
 struct Reader {
-    int row[HD / 16], col[2][HD / 32];
+    static constexpr int HALF = HD == 128 ? 2 : 1;   // steps that stand side by side whatever the row
+    int row[HD / 16 / HALF], col[2 / HALF][HD / 32];
     __device__ __forceinline__ void init(int lane) {
         const int g = lane >> 5, j = lane & 31, i = lane & 15;
 #pragma unroll
-        for (int s = 0; s < HD / 16; ++s) row[s] = Rows<HD>::at(j, 2 * s + g);
+        for (int s = 0; s < HD / 16 / HALF; ++s) row[s] = Rows<HD>::at(j, 2 * HALF * s + g);
 #pragma unroll
         for (int d = 0; d < HD / 32; ++d)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {   // 16 lanes read 4 rows of 16 columns, 8 bytes each
+            for (int y = 0; y < 2 / HALF; ++y) {   // 16 lanes read 4 rows of 16 columns, 8 bytes each
                 const int c = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (i & 3);
                 col[y][d] = Rows<HD>::at(8 * y + 4 * g + (i >> 2), c >> 3) + 2 * (c & 7);
             }
     }
     __device__ __forceinline__ u32x4_t direct(const char *m, int t, int s) const {
-        return *reinterpret_cast<const u32x4_t *>(m + row[s] + 32 * t * Rows<HD>::BYTES);
+        return *reinterpret_cast<const u32x4_t *>(m + row[s / HALF] + s % HALF * 32 + Rows<HD>::matrix(32 * t));
     }
     __device__ __forceinline__ u32x4_t turned(const char *m, int s, int d) const {
         u32x2_t w[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-            w[y] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) i16x4_t *)(m + col[y][d] + 16 * s * Rows<HD>::BYTES)));
+            w[y] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t *)(
+                m + col[y / HALF][d] + (HALF == 2 ? Rows<HD>::matrix(8 * y) : 0) + Rows<HD>::matrix(16 * s))));
         return (u32x4_t){w[0][0], w[0][1], w[1][0], w[1][1]};
     }
 };
@@ -89,21 +94,13 @@ __device__ __forceinline__ void load_to_lds(const void *from, uint32_t to) {
 __device__ __forceinline__ uint32_t lds_address(const void *p) { return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)p; }
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// A block's LDS: two buffers of two matrices of 64 rows first, so that what is loaded straight into them stands in the
-// first 64 KB, which the loads' 16-bit base reaches.
-template <int HD, class T>
-struct Staged {
-    __align__(16) char buffer[2][2][64 * HD * 2];
-    __align__(16) T rest;
-};
-
 // What stands for a row that does not exist.
 __device__ const uint32_t kZeroRow[64] __attribute__((aligned(16))) = {};
 
 // A block's staging of 64 keys (or values) of one user and head.
 template <int HD, int WAVES>
 struct KeyLoads {
-    static constexpr int N = 64 * HD / 8 / (64 * WAVES), STAGE = 64 * HD * 2;
+    static constexpr int N = 64 * HD / 8 / (64 * WAVES);
     const char *from[N];
     int key[N];
     uint32_t chunk[N];
@@ -122,7 +119,7 @@ struct KeyLoads {
     __device__ __forceinline__ void next(uint32_t to, int wv, int len) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            load_to_lds(key[i] < len ? from[i] : reinterpret_cast<const char *>(kZeroRow) + chunk[i], to + (i * WAVES + wv) * 1024);
+            load_to_lds(key[i] < len ? from[i] : reinterpret_cast<const char *>(kZeroRow) + chunk[i], to + (i * WAVES + wv) * Rows<HD>::GROUP);
             key[i] += 64;
             from[i] += step;
         }
@@ -158,6 +155,52 @@ struct Random {
     // The bytes of the 16 tokens 32 `block` + 8 w + 4 g + e: byte e of word w.
     __device__ __forceinline__ u32x4_t weights(int block, int g, uint32_t row, uint32_t head) const {
         return philox(2 * block + g, row, head, offset, k0, k1);
+    }
+};
+
+// The same decisions with tokens in the lanes.  Lane (g, j) gives the words of row j, whose byte e of word w is that of token 8 w +
+// 4 g + e; it gets bit r: whether row r keeps token 8 (j % 4) + j & 4 + j / 8 (`token`).  The bytes are compared four at a time;
+// the bits of a row and its tokens are turned by exchanges with the lanes 16, 8, 4, 2 and 1 away.
+struct Turn {
+    uint32_t bytes16, bytes8, by4, by2, by1, own4, own2, own1, half;
+    static __device__ __forceinline__ int token(int j) { return 8 * (j & 3) + (j & 4) + (j >> 3); }
+    __device__ __forceinline__ void init(int lane) {
+        bytes16 = lane & 16 ? 0x07060302u : 0x05040100u;   // of the pair (lane with bit 4 set : clear)
+        bytes8 = lane & 8 ? 0x07030501u : 0x02060004u;     // of the pair (own : other)
+        by4 = lane & 4 ? 4 : 28;
+        by2 = lane & 2 ? 2 : 30;
+        by1 = lane & 1 ? 1 : 31;
+        own4 = lane & 4 ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
+        own2 = lane & 2 ? 0xCCCCCCCCu : 0x33333333u;
+        own1 = lane & 1 ? 0xAAAAAAAAu : 0x55555555u;
+        half = lane & 32 ? 0 : 4;
+    }
+    static __device__ __forceinline__ uint32_t pick(uint32_t mask, uint32_t a, uint32_t b) { return (mask & a) | (~mask & b); }
+    template <int CTRL>
+    static __device__ __forceinline__ uint32_t from(uint32_t x) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, true); }
+    __device__ __forceinline__ uint32_t rows(const u32x4_t &w, uint32_t edge) const {
+        // Bit 7 of each byte: whether it is at least `edge`.  The low 7 bits decide, unless the top ones differ.
+        const uint32_t low = (edge & 127) * 0x01010101u, top = edge & 128 ? 0u : 0xFFFFFFFFu;
+        uint32_t f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t d = (w[i] | 0x80808080u) - low;
+            f[i] = pick(w[i] ^ d, top, d);
+        }
+        uint32_t x = pick(0x80808080u, f[3], f[2] >> 1);
+        x = pick(0xC0C0C0C0u, x, f[1] >> 2);
+        x = (pick(0xE0E0E0E0u, x, f[0] >> 3) & 0xF0F0F0F0u) >> half;   // token 8 w + 4 g + e at bit 8 e + 4 g + w
+        const auto h = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        x = h[0] | h[1];
+        const auto q = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        x = __builtin_amdgcn_perm(q[1], q[0], bytes16);
+        x = __builtin_amdgcn_perm(x, from<0x128>(x), bytes8);                       // 8 lanes round in 16
+        uint32_t y = from<0x1B>(from<0x141>(x));                                    // 7 - j in 8, 3 - j in 4: 4 away
+        x = pick(own4, x, __builtin_amdgcn_alignbit(y, y, by4));
+        y = from<0x4E>(x);                                                          // 2 away
+        x = pick(own2, x, __builtin_amdgcn_alignbit(y, y, by2));
+        y = from<0xB1>(x);                                                          // 1 away
+        return pick(own1, x, __builtin_amdgcn_alignbit(y, y, by1));
     }
 };
 

@@ -17,10 +17,9 @@ constexpr float kSlack = 8.0f;
 
 template <int HD, int NT, int WAVES, bool DROP>
 __global__ void __launch_bounds__(64 * WAVES, 1) train_fwd_kernel(TrainArgs a) {
-    constexpr int TK = HD / 16, DT = HD / 32, STAGE = 64 * HD * 2, ROWS = 32 * NT * WAVES;
-    __shared__ Staged<HD, int[WAVES]> sh;
-    char (&lds)[2][2][STAGE] = sh.buffer;
-    int (&s_most)[WAVES] = sh.rest;
+    constexpr int TK = HD / 16, DT = HD / 32, STAGE = Rows<HD>::matrix(64), ROWS = 32 * NT * WAVES;
+    __shared__ __align__(16) char lds[2][2][STAGE];
+    __shared__ int s_most[WAVES];
     const int n_tiles = a.count[0];
     const int unit = unit_of((int)blockIdx.x, n_tiles * a.H_kv * a.splits);
     if (unit < 0) return;   // the whole block: no barrier has run

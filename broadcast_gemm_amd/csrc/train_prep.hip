@@ -14,8 +14,8 @@ namespace {
 constexpr int kThreads = 1024, kMaxUsers = IKBO_KV_MAX_USERS;
 constexpr int kPer = kMaxUsers / kThreads;     // users per thread, at most
 
-// Ints of LDS besides the counts per wave: the users' offsets, and prefix sums of tiles, chunks and slots.
-__host__ __device__ inline int prep_ints(int B_u, int waves) { return waves * B_u + 4 * (B_u + 1); }
+// Ints of LDS besides the counts per wave: the users' offsets, and prefix sums of tiles, chunks, slots and notes.
+__host__ __device__ inline int prep_ints(int B_u, int waves) { return waves * B_u + 5 * (B_u + 1); }
 
 // Exclusive prefix sums over the block's threads of v[0..N); totals in all.  sh: 16 N ints.
 template <int N>
@@ -80,13 +80,13 @@ __device__ void fill_padding(const TrainArgs &a, int head_dim, bool backward) {
 
 __global__ void __launch_bounds__(kThreads) train_prep_kernel(TrainArgs a, int waves, int tile_rows, int head_dim, int backward) {
     extern __shared__ int sh[];
-    __shared__ int s_scan[64];
+    __shared__ int s_scan[64];   // 16 waves, 4 sums
     if (blockIdx.x > 0) {
         fill_padding(a, head_dim, backward);
         return;
     }
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = tid >> 6, B = a.B_u;
-    int *cnt = sh, *offs = sh + waves * B, *t_at = offs + B + 1, *c_at = t_at + B + 1, *s_at = c_at + B + 1;
+    int *cnt = sh, *offs = sh + waves * B, *t_at = offs + B + 1, *c_at = t_at + B + 1, *s_at = c_at + B + 1, *n_at = s_at + B + 1;
     uint32_t err = 0;
     for (int i = tid; i < waves * B; i += kThreads) cnt[i] = 0;
     __syncthreads();
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) train_prep_kernel(TrainArgs a, int w
     scan(v, all, s_scan);
     // Chunks of a user's rows for dK and dV: even ones, one at least (it writes the zeros of a user without candidates);
     // the chunks of users with several have places for partial results.
-    int c[3] = {0, 0, 0}, n_t[kPer], n_c[kPer], at = v[0];
+    int c[4] = {0, 0, 0, 0}, n_t[kPer], n_c[kPer], at = v[0];
     const int GL = a.G * a.L_q;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
@@ -144,10 +144,11 @@ __global__ void __launch_bounds__(kThreads) train_prep_kernel(TrainArgs a, int w
             c[0] += n_t[e];
             c[1] += n_c[e];
             c[2] += n_c[e] > 1 ? n_c[e] : 0;
+            c[3] += (rows + 63) / 64;
             if (a.lens && (a.lens[u] < 0 || a.lens[u] > a.L_kv)) err |= kTrainStLens;
         }
     }
-    int total[3];
+    int total[4];
     scan(c, total, s_scan);
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
@@ -156,10 +157,12 @@ __global__ void __launch_bounds__(kThreads) train_prep_kernel(TrainArgs a, int w
             t_at[u] = c[0];
             c_at[u] = c[1];
             s_at[u] = c[2];
+            n_at[u] = c[3];
             if (backward) a.user_chunk[u] = make_int2(c[2], n_c[e] > 1 ? n_c[e] : 0);
             c[0] += n_t[e];
             c[1] += n_c[e];
             c[2] += n_c[e] > 1 ? n_c[e] : 0;
+            c[3] += (n_u[e] * GL + 63) / 64;
         }
     }
     if (tid == 0) {
@@ -179,12 +182,13 @@ __global__ void __launch_bounds__(kThreads) train_prep_kernel(TrainArgs a, int w
     for (int u = tid; u <= B; u += kThreads) a.off[u] = offs[u];
     for (int t = tid; t < total[0]; t += kThreads) {
         const int u = find(t_at, B, t);
-        a.tile[t] = make_int2(u, (t - t_at[u]) * tile_rows);
+        const int r = (t - t_at[u]) * tile_rows;
+        a.tile[t] = make_int4(u, r, n_at[u] + r / 64, 0);
     }
     for (int t = tid; t < total[1]; t += kThreads) {
         const int u = find(c_at, B, t), n = c_at[u + 1] - c_at[u], i = t - c_at[u];
-        const int rows = (offs[u + 1] - offs[u]) * GL, each = ((rows + n - 1) / n + 63) / 64 * 64;   // whole stages of 64 rows
-        a.chunk[t] = make_int4(u, min(rows, i * each), min(rows, (i + 1) * each), n > 1 ? s_at[u] + i : -1);
+        const int blocks = ((offs[u + 1] - offs[u]) * GL + 63) / 64, each = (blocks + n - 1) / n, from = min(blocks, i * each);
+        a.chunk[t] = make_int4(u, n_at[u] + from, min(blocks, from + each) - from, n > 1 ? s_at[u] + i : -1);
     }
     if (err) atomicOr(a.status, err);
 }

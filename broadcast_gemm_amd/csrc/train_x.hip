@@ -1,0 +1,485 @@
+// train_backward.hip -- the gradients of target attention (ikbo_attention_backward), probabilities recomputed.
+//
+// Two kernels, each with all it sums in registers, so that nothing is added up by atomics and no block waits for another:
+//
+// dQ: as the forward, a block takes a tile of rows against a range of keys: S^T = K Q^T, dP^T = V dO^T, P = exp(S - lse),
+// dS = P (dP - D), dQ^T += K^T dS^T.  It first forms D = rowsum(dO O), which the other kernel reads.  For a row that
+// sees no more than the first 64 keys D is the sum of P dP instead: with few keys the rounding of O shows in dP - D.
+//
+// dK and dV: a wave keeps 32 keys' K and V and their gradients in registers, and the block goes over a chunk of the
+// user's rows, staged in LDS 64 at a time: S = Q K^T, dP = dO V^T, dV^T += dO^T P, dK^T += Q^T dS.  Rows stand in the
+// results' rows here, so P and dS are the B operands as they stand.  The weights that stay are decided with the rows
+// in the lanes, as in the other kernels (one generator call for 16 tokens of a row), and the bits turned round by
+// ballots.  Chunks of one user are joined by a third launch, in their order.
+//
+// That is 7 products against the 5 that one pass needs; adding up dQ across key ranges instead would write and read 4
+// bytes an element for every range.  P and dS are rounded to bf16 for their products; all sums are float32.
+#include <algorithm>
+
+#include "train_device.h"
+
+namespace ikbo {
+namespace {
+
+template <int HD, int NT, int WAVES, bool DROP>
+__global__ void __launch_bounds__(64 * WAVES, 1) train_dq_kernel(TrainArgs a) {
+    constexpr int TK = HD / 16, DT = HD / 32, STAGE = 64 * HD * 2, ROWS = 32 * NT * WAVES;
+    __shared__ Staged<HD, int[WAVES]> sh;
+    char (&lds)[2][2][STAGE] = sh.buffer;
+    int (&s_most)[WAVES] = sh.rest;
+    const int n_tiles = a.count[0];
+    const int unit = unit_of((int)blockIdx.x, n_tiles * a.H_kv * a.splits);
+    if (unit < 0) return;   // the whole block: no barrier has run
+    const int tile = unit % n_tiles, hk = unit / n_tiles % a.H_kv, split = unit / n_tiles / a.H_kv;
+    const int tid = (int)threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5, j = lane & 31;
+    const int u = __builtin_amdgcn_readfirstlane(a.tile[tile].x), row0 = __builtin_amdgcn_readfirstlane(a.tile[tile].y);
+    const int first = a.off[u], n_rows = (a.off[u + 1] - first) * a.G * a.L_q, len = user_len(a, u);
+
+    const int r0 = row0 + wv * 32 * NT;
+    Place at[NT];
+    int limit[NT], most = 0, least = len;
+    bool live[NT];
+    u32x4_t qf[TK][NT], gf[TK][NT];
+    float shift[NT], D[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int r = r0 + 32 * n + j;
+        live[n] = r < n_rows;
+        at[n] = place_of(a, first, hk, live[n] ? r : 0);
+        limit[n] = live[n] ? limit_of(a, at[n], len) : 0;
+        const bool sees = limit[n] > 0;   // other rows are not read: they have no gradient, whatever theirs is
+        const uint16_t *q = a.Q + at[n].cand * a.q_cand + at[n].head * a.q_head + at[n].query * a.q_query + 8 * g;
+        const uint16_t *dy = a.dO + at[n].cand * a.do_cand + at[n].head * a.do_head + at[n].query * a.do_query + 8 * g;
+        const uint16_t *y = a.O + at[n].cand * a.o_cand + at[n].head * a.o_head + at[n].query * a.o_query + 8 * g;
+        const int64_t stat = ((int64_t)at[n].cand * a.H_q + at[n].head) * a.L_q + at[n].query;
+        float sum = 0.f;
+#pragma unroll
+        for (int s = 0; s < TK; ++s) {
+            qf[s][n] = sees ? *reinterpret_cast<const u32x4_t *>(q + 16 * s) : (u32x4_t){0, 0, 0, 0};
+            gf[s][n] = sees ? *reinterpret_cast<const u32x4_t *>(dy + 16 * s) : (u32x4_t){0, 0, 0, 0};
+            const u32x4_t of = sees ? *reinterpret_cast<const u32x4_t *>(y + 16 * s) : (u32x4_t){0, 0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sum = __builtin_fmaf(__builtin_bit_cast(float, of[e] << 16), __builtin_bit_cast(float, gf[s][n][e] << 16), sum);
+                sum = __builtin_fmaf(__builtin_bit_cast(float, of[e] & 0xFFFF0000u), __builtin_bit_cast(float, gf[s][n][e] & 0xFFFF0000u), sum);
+            }
+        }
+        D[n] = sum_halves(sum);
+        shift[n] = sees ? -a.lse[stat] * kLog2e : 0.f;
+        most = max(most, limit[n]);
+        if (live[n]) least = min(least, limit[n]);
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        most = max(most, __shfl_xor(most, d));
+        least = min(least, __shfl_xor(least, d));
+    }
+    most = __builtin_amdgcn_readfirstlane(most);
+    least = __builtin_amdgcn_readfirstlane(least);
+    if (lane == 0) s_most[wv] = most;
+    __syncthreads();
+    int end = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) end = max(end, s_most[w]);
+    const int key0 = split * a.split_keys;
+    end = min(end, key0 + a.split_keys);
+
+    Random rnd;
+    if constexpr (DROP) rnd.init(a.rng);
+    f32x16_t dq[DT][NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) dq[d][n] = (f32x16_t)(0.f);
+    KeyLoads<HD, WAVES> kl, vl;
+    kl.init(a.K + u * a.k_user + hk * a.k_head, a.k_token, key0, lane, wv);
+    vl.init(a.V + u * a.v_user + hk * a.v_head, a.v_token, key0, lane, wv);
+    Reader<HD> rd;
+    rd.init(lane);
+    const uint32_t lds0 = lds_address(lds);
+    const int stages = max(0, (end - key0 + 63) >> 6);
+    if (stages > 0) {
+        kl.next(lds0, wv, len);
+        vl.next(lds0 + STAGE, wv, len);
+    }
+    for (int st = 0; st < stages; ++st) {
+        landed();
+        __syncthreads();   // stage st is there, and its other buffer has been read
+        if (st + 1 < stages) {
+            const uint32_t to = lds0 + ((st + 1) & 1) * 2 * STAGE;
+            kl.next(to, wv, len);
+            vl.next(to + STAGE, wv, len);
+        }
+        const int t0 = key0 + 64 * st;
+        if (t0 >= most) continue;   // none of the wave's rows sees these keys
+        const char *K = lds[st & 1][0], *V = lds[st & 1][1];
+        f32x16_t S[2][NT], dP[2][NT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) S[h][n] = dP[h][n] = (f32x16_t)(0.f);
+#pragma unroll
+            for (int s = 0; s < TK; ++s) {
+                const u32x4_t kf = rd.direct(K, h, s), vf = rd.direct(V, h, s);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    S[h][n] = mfma32(kf, qf[s][n], S[h][n]);
+                    dP[h][n] = mfma32(vf, gf[s][n], dP[h][n]);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[h][n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[h][n][i], a.scale_log2, shift[n]));
+                if constexpr (DROP) {
+                    const u32x4_t w = rnd.weights((t0 >> 5) + h, g, (uint32_t)(at[n].cand * a.L_q + at[n].query), (uint32_t)at[n].head);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) dP[h][n][i] = ((w[i >> 2] >> (8 * (i & 3))) & 255u) >= a.edge ? dP[h][n][i] * a.keep : 0.f;
+                }
+            }
+        }
+        if (t0 + 64 > least) {
+            asm volatile("");   // stays a branch: as selects its body would be paid by every stage
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (t0 + 32 * h + 8 * (i >> 2) + 4 * g + (i & 3) >= limit[n]) S[h][n][i] = 0.f;
+        }
+        if (t0 == 0 && least <= 64) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float sum = 0.f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(S[h][n][i], dP[h][n][i], sum);
+                sum = sum_halves(sum);
+                D[n] = limit[n] <= 64 ? sum : D[n];
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            u32x4_t pf[2][NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = S[h][n][i] * (dP[h][n][i] - D[n]);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    pf[s][n] = (u32x4_t){pack_bf16x2(x[8 * s], x[8 * s + 1]), pack_bf16x2(x[8 * s + 2], x[8 * s + 3]),
+                                         pack_bf16x2(x[8 * s + 4], x[8 * s + 5]), pack_bf16x2(x[8 * s + 6], x[8 * s + 7])};
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const u32x4_t kt = rd.turned(K, 2 * h + s, d);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) dq[d][n] = mfma32(kt, pf[s][n], dq[d][n]);
+                }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        if (!live[n]) continue;
+        if (split == 0 && g == 0) a.delta[((int64_t)at[n].cand * a.H_q + at[n].head) * a.L_q + at[n].query] = D[n];
+        if (a.splits == 1) {
+            uint16_t *to = a.dQ + at[n].cand * a.dq_cand + at[n].head * a.dq_head + at[n].query * a.dq_query + 8 * g;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) *reinterpret_cast<u32x4_t *>(to + 32 * d + 16 * p) = eight_rows(dq[d][n], p, a.scale);
+        } else {
+            float *to = a.part + ((((int64_t)split * a.tiles + tile) * a.H_kv + hk) * ROWS + wv * 32 * NT + 32 * n + j) * HD + 4 * g;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<f32x4_t *>(to + 32 * d + 8 * q) = (f32x4_t){dq[d][n][4 * q], dq[d][n][4 * q + 1], dq[d][n][4 * q + 2], dq[d][n][4 * q + 3]};
+        }
+    }
+}
+
+// The parts of one row of dQ, by HD / 4 lanes, in the order of the keys.
+template <int HD>
+__global__ void __launch_bounds__(256) train_dq_join_kernel(TrainArgs a, int tile_rows) {
+    constexpr int LANES = HD / 4;
+    const int n_tiles = a.count[0], x = (int)threadIdx.x % LANES;
+    const int64_t i = (int64_t)blockIdx.x * (256 / LANES) + (int)threadIdx.x / LANES, n = (int64_t)n_tiles * a.H_kv * tile_rows;
+    if (i >= n) return;
+    const int in_tile = (int)(i % tile_rows), hk = (int)(i / tile_rows % a.H_kv), tile = (int)(i / tile_rows / a.H_kv);
+    const int u = a.tile[tile].x, r = a.tile[tile].y + in_tile, first = a.off[u];
+    if (r >= (a.off[u + 1] - first) * a.G * a.L_q) return;
+    const int64_t row0 = ((int64_t)tile * a.H_kv + hk) * tile_rows + in_tile, step = (int64_t)a.tiles * a.H_kv * tile_rows;
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) o += *reinterpret_cast<const f32x4_t *>(a.part + (row0 + s * step) * HD + 4 * x);
+    const Place p = place_of(a, first, hk, r);
+    *reinterpret_cast<u32x2_t *>(a.dQ + p.cand * a.dq_cand + p.head * a.dq_head + p.query * a.dq_query + 4 * x) =
+        (u32x2_t){pack_bf16x2(o[0] * a.scale, o[1] * a.scale), pack_bf16x2(o[2] * a.scale, o[3] * a.scale)};
+}
+
+// What the dK and dV kernel keeps of 64 staged rows besides Q and dO.
+struct RowsMeta {
+    const char *q[64], *dy[64];       // where they stand; a row that does not exist or sees nothing is zeros
+    float shift[64], D[64];           // -lse in base 2 (-inf for such a row: no weights), rowsum(dO O)
+    int limit[64], row[64], head[64]; // tokens it sees, b L_q + l, h
+    int least, most;
+};
+
+template <int HD, int NK, int WAVES, bool DROP>
+__global__ void __launch_bounds__(64 * WAVES, 1) train_dkv_kernel(TrainArgs a) {
+    constexpr int TK = HD / 16, DT = HD / 32, STAGE = 64 * HD * 2, KEYS = 32 * NK * WAVES, N = 64 * HD / 8 / (64 * WAVES);
+    __shared__ Staged<HD, RowsMeta[3]> sh;
+    char (&lds)[2][2][STAGE] = sh.buffer;
+    RowsMeta (&meta)[3] = sh.rest;
+    const int n_chunks = a.count[1], ranges = (a.L_kv + KEYS - 1) / KEYS;
+    const int unit = unit_of((int)blockIdx.x, n_chunks * a.H_kv * ranges);
+    if (unit < 0) return;   // the whole block: no barrier has run
+    const int range = unit % ranges, hk = unit / ranges % a.H_kv, c = unit / ranges / a.H_kv;   // neighbours share rows
+    const int tid = (int)threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5, j = lane & 31;
+    const int4 ch = a.chunk[c];
+    const int u = __builtin_amdgcn_readfirstlane(ch.x), r0 = __builtin_amdgcn_readfirstlane(ch.y), r1 = __builtin_amdgcn_readfirstlane(ch.z);
+    const int first = a.off[u], len = user_len(a, u);
+    const int key0 = range * KEYS + wv * 32 * NK;
+
+    Random rnd;
+    if constexpr (DROP) rnd.init(a.rng);
+    u32x4_t kf[TK][NK], vf[TK][NK];
+    f32x16_t dk[DT][NK], dv[DT][NK];
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+        const int t = key0 + 32 * n + j;
+        const uint16_t *k = a.K + u * a.k_user + hk * a.k_head + t * a.k_token + 8 * g;
+        const uint16_t *v = a.V + u * a.v_user + hk * a.v_head + t * a.v_token + 8 * g;
+#pragma unroll
+        for (int s = 0; s < TK; ++s) {
+            kf[s][n] = t < len ? *reinterpret_cast<const u32x4_t *>(k + 16 * s) : (u32x4_t){0, 0, 0, 0};
+            vf[s][n] = t < len ? *reinterpret_cast<const u32x4_t *>(v + 16 * s) : (u32x4_t){0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) dk[d][n] = dv[d][n] = (f32x16_t)(0.f);
+    }
+    Reader<HD> rd;
+    rd.init(lane);
+    const uint32_t lds0 = lds_address(lds);
+    const int stages = range * KEYS < len ? (r1 - r0 + 63) >> 6 : 0;   // keys behind the history: zeros
+    // One wave notes stage st's rows.
+    auto note = [&](int st) {
+        RowsMeta &x = meta[st % 3];
+        const int r = r0 + 64 * st + lane;
+        const bool exists = r < r1;
+        const Place p = place_of(a, first, hk, exists ? r : r0);
+        const int limit = exists ? limit_of(a, p, len) : 0;
+        const int64_t stat = ((int64_t)p.cand * a.H_q + p.head) * a.L_q + p.query;
+        const bool sees = limit > 0;
+        const float lse = a.lse[stat], D = a.delta[stat];
+        x.q[lane] = reinterpret_cast<const char *>(sees ? reinterpret_cast<const uint16_t *>(a.Q) + p.cand * a.q_cand + p.head * a.q_head + p.query * a.q_query
+                                                        : reinterpret_cast<const uint16_t *>(kZeroRow));
+        x.dy[lane] = reinterpret_cast<const char *>(sees ? a.dO + p.cand * a.do_cand + p.head * a.do_head + p.query * a.do_query
+                                                         : reinterpret_cast<const uint16_t *>(kZeroRow));
+        x.shift[lane] = sees ? -lse * kLog2e : neg_inf();
+        x.D[lane] = sees ? D : 0.f;
+        x.limit[lane] = limit;
+        x.row[lane] = p.cand * a.L_q + p.query;
+        x.head[lane] = p.head;
+        int least = exists ? limit : len, most = limit;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            least = min(least, __shfl_xor(least, d));
+            most = max(most, __shfl_xor(most, d));
+        }
+        if (lane == 0) {
+            x.least = least;
+            x.most = most;
+        }
+    };
+    auto load = [&](int st) {
+        const RowsMeta &x = meta[st % 3];
+        const uint32_t to = lds0 + (st & 1) * 2 * STAGE;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int p = (i * WAVES + wv) * 64 + lane, row = p / Rows<HD>::CHUNKS;
+            const int chunk = ((p % Rows<HD>::CHUNKS) ^ Rows<HD>::number(row)) * 16;
+            load_to_lds(x.q[row] + chunk, to + (i * WAVES + wv) * 1024);
+            load_to_lds(x.dy[row] + chunk, to + STAGE + (i * WAVES + wv) * 1024);
+        }
+    };
+    if (stages > 0) {
+        if (wv == 0) note(0);
+        if (wv == 1 % WAVES && stages > 1) note(1);
+        __syncthreads();
+        load(0);
+    }
+    for (int st = 0; st < stages; ++st) {
+        landed();
+        __syncthreads();   // stage st and the notes of the next are there, and the other buffer has been read
+        if (st + 1 < stages) load(st + 1);
+        if (wv == (st & (WAVES - 1)) && st + 2 < stages) note(st + 2);
+        const RowsMeta &x = meta[st % 3];
+        const int least = __builtin_amdgcn_readfirstlane(x.least);
+        if (__builtin_amdgcn_readfirstlane(x.most) <= key0) continue;   // no row sees the wave's keys
+        const char *Q = lds[st & 1][0], *Y = lds[st & 1][1];
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            f32x16_t S[NK], dP[NK];
+#pragma unroll
+            for (int n = 0; n < NK; ++n) S[n] = dP[n] = (f32x16_t)(0.f);
+#pragma unroll
+            for (int s = 0; s < TK; ++s) {
+                const u32x4_t qf = rd.direct(Q, h, s), yf = rd.direct(Y, h, s);
+#pragma unroll
+                for (int n = 0; n < NK; ++n) {
+                    S[n] = mfma32(qf, kf[s][n], S[n]);
+                    dP[n] = mfma32(yf, vf[s][n], dP[n]);
+                }
+            }
+            f32x4_t shift[4], D[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                shift[q] = *reinterpret_cast<const f32x4_t *>(x.shift + 32 * h + 8 * q + 4 * g);
+                D[q] = *reinterpret_cast<const f32x4_t *>(x.D + 32 * h + 8 * q + 4 * g);
+            }
+            u32x4_t pf[2][NK], sf[2][NK];
+#pragma unroll
+            for (int n = 0; n < NK; ++n) {
+                float p[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[n][i], a.scale_log2, shift[i >> 2][i & 3]));
+                if (key0 + 32 * n + 32 > least) {
+                    asm volatile("");
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (key0 + 32 * n + j >= x.limit[32 * h + 8 * (i >> 2) + 4 * g + (i & 3)]) p[i] = 0.f;
+                }
+                uint32_t stays = 0xFFFFFFFFu;
+                if constexpr (DROP) {
+                    // Lane (g, j) decides row j's tokens 8 w + 4 g + e; bit j (of half g) of ballot 4 w + e is that token's row j.
+                    const u32x4_t w = rnd.weights((key0 >> 5) + n, g, (uint32_t)x.row[32 * h + j], (uint32_t)x.head[32 * h + j]);
+                    stays = 0;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t b = __ballot(((w[i >> 2] >> (8 * (i & 3))) & 255u) >= a.edge);
+                        const int t = 8 * (i >> 2) + (i & 3);
+                        stays = j == t ? (uint32_t)b : j == t + 4 ? (uint32_t)(b >> 32) : stays;
+                    }
+                    stays >>= 4 * g;
+                }
+                float ds[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float dp = dP[n][i];
+                    if constexpr (DROP) dp = (stays >> (8 * (i >> 2) + (i & 3))) & 1 ? dp * a.keep : 0.f;
+                    ds[i] = p[i] * (dp - D[i >> 2][i & 3]);
+                    if constexpr (DROP) p[i] = (stays >> (8 * (i >> 2) + (i & 3))) & 1 ? p[i] : 0.f;
+                }
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    pf[s][n] = (u32x4_t){pack_bf16x2(p[8 * s], p[8 * s + 1]), pack_bf16x2(p[8 * s + 2], p[8 * s + 3]),
+                                         pack_bf16x2(p[8 * s + 4], p[8 * s + 5]), pack_bf16x2(p[8 * s + 6], p[8 * s + 7])};
+                    sf[s][n] = (u32x4_t){pack_bf16x2(ds[8 * s], ds[8 * s + 1]), pack_bf16x2(ds[8 * s + 2], ds[8 * s + 3]),
+                                         pack_bf16x2(ds[8 * s + 4], ds[8 * s + 5]), pack_bf16x2(ds[8 * s + 6], ds[8 * s + 7])};
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const u32x4_t yt = rd.turned(Y, 2 * h + s, d), qt = rd.turned(Q, 2 * h + s, d);
+#pragma unroll
+                    for (int n = 0; n < NK; ++n) {
+                        dv[d][n] = mfma32(yt, pf[s][n], dv[d][n]);
+                        dk[d][n] = mfma32(qt, sf[s][n], dk[d][n]);
+                    }
+                }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NK; ++n) {
+        const int t = key0 + 32 * n + j;
+        if (t >= a.L_kv) continue;
+        if (ch.w < 0) {
+            const float by = t < len ? 1.f : 0.f;   // what a key behind the history has gathered is no gradient
+            uint16_t *k = a.dK + u * a.dk_user + hk * a.dk_head + t * a.dk_token + 8 * g, *v = a.dV + u * a.dv_user + hk * a.dv_head + t * a.dv_token + 8 * g;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const u32x4_t x = eight_rows(dk[d][n], p, a.scale), y = eight_rows(dv[d][n], p, a.keep), zero = {0, 0, 0, 0};
+                    *reinterpret_cast<u32x4_t *>(k + 32 * d + 16 * p) = by > 0.f ? x : zero;
+                    *reinterpret_cast<u32x4_t *>(v + 32 * d + 16 * p) = by > 0.f ? y : zero;
+                }
+        } else {
+            const int64_t row = ((int64_t)ch.w * a.H_kv + hk) * a.L_kv + t;
+            float *k = a.part_dk + row * HD + 4 * g, *v = a.part_dv + row * HD + 4 * g;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    *reinterpret_cast<f32x4_t *>(k + 32 * d + 8 * q) = (f32x4_t){dk[d][n][4 * q], dk[d][n][4 * q + 1], dk[d][n][4 * q + 2], dk[d][n][4 * q + 3]};
+                    *reinterpret_cast<f32x4_t *>(v + 32 * d + 8 * q) = (f32x4_t){dv[d][n][4 * q], dv[d][n][4 * q + 1], dv[d][n][4 * q + 2], dv[d][n][4 * q + 3]};
+                }
+        }
+    }
+}
+
+// One key's dK and dV from the chunks of its user, by HD / 4 lanes, in the order of the chunks.
+template <int HD>
+__global__ void __launch_bounds__(256) train_dkv_join_kernel(TrainArgs a) {
+    constexpr int LANES = HD / 4;
+    const int x = (int)threadIdx.x % LANES;
+    const int64_t heads = (int64_t)a.L_kv * a.H_kv;
+    for (int64_t i = (int64_t)blockIdx.x * (256 / LANES) + (int)threadIdx.x / LANES; i < heads * a.B_u; i += (int64_t)gridDim.x * (256 / LANES)) {
+        const int u = (int)(i / heads), hk = (int)(i / a.L_kv % a.H_kv), t = (int)(i % a.L_kv);
+        const int2 mine = a.user_chunk[u];
+        if (mine.y == 0) continue;   // written by its one chunk
+        f32x4_t k = {0.f, 0.f, 0.f, 0.f}, v = {0.f, 0.f, 0.f, 0.f};
+        if (t < user_len(a, u)) {
+    #pragma unroll 4
+            for (int c = 0; c < mine.y; ++c) {
+                const int64_t row = ((int64_t)(mine.x + c) * a.H_kv + hk) * a.L_kv + t;
+                k += *reinterpret_cast<const f32x4_t *>(a.part_dk + row * HD + 4 * x);
+                v += *reinterpret_cast<const f32x4_t *>(a.part_dv + row * HD + 4 * x);
+            }
+            k *= a.scale;
+            v *= a.keep;
+        }
+        *reinterpret_cast<u32x2_t *>(a.dK + u * a.dk_user + hk * a.dk_head + t * a.dk_token + 4 * x) = (u32x2_t){pack_bf16x2(k[0], k[1]), pack_bf16x2(k[2], k[3])};
+        *reinterpret_cast<u32x2_t *>(a.dV + u * a.dv_user + hk * a.dv_head + t * a.dv_token + 4 * x) = (u32x2_t){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    }
+}
+
+template <int HD, int NT, int WAVES, int NK, int KW>
+hipError_t launch(const TrainArgs &a, hipStream_t s) {
+    constexpr int ROWS = 32 * NT * WAVES, KEYS = 32 * NK * KW, EACH = 1024 / HD;
+    static_assert(KEYS > 0, "the layout's chunks");
+    hipError_t e;
+    if (a.tiles > 0) {
+        const dim3 grid((unsigned)(((int64_t)a.tiles * a.H_kv * a.splits + 7) / 8 * 8));
+        if (a.edge) hipLaunchKernelGGL((train_dq_kernel<HD, NT, WAVES, true>), grid, dim3(64 * WAVES), 0, s, a);
+        else hipLaunchKernelGGL((train_dq_kernel<HD, NT, WAVES, false>), grid, dim3(64 * WAVES), 0, s, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (a.splits > 1) {
+            hipLaunchKernelGGL((train_dq_join_kernel<HD>), dim3((unsigned)(((int64_t)a.tiles * a.H_kv * ROWS + EACH - 1) / EACH)), dim3(256), 0, s, a, ROWS);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+    }
+    const dim3 grid((unsigned)(((int64_t)a.chunks * a.H_kv * ((a.L_kv + KEYS - 1) / KEYS) + 7) / 8 * 8));
+    if (a.edge) hipLaunchKernelGGL((train_dkv_kernel<HD, NK, KW, true>), grid, dim3(64 * KW), 0, s, a);
+    else hipLaunchKernelGGL((train_dkv_kernel<HD, NK, KW, false>), grid, dim3(64 * KW), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess || a.slots == 0) return e;
+    hipLaunchKernelGGL((train_dkv_join_kernel<HD>), dim3((unsigned)std::min<int64_t>(((int64_t)a.B_u * a.H_kv * a.L_kv + EACH - 1) / EACH, 1 << 16)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_train_backward(const TrainArgs &a, const TrainLayout &, int head_dim, hipStream_t s) {
+    return head_dim == 128 ? launch<128, 1, 8, 2, 4>(a, s) : launch<64, 1, 8, 1, 8>(a, s);
+}
+
+}  // namespace ikbo
