@@ -16,6 +16,7 @@ namespace {
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 constexpr int64_t kInt = std::numeric_limits<int32_t>::max();
+constexpr int64_t kMaxToken = 1 << 24;   // elements from token to token
 constexpr int kMaxHeads = 4096, kTileRows = 256, kThreads = 512, kCus = 256;
 
 // Probability as whole steps of 1 / of; 0 and `of` only for probabilities of 0 and 1.
@@ -45,6 +46,7 @@ int check(const ikbo_attention_args *a, bool backward) {
         if (strides[i] < 0) return IKBO_ERR_INVALID_ARG;
     for (int i = 0; i < (backward ? 24 : 12); ++i)
         if (strides[i] % 8 != 0) return IKBO_ERR_ALIGNMENT;
+    if (a->k_token > kMaxToken || a->v_token > kMaxToken) return IKBO_ERR_UNSUPPORTED;
     const bool rows = a->B_c > 0;
     if (!a->status || !a->workspace || a->workspace_bytes < need || (a->dropout > 0 && !a->rng)) return IKBO_ERR_INVALID_ARG;
     if (rows && (!a->Q || !a->K || !a->V || !a->O || !a->lse || !a->map)) return IKBO_ERR_INVALID_ARG;

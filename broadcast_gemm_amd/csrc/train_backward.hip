@@ -31,10 +31,10 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_dq_kernel(TrainArgs a) {
     const int tile = unit % n_tiles, hk = unit / n_tiles % a.H_kv, split = unit / n_tiles / a.H_kv;
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5, j = lane & 31;
     const int u = __builtin_amdgcn_readfirstlane(a.tile[tile].x), row0 = __builtin_amdgcn_readfirstlane(a.tile[tile].y);
-    const int first = a.off[u], n_rows = (a.off[u + 1] - first) * a.G * a.L_q, len = user_len(a, u);
+    const int first = a.off[u], n_rows = (a.off[u + 1] - first) * a.G * a.L_q, len = __builtin_amdgcn_readfirstlane(user_len(a, u));
 
     const int r0 = row0 + wv * 32 * NT;
-    Place at[NT];
+    uint32_t row[NT], head[NT];
     int limit[NT], most = 0, least = len;
     bool live[NT];
     u32x4_t qf[TK][NT], gf[TK][NT];
@@ -43,13 +43,15 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_dq_kernel(TrainArgs a) {
     for (int n = 0; n < NT; ++n) {
         const int r = r0 + 32 * n + j;
         live[n] = r < n_rows;
-        at[n] = place_of(a, first, hk, live[n] ? r : 0);
-        limit[n] = live[n] ? limit_of(a, at[n], len) : 0;
+        const Place at = place_of(a, first, hk, live[n] ? r : 0);
+        limit[n] = live[n] ? limit_of(a, at, len) : 0;
+        row[n] = (uint32_t)(at.cand * a.L_q + at.query);
+        head[n] = (uint32_t)at.head;
         const bool sees = limit[n] > 0;   // other rows are not read: they have no gradient, whatever theirs is
-        const uint16_t *q = a.Q + at[n].cand * a.q_cand + at[n].head * a.q_head + at[n].query * a.q_query + 8 * g;
-        const uint16_t *dy = a.dO + at[n].cand * a.do_cand + at[n].head * a.do_head + at[n].query * a.do_query + 8 * g;
-        const uint16_t *y = a.O + at[n].cand * a.o_cand + at[n].head * a.o_head + at[n].query * a.o_query + 8 * g;
-        const int64_t stat = ((int64_t)at[n].cand * a.H_q + at[n].head) * a.L_q + at[n].query;
+        const uint16_t *q = a.Q + at.cand * a.q_cand + at.head * a.q_head + at.query * a.q_query + 8 * g;
+        const uint16_t *dy = a.dO + at.cand * a.do_cand + at.head * a.do_head + at.query * a.do_query + 8 * g;
+        const uint16_t *y = a.O + at.cand * a.o_cand + at.head * a.o_head + at.query * a.o_query + 8 * g;
+        const int64_t stat = ((int64_t)at.cand * a.H_q + at.head) * a.L_q + at.query;
         float sum = 0.f;
 #pragma unroll
         for (int s = 0; s < TK; ++s) {
@@ -89,116 +91,115 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_dq_kernel(TrainArgs a) {
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int d = 0; d < DT; ++d) dq[d][n] = (f32x16_t)(0.f);
-    KeyLoads<HD, WAVES> kl, vl;
-    kl.init(a.K + u * a.k_user + hk * a.k_head, a.k_token, key0, lane, wv);
-    vl.init(a.V + u * a.v_user + hk * a.v_head, a.v_token, key0, lane, wv);
+    KeyLoads<HD, WAVES> keys;
+    keys.init(a, u, hk, lane, wv);
     Reader<HD> rd;
     rd.init(lane);
     const uint32_t lds0 = lds_address(lds);
     const int stages = max(0, (end - key0 + 63) >> 6);
-    if (stages > 0) {
-        kl.next(lds0, wv, len);
-        vl.next(lds0 + STAGE, wv, len);
-    }
+    if (stages > 0) keys.load(lds0, wv, key0, len);
     for (int st = 0; st < stages; ++st) {
         landed();
         __syncthreads();   // stage st is there, and its other buffer has been read
-        if (st + 1 < stages) {
-            const uint32_t to = lds0 + ((st + 1) & 1) * 2 * STAGE;
-            kl.next(to, wv, len);
-            vl.next(to + STAGE, wv, len);
-        }
+        if (st + 1 < stages) keys.load(lds0 + ((st + 1) & 1) * 2 * STAGE, wv, key0 + 64 * st + 64, len);
         const int t0 = key0 + 64 * st;
         if (t0 >= most) continue;   // none of the wave's rows sees these keys
         const char *K = lds[st & 1][0], *V = lds[st & 1][1];
-        f32x16_t S[2][NT], dP[2][NT];
+        // P in S, and dP, of keys t0 + 32 h + 8 (i / 4) + 4 g + i % 4.
+        f32x16_t S[NT], dP[NT];
+        auto probabilities = [&](int h) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) S[h][n] = dP[h][n] = (f32x16_t)(0.f);
+            for (int n = 0; n < NT; ++n) S[n] = dP[n] = (f32x16_t)(0.f);
+            u32x4_t kf[2], vf[2];
+            kf[0] = rd.direct(K, h, 0);
+            vf[0] = rd.direct(V, h, 0);
 #pragma unroll
             for (int s = 0; s < TK; ++s) {
-                const u32x4_t kf = rd.direct(K, h, s), vf = rd.direct(V, h, s);
+                if (s + 1 < TK) {
+                    kf[(s + 1) & 1] = rd.direct(K, h, s + 1);
+                    vf[(s + 1) & 1] = rd.direct(V, h, s + 1);
+                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    S[h][n] = mfma32(kf, qf[s][n], S[h][n]);
-                    dP[h][n] = mfma32(vf, gf[s][n], dP[h][n]);
+                    S[n] = mfma32(kf[s & 1], qf[s][n], S[n]);
+                    dP[n] = mfma32(vf[s & 1], gf[s][n], dP[n]);
                 }
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[h][n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[h][n][i], a.scale_log2, shift[n]));
+                for (int i = 0; i < 16; ++i) S[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[n][i], a.scale_log2, shift[n]));
                 if constexpr (DROP) {
-                    const u32x4_t w = rnd.weights((t0 >> 5) + h, g, (uint32_t)(at[n].cand * a.L_q + at[n].query), (uint32_t)at[n].head);
+                    const u32x4_t w = rnd.weights((t0 >> 5) + h, g, row[n], head[n]);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) dP[h][n][i] = ((w[i >> 2] >> (8 * (i & 3))) & 255u) >= a.edge ? dP[h][n][i] * a.keep : 0.f;
+                    for (int i = 0; i < 16; ++i) dP[n][i] = ((w[i >> 2] >> (8 * (i & 3))) & 255u) >= a.edge ? dP[n][i] * a.keep : 0.f;
                 }
             }
+            if (t0 + 32 * h + 32 > least) {
+                asm volatile("");   // stays a branch: as selects its body would be paid by every stage
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (t0 + 32 * h + 8 * (i >> 2) + 4 * g + (i & 3) >= limit[n]) S[n][i] = 0.f;
+            }
+        };
+        if (t0 == 0 && least <= 64) {
+            float sum[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) sum[n] = 0.f;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                probabilities(h);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum[n] = __builtin_fmaf(S[n][i], dP[n][i], sum[n]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                sum[n] = sum_halves(sum[n]);
+                D[n] = limit[n] <= 64 ? sum[n] : D[n];
+            }
         }
-        if (t0 + 64 > least) {
-            asm volatile("");   // stays a branch: as selects its body would be paid by every stage
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            probabilities(h);
+            u32x4_t pf[2][NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int i = 0; i < 16; i += 2)
+                    pf[i >> 3][n][(i >> 1) & 3] = pack_bf16x2(S[n][i] * (dP[n][i] - D[n]), S[n][i + 1] * (dP[n][i + 1] - D[n]));
+                        u32x4_t kt[2];
+            kt[0] = rd.turned(K, 2 * h, 0);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (t0 + 32 * h + 8 * (i >> 2) + 4 * g + (i & 3) >= limit[n]) S[h][n][i] = 0.f;
-        }
-        if (t0 == 0 && least <= 64) {
+            for (int i = 0; i < 2 * DT; ++i) {
+                if (i + 1 < 2 * DT) kt[(i + 1) & 1] = rd.turned(K, 2 * h + (i + 1) / DT, (i + 1) % DT);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float sum = 0.f;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(S[h][n][i], dP[h][n][i], sum);
-                sum = sum_halves(sum);
-                D[n] = limit[n] <= 64 ? sum : D[n];
-            }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            u32x4_t pf[2][NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float x[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = S[h][n][i] * (dP[h][n][i] - D[n]);
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    pf[s][n] = (u32x4_t){pack_bf16x2(x[8 * s], x[8 * s + 1]), pack_bf16x2(x[8 * s + 2], x[8 * s + 3]),
-                                         pack_bf16x2(x[8 * s + 4], x[8 * s + 5]), pack_bf16x2(x[8 * s + 6], x[8 * s + 7])};
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const u32x4_t kt = rd.turned(K, 2 * h + s, d);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) dq[d][n] = mfma32(kt, pf[s][n], dq[d][n]);
-                }
+                for (int n = 0; n < NT; ++n) dq[i % DT][n] = mfma32(kt[i & 1], pf[i / DT][n], dq[i % DT][n]);
+                            }
         }
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int r = r0 + 32 * n + j;
+        const Place to_row = place_of(a, first, hk, live[n] ? r : 0);   // again, rather than kept
         if (split == 0 && g == 0 && r < ((n_rows + 63) & ~63)) {
             RowNotes &x = a.notes[(int64_t)hk * a.n_notes + a.tile[tile].z + ((r - row0) >> 6)];
             const int i = r & 63;
             const bool sees = limit[n] > 0;
-            x.q[i] = sees ? (const void *)(a.Q + at[n].cand * a.q_cand + at[n].head * a.q_head + at[n].query * a.q_query) : kZeroRow;
-            x.dy[i] = sees ? (const void *)(a.dO + at[n].cand * a.do_cand + at[n].head * a.do_head + at[n].query * a.do_query) : kZeroRow;
+            x.q[i] = sees ? (const void *)(a.Q + to_row.cand * a.q_cand + to_row.head * a.q_head + to_row.query * a.q_query) : kZeroRow;
+            x.dy[i] = sees ? (const void *)(a.dO + to_row.cand * a.do_cand + to_row.head * a.do_head + to_row.query * a.do_query) : kZeroRow;
             x.shift[i] = sees ? shift[n] : neg_inf();
             x.D[i] = D[n];
             x.limit[i] = limit[n];
-            x.row[i] = at[n].cand * a.L_q + at[n].query;
-            x.head[i] = at[n].head;
+            x.row[i] = to_row.cand * a.L_q + to_row.query;
+            x.head[i] = to_row.head;
         }
         if (!live[n]) continue;
         if (a.splits == 1) {
-            uint16_t *to = a.dQ + at[n].cand * a.dq_cand + at[n].head * a.dq_head + at[n].query * a.dq_query + 8 * g;
+            uint16_t *to = a.dQ + to_row.cand * a.dq_cand + to_row.head * a.dq_head + to_row.query * a.dq_query + 8 * g;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -233,9 +234,9 @@ __global__ void __launch_bounds__(256) train_dq_join_kernel(TrainArgs a, int til
         (u32x2_t){pack_bf16x2(o[0] * a.scale, o[1] * a.scale), pack_bf16x2(o[2] * a.scale, o[3] * a.scale)};
 }
 
-template <int HD, int NK, int WAVES, bool DROP>
+template <int HD, int WAVES, bool DROP>
 __global__ void __launch_bounds__(64 * WAVES, 1) train_dkv_kernel(TrainArgs a) {
-    constexpr int TK = HD / 16, DT = HD / 32, STAGE = Rows<HD>::matrix(64), KEYS = 32 * NK * WAVES, N = 64 * HD / 8 / (64 * WAVES);
+    constexpr int TK = HD / 16, DT = HD / 32, STAGE = Rows<HD>::matrix(64), KEYS = 32 * WAVES, N = 64 * HD / 8 / (64 * WAVES);
     constexpr bool V_LDS = HD == 128;   // V stays in LDS: 32 registers less, which lets two waves stand on a SIMD
     __shared__ __align__(16) char lds[2][2][STAGE], v_lds[V_LDS ? Rows<HD>::matrix(KEYS) : 16];
     __shared__ __align__(16) RowNotes notes[3];
@@ -245,8 +246,8 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_dkv_kernel(TrainArgs a) {
     const int range = unit % ranges, hk = unit / ranges % a.H_kv, c = unit / ranges / a.H_kv;   // neighbours share rows
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5, j = lane & 31;
     const int4 ch = a.chunk[c];
-    const int u = __builtin_amdgcn_readfirstlane(ch.x), len = user_len(a, u);
-    const int key0 = range * KEYS + wv * 32 * NK;
+    const int u = __builtin_amdgcn_readfirstlane(ch.x), len = __builtin_amdgcn_readfirstlane(user_len(a, u));
+    const int key0 = range * KEYS + wv * 32;
 
     const int token = Turn::token(j);   // of each 32 keys, the one in this lane
     Random rnd;
@@ -255,29 +256,28 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_dkv_kernel(TrainArgs a) {
         rnd.init(a.rng);
         turn.init(lane);
     }
-    u32x4_t kf[TK][NK], vf[V_LDS ? 1 : TK][NK];
-    f32x16_t dk[DT][NK], dv[DT][NK];
-#pragma unroll
-    for (int n = 0; n < NK; ++n) {
-        const int t = key0 + 32 * n + token;
+    u32x4_t kf[TK], vf[V_LDS ? 1 : TK];
+    f32x16_t dk[DT], dv[DT];
+    {
+        const int t = key0 + token;
         const uint16_t *k = a.K + u * a.k_user + hk * a.k_head + t * a.k_token + 8 * g;
         const uint16_t *v = a.V + u * a.v_user + hk * a.v_head + t * a.v_token + 8 * g;
 #pragma unroll
         for (int s = 0; s < TK; ++s) {
-            kf[s][n] = t < len ? *reinterpret_cast<const u32x4_t *>(k + 16 * s) : (u32x4_t){0, 0, 0, 0};
-            if constexpr (!V_LDS) vf[s][n] = t < len ? *reinterpret_cast<const u32x4_t *>(v + 16 * s) : (u32x4_t){0, 0, 0, 0};
+            kf[s] = t < len ? *reinterpret_cast<const u32x4_t *>(k + 16 * s) : (u32x4_t){0, 0, 0, 0};
+            if constexpr (!V_LDS) vf[s] = t < len ? *reinterpret_cast<const u32x4_t *>(v + 16 * s) : (u32x4_t){0, 0, 0, 0};
         }
 #pragma unroll
-        for (int d = 0; d < DT; ++d) dk[d][n] = dv[d][n] = (f32x16_t)(0.f);
+        for (int d = 0; d < DT; ++d) dk[d] = dv[d] = (f32x16_t)(0.f);
     }
     if constexpr (V_LDS) {   // each wave its own keys
         const uint16_t *v = a.V + u * a.v_user + hk * a.v_head;
 #pragma unroll
-        for (int i = 0; i < 32 * NK * HD / 8 / 64; ++i) {
+        for (int i = 0; i < 32 * HD / 8 / 64; ++i) {
             const int p = i * 64 + lane, row = p / Rows<HD>::CHUNKS, chunk = ((p % Rows<HD>::CHUNKS) ^ Rows<HD>::number(row)) * 16;
-            const int t = key0 + (row & ~31) + Turn::token(row & 31);
+            const int t = key0 + Turn::token(row);
             load_to_lds(t < len ? reinterpret_cast<const char *>(v + t * a.v_token) + chunk : reinterpret_cast<const char *>(kZeroRow) + chunk,
-                        lds_address(v_lds) + Rows<HD>::matrix(32 * NK) * wv + i * Rows<HD>::GROUP);
+                        lds_address(v_lds) + Rows<HD>::matrix(32) * wv + i * Rows<HD>::GROUP);
         }
     }
     Reader<HD> rd;
@@ -315,76 +315,76 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_dkv_kernel(TrainArgs a) {
         const RowNotes &x = notes[st % 3];
         const int limit = x.limit[lane];
         if (!__ballot(limit > key0)) continue;   // no row sees the wave's keys
-        const bool partly = __ballot(limit < key0 + 32 * NK) != 0;
+        const bool partly = __ballot(limit < key0 + 32) != 0;
         const char *Q = lds[st & 1][0], *Y = lds[st & 1][1];
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-            f32x16_t S[NK], dP[NK];
-#pragma unroll
-            for (int n = 0; n < NK; ++n) S[n] = dP[n] = (f32x16_t)(0.f);
+            // Operands are read one step ahead of their products; the fences keep the compiler from reading further ahead,
+            // for which it would spill: a spilled register's load would wait for the next stage's.
+            f32x16_t S, dP;
+            S = dP = (f32x16_t)(0.f);
+            u32x4_t qf[2], yf[2], vl[2];
+            auto operands = [&](int s) {
+                qf[s & 1] = rd.direct(Q, h, s);
+                yf[s & 1] = rd.direct(Y, h, s);
+                if constexpr (V_LDS) vl[s & 1] = rd.direct(v_lds + Rows<HD>::matrix(32) * wv, 0, s);
+            };
+            operands(0);
 #pragma unroll
             for (int s = 0; s < TK; ++s) {
-                const u32x4_t qf = rd.direct(Q, h, s), yf = rd.direct(Y, h, s);
-#pragma unroll
-                for (int n = 0; n < NK; ++n) {
-                    S[n] = mfma32(qf, kf[s][n], S[n]);
-                    dP[n] = mfma32(yf, V_LDS ? rd.direct(v_lds + Rows<HD>::matrix(32 * NK) * wv, n, s) : vf[V_LDS ? 0 : s][n], dP[n]);
-                }
+                if (s + 1 < TK) operands(s + 1);
+                S = mfma32(qf[s & 1], kf[s], S);
+                dP = mfma32(yf[s & 1], V_LDS ? vl[s & 1] : vf[V_LDS ? 0 : s], dP);
+                fence<HD == 128>();
             }
-            f32x4_t shift[4], D[4];
+            uint32_t stays = 0;
+            if constexpr (DROP) stays = turn.rows(rnd.weights(key0 >> 5, g, (uint32_t)x.row[32 * h + j], (uint32_t)x.head[32 * h + j]), a.edge) >> (4 * g);
+            u32x4_t pf[2], sf[2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                shift[q] = *reinterpret_cast<const f32x4_t *>(x.shift + 32 * h + 8 * q + 4 * g);
-                D[q] = *reinterpret_cast<const f32x4_t *>(x.D + 32 * h + 8 * q + 4 * g);
-            }
-            u32x4_t pf[2][NK], sf[2][NK];
+            for (int q = 0; q < 4; ++q) {   // rows 8 q + 4 g + e
+                const f32x4_t shift = *reinterpret_cast<const f32x4_t *>(x.shift + 32 * h + 8 * q + 4 * g);
+                const f32x4_t D = *reinterpret_cast<const f32x4_t *>(x.D + 32 * h + 8 * q + 4 * g);
+                float p[4], ds[4];
 #pragma unroll
-            for (int n = 0; n < NK; ++n) {
-                float p[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[n][i], a.scale_log2, shift[i >> 2][i & 3]));
+                for (int e = 0; e < 4; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[4 * q + e], a.scale_log2, shift[e]));
                 if (partly) {
                     asm volatile("");
+                    const u32x4_t limits = *reinterpret_cast<const u32x4_t *>(x.limit + 32 * h + 8 * q + 4 * g);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (key0 + 32 * n + token >= x.limit[32 * h + 8 * (i >> 2) + 4 * g + (i & 3)]) p[i] = 0.f;
-                }
-                uint32_t stays = 0;
-                if constexpr (DROP)
-                    stays = turn.rows(rnd.weights((key0 >> 5) + n, g, (uint32_t)x.row[32 * h + j], (uint32_t)x.head[32 * h + j]), a.edge) >> (4 * g);
-                float ds[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float dp = dP[n][i];
-                    if constexpr (DROP) dp = (stays >> (8 * (i >> 2) + (i & 3))) & 1 ? dp * a.keep : 0.f;
-                    ds[i] = p[i] * (dp - D[i >> 2][i & 3]);
-                    if constexpr (DROP) p[i] = (stays >> (8 * (i >> 2) + (i & 3))) & 1 ? p[i] : 0.f;
+                    for (int e = 0; e < 4; ++e) p[e] = key0 + token < (int)limits[e] ? p[e] : 0.f;
                 }
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    pf[s][n] = (u32x4_t){pack_bf16x2(p[8 * s], p[8 * s + 1]), pack_bf16x2(p[8 * s + 2], p[8 * s + 3]),
-                                         pack_bf16x2(p[8 * s + 4], p[8 * s + 5]), pack_bf16x2(p[8 * s + 6], p[8 * s + 7])};
-                    sf[s][n] = (u32x4_t){pack_bf16x2(ds[8 * s], ds[8 * s + 1]), pack_bf16x2(ds[8 * s + 2], ds[8 * s + 3]),
-                                         pack_bf16x2(ds[8 * s + 4], ds[8 * s + 5]), pack_bf16x2(ds[8 * s + 6], ds[8 * s + 7])};
+                for (int e = 0; e < 4; ++e) {
+                    float dp = dP[4 * q + e];
+                    const bool stay = !DROP || (stays >> (8 * q + e) & 1);
+                    if constexpr (DROP) dp = stay ? dp * a.keep : 0.f;
+                    ds[e] = p[e] * (dp - D[e]);
+                    p[e] = stay ? p[e] : 0.f;
                 }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    pf[q >> 1][2 * (q & 1) + e] = pack_bf16x2(p[2 * e], p[2 * e + 1]);
+                    sf[q >> 1][2 * (q & 1) + e] = pack_bf16x2(ds[2 * e], ds[2 * e + 1]);
+                }
+                fence<HD == 128>();
             }
+            u32x4_t yt[2], qt[2];
+            auto turned = [&](int i) {
+                yt[i & 1] = rd.turned(Y, 2 * h + i / DT, i % DT);
+                qt[i & 1] = rd.turned(Q, 2 * h + i / DT, i % DT);
+            };
+            turned(0);
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const u32x4_t yt = rd.turned(Y, 2 * h + s, d), qt = rd.turned(Q, 2 * h + s, d);
-#pragma unroll
-                    for (int n = 0; n < NK; ++n) {
-                        dv[d][n] = mfma32(yt, pf[s][n], dv[d][n]);
-                        dk[d][n] = mfma32(qt, sf[s][n], dk[d][n]);
-                    }
-                }
+            for (int i = 0; i < 2 * DT; ++i) {
+                if (i + 1 < 2 * DT) turned(i + 1);
+                dv[i % DT] = mfma32(yt[i & 1], pf[i / DT], dv[i % DT]);
+                dk[i % DT] = mfma32(qt[i & 1], sf[i / DT], dk[i % DT]);
+                fence<HD == 128>();
+            }
         }
     }
-#pragma unroll
-    for (int n = 0; n < NK; ++n) {
-        const int t = key0 + 32 * n + token;
-        if (t >= a.L_kv) continue;
+    const int t = key0 + token;
+    if (t < a.L_kv) {
         if (ch.w < 0) {
             const float by = t < len ? 1.f : 0.f;   // what a key behind the history has gathered is no gradient
             uint16_t *k = a.dK + u * a.dk_user + hk * a.dk_head + t * a.dk_token + 8 * g, *v = a.dV + u * a.dv_user + hk * a.dv_head + t * a.dv_token + 8 * g;
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_dkv_kernel(TrainArgs a) {
             for (int d = 0; d < DT; ++d)
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    const u32x4_t x = eight_rows(dk[d][n], p, a.scale), y = eight_rows(dv[d][n], p, a.keep), zero = {0, 0, 0, 0};
+                    const u32x4_t x = eight_rows(dk[d], p, a.scale), y = eight_rows(dv[d], p, a.keep), zero = {0, 0, 0, 0};
                     *reinterpret_cast<u32x4_t *>(k + 32 * d + 16 * p) = by > 0.f ? x : zero;
                     *reinterpret_cast<u32x4_t *>(v + 32 * d + 16 * p) = by > 0.f ? y : zero;
                 }
@@ -403,8 +403,8 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_dkv_kernel(TrainArgs a) {
             for (int d = 0; d < DT; ++d)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    *reinterpret_cast<f32x4_t *>(k + 32 * d + 8 * q) = (f32x4_t){dk[d][n][4 * q], dk[d][n][4 * q + 1], dk[d][n][4 * q + 2], dk[d][n][4 * q + 3]};
-                    *reinterpret_cast<f32x4_t *>(v + 32 * d + 8 * q) = (f32x4_t){dv[d][n][4 * q], dv[d][n][4 * q + 1], dv[d][n][4 * q + 2], dv[d][n][4 * q + 3]};
+                    *reinterpret_cast<f32x4_t *>(k + 32 * d + 8 * q) = (f32x4_t){dk[d][4 * q], dk[d][4 * q + 1], dk[d][4 * q + 2], dk[d][4 * q + 3]};
+                    *reinterpret_cast<f32x4_t *>(v + 32 * d + 8 * q) = (f32x4_t){dv[d][4 * q], dv[d][4 * q + 1], dv[d][4 * q + 2], dv[d][4 * q + 3]};
                 }
         }
     }
@@ -436,9 +436,9 @@ __global__ void __launch_bounds__(256) train_dkv_join_kernel(TrainArgs a) {
     }
 }
 
-template <int HD, int NT, int WAVES, int NK, int KW>
+template <int HD, int NT, int WAVES, int KW>
 hipError_t launch(const TrainArgs &a, hipStream_t s) {
-    constexpr int ROWS = 32 * NT * WAVES, KEYS = 32 * NK * KW, EACH = 1024 / HD;
+    constexpr int ROWS = 32 * NT * WAVES, KEYS = 32 * KW, EACH = 1024 / HD;
     static_assert(KEYS == kKeys, "the layout's chunks");
     hipError_t e;
     if (a.tiles > 0) {
@@ -452,8 +452,8 @@ hipError_t launch(const TrainArgs &a, hipStream_t s) {
         }
     }
     const dim3 grid((unsigned)(((int64_t)a.chunks * a.H_kv * ((a.L_kv + KEYS - 1) / KEYS) + 7) / 8 * 8));
-    if (a.edge) hipLaunchKernelGGL((train_dkv_kernel<HD, NK, KW, true>), grid, dim3(64 * KW), 0, s, a);
-    else hipLaunchKernelGGL((train_dkv_kernel<HD, NK, KW, false>), grid, dim3(64 * KW), 0, s, a);
+    if (a.edge) hipLaunchKernelGGL((train_dkv_kernel<HD, KW, true>), grid, dim3(64 * KW), 0, s, a);
+    else hipLaunchKernelGGL((train_dkv_kernel<HD, KW, false>), grid, dim3(64 * KW), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess || a.slots == 0) return e;
     hipLaunchKernelGGL((train_dkv_join_kernel<HD>), dim3((unsigned)std::min<int64_t>(((int64_t)a.B_u * a.H_kv * a.L_kv + EACH - 1) / EACH, 1 << 16)), dim3(256), 0, s, a);
     return hipGetLastError();
@@ -462,7 +462,7 @@ hipError_t launch(const TrainArgs &a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_train_backward(const TrainArgs &a, const TrainLayout &, int head_dim, hipStream_t s) {
-    return head_dim == 128 ? launch<128, 1, 8, 1, 8>(a, s) : launch<64, 1, 8, 1, 8>(a, s);
+    return head_dim == 128 ? launch<128, 1, 8, 8>(a, s) : launch<64, 1, 8, 8>(a, s);
 }
 
 }  // namespace ikbo

@@ -20,6 +20,12 @@ __device__ __forceinline__ f32x16_t mfma32(const u32x4_t &a, const u32x4_t &b, f
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
 }
 
+// Nothing is scheduled across.
+template <bool ON>
+__device__ __forceinline__ void fence() {
+    if constexpr (ON) __builtin_amdgcn_sched_barrier(0);
+}
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
@@ -91,37 +97,52 @@ struct Reader {
 __device__ __forceinline__ void load_to_lds(const void *from, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(from) : "memory");
 }
+// The same with a uniform base and an offset per lane.
+__device__ __forceinline__ void load_to_lds(const char *base, uint32_t off, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(base) : "memory");
+}
 __device__ __forceinline__ uint32_t lds_address(const void *p) { return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)p; }
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // What stands for a row that does not exist.
 __device__ const uint32_t kZeroRow[64] __attribute__((aligned(16))) = {};
 
-// A block's staging of 64 keys (or values) of one user and head.
+// A block's staging of 64 keys and their values of one user and head: uniform addresses and one offset per lane, but for the
+// last keys of a history.
 template <int HD, int WAVES>
 struct KeyLoads {
-    static constexpr int N = 64 * HD / 8 / (64 * WAVES);
-    const char *from[N];
-    int key[N];
-    uint32_t chunk[N];
-    int64_t step;
-    __device__ __forceinline__ void init(const uint16_t *base, int64_t token, int first, int lane, int wv) {
-        step = token * 128;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int p = (i * WAVES + wv) * 64 + lane, row = p / Rows<HD>::CHUNKS;
-            chunk[i] = ((p % Rows<HD>::CHUNKS) ^ Rows<HD>::number(row)) * 16;
-            key[i] = first + row;
-            from[i] = reinterpret_cast<const char *>(base + key[i] * token) + chunk[i];
-        }
+    static constexpr int N = 64 * HD / 8 / (64 * WAVES), STEP = Rows<HD>::EACH * WAVES;   // loads of a matrix, and rows between them
+    static_assert(STEP % 16 == 0, "the rows of a lane's loads have one number");
+    const char *k, *v;
+    int64_t k_row, v_row;   // bytes from token to token
+    uint32_t k_off, v_off;
+    int row, chunk;
+    __device__ __forceinline__ void init(const TrainArgs &a, int u, int hk, int lane, int wv) {
+        k = reinterpret_cast<const char *>(a.K + u * a.k_user + hk * a.k_head);
+        v = reinterpret_cast<const char *>(a.V + u * a.v_user + hk * a.v_head);
+        k_row = 2 * a.k_token;
+        v_row = 2 * a.v_token;
+        const int p = wv * 64 + lane;
+        row = p / Rows<HD>::CHUNKS;
+        chunk = ((p % Rows<HD>::CHUNKS) ^ Rows<HD>::number(row)) * 16;
+        k_off = (uint32_t)(row * k_row + chunk);   // below 2^32: the host allows tokens 2^24 elements apart
+        v_off = (uint32_t)(row * v_row + chunk);
     }
-    // The next 64; keys from `len` on are zeros.
-    __device__ __forceinline__ void next(uint32_t to, int wv, int len) {
+    // Keys t0 .. t0 + 63 to `to`, their values behind them; keys from `len` on are zeros.
+    __device__ __forceinline__ void load(uint32_t to, int wv, int t0, int len) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            load_to_lds(key[i] < len ? from[i] : reinterpret_cast<const char *>(kZeroRow) + chunk[i], to + (i * WAVES + wv) * Rows<HD>::GROUP);
-            key[i] += 64;
-            from[i] += step;
+            const uint32_t at = to + (i * WAVES + wv) * Rows<HD>::GROUP;
+            const int t = t0 + i * STEP;
+            if (t0 + 64 <= len) {
+                load_to_lds(k + t * k_row, k_off, at);
+                load_to_lds(v + t * v_row, v_off, at + Rows<HD>::matrix(64));
+            } else {
+                const bool there = t + row < len;
+                const char *zero = reinterpret_cast<const char *>(kZeroRow) + chunk;
+                load_to_lds(there ? k + t * k_row + k_off : zero, at);
+                load_to_lds(there ? v + t * v_row + v_off : zero, at + Rows<HD>::matrix(64));
+            }
         }
     }
 };

@@ -26,11 +26,11 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_fwd_kernel(TrainArgs a) {
     const int tile = unit % n_tiles, hk = unit / n_tiles % a.H_kv, split = unit / n_tiles / a.H_kv;
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5, j = lane & 31;
     const int u = __builtin_amdgcn_readfirstlane(a.tile[tile].x), row0 = __builtin_amdgcn_readfirstlane(a.tile[tile].y);
-    const int first = a.off[u], n_rows = (a.off[u + 1] - first) * a.G * a.L_q, len = user_len(a, u);
+    const int first = a.off[u], n_rows = (a.off[u + 1] - first) * a.G * a.L_q, len = __builtin_amdgcn_readfirstlane(user_len(a, u));
 
     // The wave's rows: 32 n + j.
     const int r0 = row0 + wv * 32 * NT;
-    Place at[NT];
+    uint32_t row[NT], head[NT];
     int limit[NT], most = 0, least = len;
     bool live[NT];
     u32x4_t qf[TK][NT];
@@ -38,9 +38,11 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_fwd_kernel(TrainArgs a) {
     for (int n = 0; n < NT; ++n) {
         const int r = r0 + 32 * n + j;
         live[n] = r < n_rows;
-        at[n] = place_of(a, first, hk, live[n] ? r : 0);
-        limit[n] = live[n] ? limit_of(a, at[n], len) : 0;
-        const uint16_t *q = a.Q + at[n].cand * a.q_cand + at[n].head * a.q_head + at[n].query * a.q_query + 8 * g;
+        const Place at = place_of(a, first, hk, live[n] ? r : 0);
+        limit[n] = live[n] ? limit_of(a, at, len) : 0;
+        row[n] = (uint32_t)(at.cand * a.L_q + at.query);
+        head[n] = (uint32_t)at.head;
+        const uint16_t *q = a.Q + at.cand * a.q_cand + at.head * a.q_head + at.query * a.q_query + 8 * g;
 #pragma unroll
         for (int s = 0; s < TK; ++s) qf[s][n] = live[n] ? *reinterpret_cast<const u32x4_t *>(q + 16 * s) : (u32x4_t){0, 0, 0, 0};
         most = max(most, limit[n]);
@@ -72,25 +74,17 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_fwd_kernel(TrainArgs a) {
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d][n] = (f32x16_t)(0.f);
     }
-    KeyLoads<HD, WAVES> kl, vl;
-    kl.init(a.K + u * a.k_user + hk * a.k_head, a.k_token, key0, lane, wv);
-    vl.init(a.V + u * a.v_user + hk * a.v_head, a.v_token, key0, lane, wv);
+    KeyLoads<HD, WAVES> keys;
+    keys.init(a, u, hk, lane, wv);
     Reader<HD> rd;
     rd.init(lane);
     const uint32_t lds0 = lds_address(lds);
     const int stages = max(0, (end - key0 + 63) >> 6);
-    if (stages > 0) {
-        kl.next(lds0, wv, len);
-        vl.next(lds0 + STAGE, wv, len);
-    }
+    if (stages > 0) keys.load(lds0, wv, key0, len);
     for (int st = 0; st < stages; ++st) {
         landed();
         __syncthreads();   // stage st is there, and its other buffer has been read
-        if (st + 1 < stages) {
-            const uint32_t to = lds0 + ((st + 1) & 1) * 2 * STAGE;
-            kl.next(to, wv, len);
-            vl.next(to + STAGE, wv, len);
-        }
+        if (st + 1 < stages) keys.load(lds0 + ((st + 1) & 1) * 2 * STAGE, wv, key0 + 64 * st + 64, len);
         const int t0 = key0 + 64 * st;
         if (t0 >= most) continue;   // none of the wave's rows sees these keys
         const char *K = lds[st & 1][0], *V = lds[st & 1][1];
@@ -152,7 +146,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_fwd_kernel(TrainArgs a) {
                     l[n] += p[i];
                 }
                 if constexpr (DROP) {
-                    const u32x4_t w = rnd.weights((t0 >> 5) + h, g, (uint32_t)(at[n].cand * a.L_q + at[n].query), (uint32_t)at[n].head);
+                    const u32x4_t w = rnd.weights((t0 >> 5) + h, g, row[n], head[n]);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) p[i] = ((w[i >> 2] >> (8 * (i & 3))) & 255u) >= a.edge ? p[i] : 0.f;
                 }
@@ -175,23 +169,24 @@ __global__ void __launch_bounds__(64 * WAVES, 1) train_fwd_kernel(TrainArgs a) {
     for (int n = 0; n < NT; ++n) {
         const float sum = sum_halves(l[n]);
         if (!live[n]) continue;
+        const Place to_row = place_of(a, first, hk, r0 + 32 * n + j);   // again, rather than kept
         if (a.splits == 1) {
             const float by = sum > 0.f || sum != sum ? a.keep / sum : 0.f;   // a row that sees nothing is 0
-            uint16_t *to = a.O + at[n].cand * a.o_cand + at[n].head * a.o_head + at[n].query * a.o_query + 8 * g;
+            uint16_t *to = a.O + to_row.cand * a.o_cand + to_row.head * a.o_head + to_row.query * a.o_query + 8 * g;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
                 for (int p = 0; p < 2; ++p) *reinterpret_cast<u32x4_t *>(to + 32 * d + 16 * p) = eight_rows(o[d][n], p, by);
-            if (g == 0) a.lse[((int64_t)at[n].cand * a.H_q + at[n].head) * a.L_q + at[n].query] = m[n] * kLn2 + logf(sum);
+            if (g == 0) a.lse[((int64_t)to_row.cand * a.H_q + to_row.head) * a.L_q + to_row.query] = m[n] * kLn2 + logf(sum);
         } else {
-            const int64_t row = (((int64_t)split * a.tiles + tile) * a.H_kv + hk) * ROWS + wv * 32 * NT + 32 * n + j;
-            float *to = a.part + row * HD + 4 * g;
+            const int64_t at = (((int64_t)split * a.tiles + tile) * a.H_kv + hk) * ROWS + wv * 32 * NT + 32 * n + j;
+            float *to = a.part + at * HD + 4 * g;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     *reinterpret_cast<f32x4_t *>(to + 32 * d + 8 * q) = (f32x4_t){o[d][n][4 * q], o[d][n][4 * q + 1], o[d][n][4 * q + 2], o[d][n][4 * q + 3]};
-            if (g == 0) a.ml[row] = make_float2(m[n], sum);
+            if (g == 0) a.ml[at] = make_float2(m[n], sum);
         }
     }
 }
