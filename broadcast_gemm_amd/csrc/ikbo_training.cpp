@@ -17,7 +17,7 @@ namespace {
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 constexpr int64_t kInt = std::numeric_limits<int32_t>::max();
 constexpr int64_t kMaxToken = 1 << 24;   // elements from token to token
-constexpr int kMaxHeads = 4096, kTileRows = 256, kThreads = 512, kCus = 256;
+constexpr int kMaxHeads = 4096, kThreads = 512, kCus = 256;
 
 // Probability as whole steps of 1 / of; 0 and `of` only for probabilities of 0 and 1.
 int steps(double p, int of) { return (int)std::nearbyint(p * of); }
@@ -30,8 +30,8 @@ int check_shape(int B_u, int B_c, int H_q, int H_kv, int L_q, int L_kv, int head
         return IKBO_ERR_UNSUPPORTED;   // rows and keys are counted in 32 bits
     const TrainLayout w = train_layout(B_u, B_c, H_q, H_kv, L_q, L_kv, head_dim, true);
     // Threads of one launch are counted in 32 bits.
-    const int64_t most = std::max((int64_t)w.tiles * w.splits, (int64_t)w.chunks * ((L_kv + kKeys - 1) / kKeys)) * H_kv;
-    return most + 8 > kInt / kThreads ? IKBO_ERR_UNSUPPORTED : IKBO_OK;
+    const int64_t most = std::max((int64_t)w.tiles * w.splits, (int64_t)w.chunks * ((L_kv + keys_of(head_dim) - 1) / keys_of(head_dim))) * H_kv;
+    return most + 64 > kInt / kThreads ? IKBO_ERR_UNSUPPORTED : IKBO_OK;
 }
 
 int check(const ikbo_attention_args *a, bool backward) {
@@ -70,11 +70,9 @@ TrainArgs args_of(const ikbo_attention_args &a, const TrainLayout &w) {
     t.dQ = static_cast<uint16_t *>(a.dQ); t.dK = static_cast<uint16_t *>(a.dK); t.dV = static_cast<uint16_t *>(a.dV);
     t.map = a.map; t.lens = a.lens; t.positions = a.positions; t.rng = a.rng; t.status = a.status;
     t.perm = reinterpret_cast<int32_t *>(ws + w.o_perm);
-    t.off = reinterpret_cast<int32_t *>(ws + w.o_off);
-    t.tile = reinterpret_cast<int4 *>(ws + w.o_tile);
-    t.chunk = reinterpret_cast<int4 *>(ws + w.o_chunk);
-    t.user_chunk = reinterpret_cast<int2 *>(ws + w.o_user_chunk);
-    t.count = reinterpret_cast<int32_t *>(ws + w.o_count);
+    t.tile = reinterpret_cast<TileEntry *>(ws + w.o_tile);
+    t.chunk = reinterpret_cast<ChunkEntry *>(ws + w.o_chunk);
+    t.joins = reinterpret_cast<int4 *>(ws + w.o_joins);
     t.notes = reinterpret_cast<RowNotes *>(ws + w.o_notes);
     t.part = reinterpret_cast<float *>(ws + w.o_part);
     t.ml = reinterpret_cast<float2 *>(ws + w.o_ml);
@@ -90,7 +88,7 @@ TrainArgs args_of(const ikbo_attention_args &a, const TrainLayout &w) {
     t.dv_user = a.dv_user; t.dv_head = a.dv_head; t.dv_token = a.dv_token;
     t.B_u = a.B_u; t.B_c = a.B_c; t.H_q = a.H_q; t.H_kv = a.H_kv; t.G = a.H_q / a.H_kv; t.L_q = a.L_q; t.L_kv = a.L_kv;
     t.splits = w.splits; t.split_keys = w.split_keys; t.tiles = w.tiles;
-    t.chunk_rows = w.chunk_rows; t.chunks = w.chunks; t.slots = w.slots; t.n_notes = w.notes;
+    t.chunk_rows = w.chunk_rows; t.chunks = w.chunks; t.slots = w.slots; t.n_joins = w.joins; t.n_notes = w.notes;
     t.scale = a.scale > 0.0f ? a.scale : 1.0f / std::sqrt((float)a.head_dim);
     t.scale_log2 = (float)(t.scale * 1.4426950408889634);
     t.edge = (uint32_t)steps(a.dropout, 256);
@@ -105,7 +103,6 @@ namespace ikbo {
 TrainLayout train_layout(int B_u, int B_c, int H_q, int H_kv, int L_q, int L_kv, int head_dim, bool backward) {
     TrainLayout w{};
     const int64_t rows = (int64_t)B_c * L_q * (H_q / H_kv);   // of one shared head, over all users
-    w.tile_rows = kTileRows;
     w.tiles = (int)(rows / kTileRows + std::min(B_u, B_c));
     // Fewer blocks than CUs: the keys are cut, into four stages at least.
     const int64_t units = std::max<int64_t>((int64_t)w.tiles * H_kv, 1);
@@ -119,23 +116,22 @@ TrainLayout train_layout(int B_u, int B_c, int H_q, int H_kv, int L_q, int L_kv,
         return from;
     };
     w.o_perm = take((int64_t)B_c * 4);
-    w.o_off = take((int64_t)(B_u + 1) * 4);
-    w.o_count = take(8);
-    w.o_tile = take((int64_t)w.tiles * 16);
+    w.o_tile = take((int64_t)w.tiles * (int64_t)sizeof(TileEntry));
     const int64_t parts = w.splits > 1 ? (int64_t)w.splits * w.tiles * H_kv * kTileRows : 0;
     w.o_part = take(parts * head_dim * 4);
     w.o_ml = take(backward ? 0 : parts * 8);
     if (backward) {
-        // About two blocks to a CU in all; where the users alone make as many, a user of the average size is not cut:
+        // About twice the blocks that run at once; where the users alone make as many, a user of the average size is not cut:
         // a cut costs writing and joining its parts.
-        const int64_t ranges = (L_kv + kKeys - 1) / kKeys, work = rows * H_kv * ranges, whole = (int64_t)B_u * H_kv * ranges;
-        int64_t each = std::max<int64_t>(work / (2 * kCus), 256);
-        if (whole >= kCus * 3 / 4) each = std::max(each, rows * 5 / 4 / B_u);
+        const int64_t ranges = (L_kv + keys_of(head_dim) - 1) / keys_of(head_dim), at_once = kCus * 256 / keys_of(head_dim), work = rows * H_kv * ranges, whole = (int64_t)B_u * H_kv * ranges;
+        int64_t each = std::max<int64_t>(work / (2 * at_once), 256);
+        if (whole >= at_once * 3 / 4) each = std::max(each, rows * 5 / 4 / B_u);
         w.chunk_rows = (int)((each + 63) / 64 * 64);
         w.chunks = (int)(rows / w.chunk_rows + B_u);
         w.slots = rows > w.chunk_rows ? (int)(2 * rows / w.chunk_rows + 1) : 0;   // n > 1 chunks of a user are more than n / 2 full ones
-        w.o_chunk = take((int64_t)w.chunks * 16);
-        w.o_user_chunk = take((int64_t)B_u * 8);
+        w.o_chunk = take((int64_t)w.chunks * (int64_t)sizeof(ChunkEntry));
+        w.joins = std::min(B_u, w.slots / 2);
+        w.o_joins = take((int64_t)w.joins * 16);
         w.notes = (int)(rows / 64 + std::min(B_u, B_c));
         w.o_notes = take((int64_t)w.notes * H_kv * (int64_t)sizeof(RowNotes));
         w.o_dk = take((int64_t)w.slots * H_kv * L_kv * head_dim * 4);
@@ -160,7 +156,7 @@ int ikbo_attention_forward(const ikbo_attention_args *a, void *stream) {
     const TrainLayout w = train_layout(a->B_u, a->B_c, a->H_q, a->H_kv, a->L_q, a->L_kv, a->head_dim, false);
     const TrainArgs t = args_of(*a, w);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    hipError_t e = launch_train_prep(t, w.tile_rows, false, a->head_dim, s);
+    hipError_t e = launch_train_prep(t, false, a->head_dim, s);
     if (e != hipSuccess) return hip_fail(e, "attention grouping");
     e = launch_train_forward(t, w, a->head_dim, s);
     return e == hipSuccess ? IKBO_OK : hip_fail(e, "attention forward");
@@ -172,7 +168,7 @@ int ikbo_attention_backward(const ikbo_attention_args *a, void *stream) {
     const TrainLayout w = train_layout(a->B_u, a->B_c, a->H_q, a->H_kv, a->L_q, a->L_kv, a->head_dim, true);
     const TrainArgs t = args_of(*a, w);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    hipError_t e = launch_train_prep(t, w.tile_rows, true, a->head_dim, s);
+    hipError_t e = launch_train_prep(t, true, a->head_dim, s);
     if (e != hipSuccess) return hip_fail(e, "attention grouping");
     e = launch_train_backward(t, w, a->head_dim, s);
     return e == hipSuccess ? IKBO_OK : hip_fail(e, "attention backward");

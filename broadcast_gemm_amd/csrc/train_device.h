@@ -21,10 +21,7 @@ __device__ __forceinline__ f32x16_t mfma32(const u32x4_t &a, const u32x4_t &b, f
 }
 
 // Nothing is scheduled across.
-template <bool ON>
-__device__ __forceinline__ void fence() {
-    if constexpr (ON) __builtin_amdgcn_sched_barrier(0);
-}
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
@@ -116,32 +113,33 @@ struct KeyLoads {
     const char *k, *v;
     int64_t k_row, v_row;   // bytes from token to token
     uint32_t k_off, v_off;
-    int row, chunk;
     __device__ __forceinline__ void init(const TrainArgs &a, int u, int hk, int lane, int wv) {
         k = reinterpret_cast<const char *>(a.K + u * a.k_user + hk * a.k_head);
         v = reinterpret_cast<const char *>(a.V + u * a.v_user + hk * a.v_head);
         k_row = 2 * a.k_token;
         v_row = 2 * a.v_token;
-        const int p = wv * 64 + lane;
-        row = p / Rows<HD>::CHUNKS;
-        chunk = ((p % Rows<HD>::CHUNKS) ^ Rows<HD>::number(row)) * 16;
+        const int row = row_of(wv * 64 + lane), chunk = chunk_of(wv * 64 + lane);
         k_off = (uint32_t)(row * k_row + chunk);   // below 2^32: the host allows tokens 2^24 elements apart
         v_off = (uint32_t)(row * v_row + chunk);
     }
-    // Keys t0 .. t0 + 63 to `to`, their values behind them; keys from `len` on are zeros.
-    __device__ __forceinline__ void load(uint32_t to, int wv, int t0, int len) const {
+    // Keys t0 .. t0 + 63 (or their values) to `to`; those from `len` on are zeros.
+    __device__ __forceinline__ void load_k(uint32_t to, int wv, int t0, int len) const { load(to, wv, t0, len, k, k_row, k_off); }
+    __device__ __forceinline__ void load_v(uint32_t to, int wv, int t0, int len) const { load(to, wv, t0, len, v, v_row, v_off); }
+
+private:
+    static __device__ __forceinline__ int row_of(int p) { return p / Rows<HD>::CHUNKS; }
+    static __device__ __forceinline__ int chunk_of(int p) { return ((p % Rows<HD>::CHUNKS) ^ Rows<HD>::number(row_of(p))) * 16; }
+    __device__ __forceinline__ void load(uint32_t to, int wv, int t0, int len, const char *from, int64_t bytes, uint32_t off) const {
+        int p = (int)threadIdx.x;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const uint32_t at = to + (i * WAVES + wv) * Rows<HD>::GROUP;
             const int t = t0 + i * STEP;
             if (t0 + 64 <= len) {
-                load_to_lds(k + t * k_row, k_off, at);
-                load_to_lds(v + t * v_row, v_off, at + Rows<HD>::matrix(64));
+                load_to_lds(from + t * bytes, off, at);
             } else {
-                const bool there = t + row < len;
-                const char *zero = reinterpret_cast<const char *>(kZeroRow) + chunk;
-                load_to_lds(there ? k + t * k_row + k_off : zero, at);
-                load_to_lds(there ? v + t * v_row + v_off : zero, at + Rows<HD>::matrix(64));
+                asm volatile("" : "+v"(p));   // formed here: rows and chunks kept for the last keys would cost registers
+                load_to_lds(t + row_of(p) < len ? from + t * bytes + off : reinterpret_cast<const char *>(kZeroRow) + chunk_of(p), at);
             }
         }
     }
@@ -180,26 +178,22 @@ struct Random {
 };
 
 // The same decisions with tokens in the lanes.  Lane (g, j) gives the words of row j, whose byte e of word w is that of token 8 w +
-// 4 g + e; it gets bit r: whether row r keeps token 8 (j % 4) + j & 4 + j / 8 (`token`).  The bytes are compared four at a time;
+// 4 g + e; it gets bit r: whether row r keeps token 8 (j % 4) + j & 4 + j / 8 (turned_token).  The bytes are compared four at a time;
 // the bits of a row and its tokens are turned by exchanges with the lanes 16, 8, 4, 2 and 1 away.
+__device__ __forceinline__ int turned_token(int j) { return 8 * (j & 3) + (j & 4) + (j >> 3); }
+template <bool KEEP>   // what depends on the lane alone, in 9 registers
 struct Turn {
-    uint32_t bytes16, bytes8, by4, by2, by1, own4, own2, own1, half;
-    static __device__ __forceinline__ int token(int j) { return 8 * (j & 3) + (j & 4) + (j >> 3); }
-    __device__ __forceinline__ void init(int lane) {
-        bytes16 = lane & 16 ? 0x07060302u : 0x05040100u;   // of the pair (lane with bit 4 set : clear)
-        bytes8 = lane & 8 ? 0x07030501u : 0x02060004u;     // of the pair (own : other)
-        by4 = lane & 4 ? 4 : 28;
-        by2 = lane & 2 ? 2 : 30;
-        by1 = lane & 1 ? 1 : 31;
-        own4 = lane & 4 ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
-        own2 = lane & 2 ? 0xCCCCCCCCu : 0x33333333u;
-        own1 = lane & 1 ? 0xAAAAAAAAu : 0x55555555u;
-        half = lane & 32 ? 0 : 4;
-    }
+    int lane;
     static __device__ __forceinline__ uint32_t pick(uint32_t mask, uint32_t a, uint32_t b) { return (mask & a) | (~mask & b); }
     template <int CTRL>
     static __device__ __forceinline__ uint32_t from(uint32_t x) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xF, 0xF, true); }
     __device__ __forceinline__ uint32_t rows(const u32x4_t &w, uint32_t edge) const {
+        int lane = this->lane;
+        if constexpr (!KEEP) asm volatile("" : "+v"(lane));
+        const uint32_t bytes16 = lane & 16 ? 0x07060302u : 0x05040100u;   // of the pair (lane with bit 4 set : clear)
+        const uint32_t bytes8 = lane & 8 ? 0x07030501u : 0x02060004u;     // of the pair (own : other)
+        const uint32_t by4 = lane & 4 ? 4 : 28, by2 = lane & 2 ? 2 : 30, by1 = lane & 1 ? 1 : 31, half = lane & 32 ? 0 : 4;
+        const uint32_t own4 = lane & 4 ? 0xF0F0F0F0u : 0x0F0F0F0Fu, own2 = lane & 2 ? 0xCCCCCCCCu : 0x33333333u, own1 = lane & 1 ? 0xAAAAAAAAu : 0x55555555u;
         // Bit 7 of each byte: whether it is at least `edge`.  The low 7 bits decide, unless the top ones differ.
         const uint32_t low = (edge & 127) * 0x01010101u, top = edge & 128 ? 0u : 0xFFFFFFFFu;
         uint32_t f[4];
@@ -244,12 +238,15 @@ __device__ __forceinline__ int limit_of(const TrainArgs &a, const Place &p, int 
     return pos < 0 ? 0 : pos < len ? pos + 1 : len;
 }
 
-// Blocks go round the 8 dies in turn; neighbouring units, which share K and V, go to one die.  Unit of this block
-// among n, or -1.
+// Blocks go round the 8 dies in turn; runs of 8 (or 4) neighbouring units, which share what they read, go to one
+// die.  Whole eighths of the units to each die would leave the dies uneven where units differ.  Unit of this block among n, or -1.
 __device__ __forceinline__ int unit_of(int block, int n) {
-    const int per = (n + 7) >> 3, at = (block & 7) * per + (block >> 3);
-    return (block >> 3) < per && at < n ? at : -1;
+    const int log_run = n >= 512 ? 3 : n >= 128 ? 2 : 0, i = block >> 3;
+    const int at = ((((i >> log_run) << 3) + (block & 7)) << log_run) + (i & ((1 << log_run) - 1));
+    return at < n ? at : -1;
 }
+// Blocks for n units.
+inline unsigned blocks_of(int64_t n) { return (unsigned)((n + 63) / 64 * 64); }
 
 // Element quads 2 p and 2 p + 1 of a result column, rounded: 8 consecutive rows 16 p + 8 g .. of it for this lane.
 __device__ __forceinline__ u32x4_t eight_rows(const f32x16_t &x, int p, float by) {
