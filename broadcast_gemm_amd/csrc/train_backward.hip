@@ -4,7 +4,8 @@
 //
 // dQ: as the forward, a block takes a tile of rows against a range of keys: S^T = K Q^T, dP^T = V dO^T, P = exp(S - lse),
 // dS = P (dP - D), dQ^T += K^T dS^T.  It first forms D = rowsum(dO O), which the other kernel reads.  For a row that
-// sees no more than the first 64 keys D is the sum of P dP instead: with few keys the rounding of O shows in dP - D.
+// sees no more than the first 128 keys D is the sum of P dP instead, formed before: with few keys the rounding of O shows
+// in dP - D, and would be a third of the error.
 //
 // dK and dV: a wave keeps 32 keys' K and V and their gradients in registers, and the block goes over a chunk of the
 // user's rows, staged in LDS 64 at a time: S = Q K^T, dP = dO V^T, dV^T += dO^T P, dK^T += Q^T dS.  Rows stand in the
@@ -24,7 +25,7 @@ template <int HD, int WAVES, bool DROP>
 __global__ void __launch_bounds__(64 * WAVES, 2) train_dq_kernel(TrainArgs a) {
     constexpr int TK = HD / 16, DT = HD / 32, STAGE = Rows<HD>::matrix(64), ROWS = 32 * WAVES;
     __shared__ __align__(16) char lds[2][2][STAGE];
-    __shared__ int s_most[WAVES];
+    __shared__ int s_most[WAVES], s_least[WAVES];
     const int unit = unit_of((int)blockIdx.x, a.tiles * a.H_kv * a.splits);
     if (unit < 0) return;   // the whole block: no barrier has run
     const int tile = unit % a.tiles, hk = unit / a.tiles % a.H_kv, split = unit / a.tiles / a.H_kv;
@@ -85,11 +86,17 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dq_kernel(TrainArgs a) {
     }
     most = __builtin_amdgcn_readfirstlane(most);
     least = __builtin_amdgcn_readfirstlane(least);
-    if (lane == 0) s_most[wv] = most;
+    if (lane == 0) {
+        s_most[wv] = most;
+        s_least[wv] = least;
+    }
     __syncthreads();
-    int end = 0;
+    int end = 0, fewest = len;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) end = max(end, s_most[w]);
+    for (int w = 0; w < WAVES; ++w) {
+        end = max(end, s_most[w]);
+        fewest = min(fewest, s_least[w]);
+    }
     end = min(end, key0 + a.split_keys);
 
     Random rnd;
@@ -101,55 +108,60 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dq_kernel(TrainArgs a) {
     rd.init(lane);
     const int stages = max(0, (end - key0 + 63) >> 6);
     landed();   // also where no stage is wanted: nothing may arrive after the block
+    // P in S, and dP, of keys t0 + 8 (i / 4) + 4 g + i % 4, t0 = key0 + 64 st + 32 h.
+    f32x16_t S, dP;
+    auto probabilities = [&](int st, int h) {
+        const char *K = lds[st & 1][0], *V = lds[st & 1][1];
+        const int t0 = key0 + 64 * st + 32 * h;
+        S = dP = (f32x16_t)(0.f);
+        u32x4_t kf[2] = {rd.direct(K, h, 0)}, vf[2] = {rd.direct(V, h, 0)};   // a step ahead
+#pragma unroll
+        for (int s = 0; s < TK; ++s) {
+            if (s + 1 < TK) {
+                kf[(s + 1) & 1] = rd.direct(K, h, s + 1);
+                vf[(s + 1) & 1] = rd.direct(V, h, s + 1);
+            }
+            S = mfma32(kf[s & 1], qf[s], S);
+            dP = mfma32(vf[s & 1], gf[s], dP);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i], a.scale_log2, shift));
+        if constexpr (DROP) {
+            const u32x4_t w = rnd.weights(t0 >> 5, g, row, head);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dP[i] = ((w[i >> 2] >> (8 * (i & 3))) & 255u) >= a.edge ? dP[i] * a.keep : 0.f;
+        }
+        if (t0 + 32 > least) {
+            asm volatile("");   // stays a branch: as selects its body would be paid by every stage
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (t0 + 8 * (i >> 2) + 4 * g + (i & 3) >= limit) S[i] = 0.f;
+        }
+    };
+    if (key0 == 0 && stages > 0 && fewest <= 128) {
+        __syncthreads();
+        if (stages > 1) load(1);
+        landed();
+        __syncthreads();
+        float sum = 0.f;
+#pragma unroll 1
+        for (int x = 0; x < 2 * min(stages, 2); ++x) {
+            probabilities(x >> 1, x & 1);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(S[i], dP[i], sum);
+        }
+        sum = sum_halves(sum);
+        D = limit <= 128 ? sum : D;
+    }
     for (int st = 0; st < stages; ++st) {
         landed();
         __syncthreads();   // stage st is there, and its other buffer has been read
         if (st + 1 < stages) load(st + 1);
-        const int t0 = key0 + 64 * st;
-        if (t0 >= most) continue;   // none of the wave's rows sees these keys
-        const char *K = lds[st & 1][0], *V = lds[st & 1][1];
-        // P in S, and dP, of keys t0 + 32 h + 8 (i / 4) + 4 g + i % 4.
-        f32x16_t S, dP;
-        auto probabilities = [&](int h) {
-            S = dP = (f32x16_t)(0.f);
-            u32x4_t kf[2] = {rd.direct(K, h, 0)}, vf[2] = {rd.direct(V, h, 0)};   // a step ahead
-#pragma unroll
-            for (int s = 0; s < TK; ++s) {
-                if (s + 1 < TK) {
-                    kf[(s + 1) & 1] = rd.direct(K, h, s + 1);
-                    vf[(s + 1) & 1] = rd.direct(V, h, s + 1);
-                }
-                S = mfma32(kf[s & 1], qf[s], S);
-                dP = mfma32(vf[s & 1], gf[s], dP);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) S[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[i], a.scale_log2, shift));
-            if constexpr (DROP) {
-                const u32x4_t w = rnd.weights((t0 >> 5) + h, g, row, head);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) dP[i] = ((w[i >> 2] >> (8 * (i & 3))) & 255u) >= a.edge ? dP[i] * a.keep : 0.f;
-            }
-            if (t0 + 32 * h + 32 > least) {
-                asm volatile("");   // stays a branch: as selects its body would be paid by every stage
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (t0 + 32 * h + 8 * (i >> 2) + 4 * g + (i & 3) >= limit) S[i] = 0.f;
-            }
-        };
-        if (t0 == 0 && least <= 64) {
-            float sum = 0.f;
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                probabilities(h);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) sum = __builtin_fmaf(S[i], dP[i], sum);
-            }
-            sum = sum_halves(sum);
-            D = limit <= 64 ? sum : D;
-        }
+        if (key0 + 64 * st >= most) continue;   // none of the wave's rows sees these keys
+        const char *K = lds[st & 1][0];
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-            probabilities(h);
+            probabilities(st, h);
             u32x4_t pf[2];
 #pragma unroll
             for (int i = 0; i < 16; i += 2) pf[i >> 3][(i >> 1) & 3] = pack_bf16x2(S[i] * (dP[i] - D), S[i + 1] * (dP[i + 1] - D));
