@@ -21,19 +21,31 @@
 namespace ikbo {
 namespace {
 
-template <int HD, int WAVES, bool DROP>
+template <int HD, int WAVES, bool DROP, bool LOCAL>
 __global__ void __launch_bounds__(64 * WAVES, 2) train_dq_kernel(TrainArgs a) {
     constexpr int TK = HD / 16, DT = HD / 32, STAGE = Rows<HD>::matrix(64), ROWS = 32 * WAVES;
     __shared__ __align__(16) char lds[2][2][STAGE];
     __shared__ int s_most[WAVES], s_least[WAVES];
     const int unit = unit_of((int)blockIdx.x, a.tiles * a.H_kv * a.splits);
-    if (unit < 0) return;   // the whole block: no barrier has run
+    if (unit < 0) {   // the whole block: no barrier has run
+        if (LOCAL && blockIdx.x == gridDim.x - 1) fill_padding(a, HD, true, 0, 1);
+        return;
+    }
     const int tile = unit % a.tiles, hk = unit / a.tiles % a.H_kv, split = unit / a.tiles / a.H_kv;
-    const TileEntry t = a.tile[tile];
+    Local<64 * WAVES> local;
+    __shared__ LocalLds s_local;
+    TileEntry t;
+    if constexpr (LOCAL) {
+        local.count(a, s_local);
+        t = local.tile(tile);
+        if (a.splits > 1 && hk == 0 && split == 0 && threadIdx.x == 0) a.tile[tile] = t;   // for the launch that joins
+    } else {
+        t = a.tile[tile];
+    }
     const int u = __builtin_amdgcn_readfirstlane(t.user), row0 = __builtin_amdgcn_readfirstlane(t.row);
     if (u < 0) return;
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5, j = lane & 31;
-    const int first = __builtin_amdgcn_readfirstlane(t.first), n_rows = __builtin_amdgcn_readfirstlane(t.rows), len = __builtin_amdgcn_readfirstlane(t.len);
+    const int n_rows = __builtin_amdgcn_readfirstlane(t.rows), len = __builtin_amdgcn_readfirstlane(t.len);
 
     // The first keys are on their way before the rows.
     const int key0 = split * a.split_keys;
@@ -46,7 +58,15 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dq_kernel(TrainArgs a) {
         keys.load_v(to + STAGE, wv, key0 + 64 * st, len);
     };
     load(0);
-
+    if constexpr (LOCAL) {
+        local.list(a, s_local, u);
+        if (a.splits > 1 && hk == 0 && split == 0 && row0 == 0)
+            for (int i = tid; i * a.G * a.L_q < n_rows; i += 64 * WAVES) a.perm[t.first + i] = s_local.list[i];
+    }
+    auto place = [&](int r) {
+        if constexpr (LOCAL) return place_of(a, s_local.list, hk, r);
+        else return place_of(a, a.perm + t.first, hk, r);
+    };
     const int r = row0 + wv * 32 + j;
     const bool live = r < n_rows;
     int limit, most, least;
@@ -54,7 +74,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dq_kernel(TrainArgs a) {
     u32x4_t qf[TK], gf[TK];
     float shift, D;
     {
-        const Place at = place_of(a, first, hk, live ? r : 0);
+        const Place at = place(live ? r : 0);
         limit = live ? limit_of(a, at, len) : 0;
         row = (uint32_t)(at.cand * a.L_q + at.query);
         head = (uint32_t)at.head;
@@ -173,7 +193,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dq_kernel(TrainArgs a) {
             }
         }
     }
-    const Place at = place_of(a, first, hk, live ? r : 0);   // again, rather than kept
+    const Place at = place(live ? r : 0);   // again, rather than kept
     if (split == 0 && r < ((n_rows + 63) & ~63)) {
         RowNotes &x = a.notes[(int64_t)hk * a.n_notes + t.note + ((r - row0) >> 6)];
         if (g == 0) {
@@ -228,12 +248,12 @@ __global__ void __launch_bounds__(256) train_dq_join_kernel(TrainArgs a) {
     if (part > 0 || !live) return;
 #pragma unroll
     for (int y = 1; y < kJoiners; ++y) o += parts[y][row][x];
-    const Place p = place_of(a, t.first, hk, r);
+    const Place p = place_of(a, a.perm + t.first, hk, r);
     *reinterpret_cast<u32x2_t *>(a.dQ + p.cand * a.dq_cand + p.head * a.dq_head + p.query * a.dq_query + 4 * x) =
         (u32x2_t){pack_bf16x2(o[0] * a.scale, o[1] * a.scale), pack_bf16x2(o[2] * a.scale, o[3] * a.scale)};
 }
 
-template <int HD, int WAVES, bool DROP>
+template <int HD, int WAVES, bool DROP, bool LOCAL>
 __global__ void __launch_bounds__(64 * WAVES, 2) train_dkv_kernel(TrainArgs a) {
     constexpr int TK = HD / 16, DT = HD / 32, STAGE = Rows<HD>::matrix(64), KEYS = 32 * WAVES, N = 64 * HD / 8 / (64 * WAVES);
     constexpr bool V_LDS = HD == 128;   // V stays in LDS: 32 registers less, which lets two waves stand on a SIMD
@@ -245,7 +265,15 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dkv_kernel(TrainArgs a) {
     if (unit < 0) return;   // the whole block: no barrier has run
     const int range = unit % ranges, hk = unit / ranges % a.H_kv, c = unit / ranges / a.H_kv;   // neighbours share rows
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5, j = lane & 31;
-    const ChunkEntry ch = a.chunk[c];
+    ChunkEntry ch;
+    if constexpr (LOCAL) {
+        __shared__ LocalLds s_local;
+        Local<64 * WAVES> local;
+        local.count(a, s_local);
+        ch = local.chunk(c);
+    } else {
+        ch = a.chunk[c];
+    }
     const int u = __builtin_amdgcn_readfirstlane(ch.user), len = __builtin_amdgcn_readfirstlane(ch.len);
     if (u < 0) return;
     const int key0 = range * KEYS + wv * 32, slot = __builtin_amdgcn_readfirstlane(ch.slot);
@@ -491,14 +519,19 @@ __global__ void __launch_bounds__(256) train_dkv_join_kernel(TrainArgs a) {
 }
 
 template <int HD, int WAVES, int KW>
-hipError_t launch(const TrainArgs &a, hipStream_t s) {
+hipError_t launch(const TrainArgs &a, bool local, hipStream_t s) {
     static_assert(kTileRows == 32 * WAVES, "the layout's tiles");
     static_assert(keys_of(HD) == 32 * KW, "the layout's chunks");
     hipError_t e;
     if (a.tiles > 0) {
-        const dim3 grid(blocks_of((int64_t)a.tiles * a.H_kv * a.splits));
-        if (a.edge) hipLaunchKernelGGL((train_dq_kernel<HD, WAVES, true>), grid, dim3(64 * WAVES), 0, s, a);
-        else hipLaunchKernelGGL((train_dq_kernel<HD, WAVES, false>), grid, dim3(64 * WAVES), 0, s, a);
+        const dim3 grid(blocks_of((int64_t)a.tiles * a.H_kv * a.splits) + local), block(64 * WAVES);   // one more for the rows of padding
+        if (local) {
+            if (a.edge) hipLaunchKernelGGL((train_dq_kernel<HD, WAVES, true, true>), grid, block, 0, s, a);
+            else hipLaunchKernelGGL((train_dq_kernel<HD, WAVES, false, true>), grid, block, 0, s, a);
+        } else {
+            if (a.edge) hipLaunchKernelGGL((train_dq_kernel<HD, WAVES, true, false>), grid, block, 0, s, a);
+            else hipLaunchKernelGGL((train_dq_kernel<HD, WAVES, false, false>), grid, block, 0, s, a);
+        }
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (a.splits > 1) {
             hipLaunchKernelGGL((train_dq_join_kernel<HD>), dim3((unsigned)((int64_t)a.tiles * a.H_kv * kTileRows * HD * kJoiners / 1024)), dim3(256), 0, s, a);
@@ -506,8 +539,14 @@ hipError_t launch(const TrainArgs &a, hipStream_t s) {
         }
     }
     const dim3 grid(blocks_of((int64_t)a.chunks * a.H_kv * ((a.L_kv + keys_of(HD) - 1) / keys_of(HD))));
-    if (a.edge) hipLaunchKernelGGL((train_dkv_kernel<HD, KW, true>), grid, dim3(64 * KW), 0, s, a);
-    else hipLaunchKernelGGL((train_dkv_kernel<HD, KW, false>), grid, dim3(64 * KW), 0, s, a);
+    const dim3 block(64 * KW);
+    if (local) {
+        if (a.edge) hipLaunchKernelGGL((train_dkv_kernel<HD, KW, true, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((train_dkv_kernel<HD, KW, false, true>), grid, block, 0, s, a);
+    } else {
+        if (a.edge) hipLaunchKernelGGL((train_dkv_kernel<HD, KW, true, false>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((train_dkv_kernel<HD, KW, false, false>), grid, block, 0, s, a);
+    }
     if ((e = hipGetLastError()) != hipSuccess || a.n_joins == 0) return e;
     hipLaunchKernelGGL((train_dkv_join_kernel<HD>), dim3((unsigned)((int64_t)a.n_joins * a.H_kv * ((a.L_kv + 15) / 16))), dim3(256), 0, s, a);
     return hipGetLastError();
@@ -515,8 +554,8 @@ hipError_t launch(const TrainArgs &a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_train_backward(const TrainArgs &a, const TrainLayout &, int head_dim, hipStream_t s) {
-    return head_dim == 128 ? launch<128, kRowWaves, 8>(a, s) : launch<64, kRowWaves, 4>(a, s);
+hipError_t launch_train_backward(const TrainArgs &a, const TrainLayout &w, int head_dim, hipStream_t s) {
+    return head_dim == 128 ? launch<128, kRowWaves, 8>(a, w.local, s) : launch<64, kRowWaves, 4>(a, w.local, s);
 }
 
 }  // namespace ikbo

@@ -226,16 +226,112 @@ __device__ __forceinline__ int user_len(const TrainArgs &a, int u) { return a.le
 struct Place {
     int cand, head, query;
 };
-// Row r of user u's rows of shared head hk; first = off[u].
-__device__ __forceinline__ Place place_of(const TrainArgs &a, int first, int hk, int r) {
+// Row r of a user's rows of shared head hk; perm: the user's candidates.
+template <class P>
+__device__ __forceinline__ Place place_of(const TrainArgs &a, P perm, int hk, int r) {
     const uint32_t per = (uint32_t)(a.G * a.L_q), slot = (uint32_t)r / per, rest = (uint32_t)r - slot * per, gr = rest / (uint32_t)a.L_q;
-    return Place{a.perm[first + (int)slot], hk * a.G + (int)gr, (int)(rest - gr * (uint32_t)a.L_q)};
+    return Place{perm[(int)slot], hk * a.G + (int)gr, (int)(rest - gr * (uint32_t)a.L_q)};
 }
 // Tokens that a query sees.
 __device__ __forceinline__ int limit_of(const TrainArgs &a, const Place &p, int len) {
     if (!a.positions) return len;
     const int pos = a.positions[(int64_t)p.cand * a.L_q + p.query];
     return pos < 0 ? 0 : pos < len ? pos + 1 : len;
+}
+
+// ---- small calls ---------------------------------------------------------------------------
+//
+// For few candidates and users every block finds its own place: how many candidates each user has, which tile (or whose
+// notes) the block's is, and that user's candidates, in their order.  That takes about as long as reading a table of them,
+// and saves the launch that writes it (5 us).
+
+struct LocalLds {
+    int count[kLocalUsers], part[kLocalCands / 64], list[kLocalCands];
+};
+
+// Counts, by all THREADS threads, whose candidates' users are left in m; then lane u of every wave knows user u's: the
+// candidates, tiles and notes before (12, 8 and 12 bits) and rows.
+template <int THREADS>
+struct Local {
+    int m[kLocalCands / THREADS], before, rows, len;
+    __device__ __forceinline__ void count(const TrainArgs &a, LocalLds &s) {
+        const int tid = (int)threadIdx.x, lane = tid & 63;
+        uint32_t err = 0;
+#pragma unroll
+        for (int i = 0; i < kLocalCands / THREADS; ++i) m[i] = tid + i * THREADS < a.B_c ? a.map[tid + i * THREADS] : -1;
+        len = lane < a.B_u ? user_len(a, lane) : 0;
+        if (lane < a.B_u && a.lens && a.lens[lane] != len) err = kTrainStLens;
+        if (tid < kLocalUsers) s.count[tid] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kLocalCands / THREADS; ++i) {
+            if (m[i] >= 0 && m[i] < a.B_u) atomicAdd(&s.count[m[i]], 1);
+            else if (m[i] != -1) err |= kTrainStMap;
+        }
+        if (err) atomicOr(a.status, err);
+        __syncthreads();
+        const int n = lane < a.B_u ? s.count[lane] : 0;
+        rows = n * a.G * a.L_q;
+        const int own = n | (rows + kTileRows - 1) / kTileRows << 12 | ((rows + 63) / 64) << 20;
+        before = own;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int x = __shfl_up(before, d);
+            if (lane >= d) before += x;
+        }
+        before -= own;
+    }
+    // The user whose tile this is; user -1 if there is none.
+    __device__ __forceinline__ TileEntry tile(int at) const {
+        const int first = before >> 12 & 255, n = (rows + kTileRows - 1) / kTileRows;
+        const uint64_t here = __ballot(at >= first && at < first + n);
+        if (!here) return TileEntry{-1, 0, 0, 0, 0, 0, {0, 0}};
+        const int u = __ffsll((unsigned long long)here) - 1, b = __builtin_amdgcn_readlane(before, u), row = (at - (b >> 12 & 255)) * kTileRows;
+        return TileEntry{u, row, b & 4095, __builtin_amdgcn_readlane(rows, u), __builtin_amdgcn_readlane(len, u), (b >> 20) + row / 64, {0, 0}};
+    }
+    // All rows of user u.
+    __device__ __forceinline__ ChunkEntry chunk(int u) const {
+        return ChunkEntry{u, __builtin_amdgcn_readlane(before, u) >> 20, (__builtin_amdgcn_readlane(rows, u) + 63) / 64, -1, __builtin_amdgcn_readlane(len, u), {0, 0, 0}};
+    }
+    // User u's candidates to s.list.
+    __device__ __forceinline__ void list(const TrainArgs &a, LocalLds &s, int u) const {
+        const int tid = (int)threadIdx.x, lane = tid & 63, wv = tid >> 6;
+        uint64_t mine[kLocalCands / THREADS];
+#pragma unroll
+        for (int i = 0; i < kLocalCands / THREADS; ++i) {
+            mine[i] = __ballot(m[i] == u);
+            if (lane == 0) s.part[i * (THREADS / 64) + wv] = __popcll(mine[i]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kLocalCands / THREADS; ++i) {
+            int at = __popcll(mine[i] & ((1ull << lane) - 1));
+            for (int w = 0; w < i * (THREADS / 64) + wv; ++w) at += s.part[w];
+            if (m[i] == u) s.list[at] = tid + i * THREADS;
+        }
+        __syncthreads();
+    }
+};
+
+// O = 0 and lse = -inf, or dQ = 0, of candidates whose map entry is no user: block `block` of `blocks` of them.
+__device__ __forceinline__ void fill_padding(const TrainArgs &a, int head_dim, bool backward, int block, int blocks) {
+    const int n = a.H_q * a.L_q, lane = (int)threadIdx.x & 63, waves = (int)blockDim.x / 64;
+    for (int b0 = (block * waves + ((int)threadIdx.x >> 6)) * 64; b0 < a.B_c; b0 += blocks * waves * 64) {
+        const int u = b0 + lane < a.B_c ? a.map[b0 + lane] : 0;
+        uint64_t none = __ballot(u < 0 || u >= a.B_u);
+        while (none) {
+            const int b = b0 + __ffsll((unsigned long long)none) - 1;
+            none &= none - 1;
+            uint16_t *to = backward ? a.dQ + b * a.dq_cand : a.O + b * a.o_cand;
+            const int64_t head = backward ? a.dq_head : a.o_head, query = backward ? a.dq_query : a.o_query;
+            for (int i = lane; i < n * (head_dim / 8); i += 64) {
+                const int r = i / (head_dim / 8), h = r / a.L_q;
+                *reinterpret_cast<u32x4_t *>(to + h * head + (r - h * a.L_q) * query + 8 * (i % (head_dim / 8))) = (u32x4_t){0, 0, 0, 0};
+            }
+            if (!backward)
+                for (int i = lane; i < n; i += 64) a.lse[(int64_t)b * n + i] = neg_inf();
+        }
+    }
 }
 
 // Blocks go round the 8 dies in turn; runs of 8 (or 4) neighbouring units, which share what they read, go to one

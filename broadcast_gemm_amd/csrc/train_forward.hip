@@ -15,19 +15,31 @@ namespace {
 
 constexpr float kSlack = 8.0f;
 
-template <int HD, int WAVES, bool DROP>
+template <int HD, int WAVES, bool DROP, bool LOCAL>
 __global__ void __launch_bounds__(64 * WAVES, 2) train_fwd_kernel(TrainArgs a) {
     constexpr int TK = HD / 16, DT = HD / 32, STAGE = Rows<HD>::matrix(64), ROWS = 32 * WAVES;
     __shared__ __align__(16) char k_lds[2][STAGE], v_lds[2][STAGE];
     __shared__ int s_most[WAVES];
     const int unit = unit_of((int)blockIdx.x, a.tiles * a.H_kv * a.splits);
-    if (unit < 0) return;   // the whole block: no barrier has run
+    if (unit < 0) {   // the whole block: no barrier has run
+        if (LOCAL && blockIdx.x == gridDim.x - 1) fill_padding(a, HD, false, 0, 1);
+        return;
+    }
     const int tile = unit % a.tiles, hk = unit / a.tiles % a.H_kv, split = unit / a.tiles / a.H_kv;
-    const TileEntry t = a.tile[tile];
+    Local<64 * WAVES> local;
+    __shared__ LocalLds s_local;
+    TileEntry t;
+    if constexpr (LOCAL) {
+        local.count(a, s_local);
+        t = local.tile(tile);
+        if (a.splits > 1 && hk == 0 && split == 0 && threadIdx.x == 0) a.tile[tile] = t;   // for the launch that joins
+    } else {
+        t = a.tile[tile];
+    }
     const int u = __builtin_amdgcn_readfirstlane(t.user), row0 = __builtin_amdgcn_readfirstlane(t.row);
     if (u < 0) return;
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 5, j = lane & 31;
-    const int first = __builtin_amdgcn_readfirstlane(t.first), n_rows = __builtin_amdgcn_readfirstlane(t.rows), len = __builtin_amdgcn_readfirstlane(t.len);
+    const int n_rows = __builtin_amdgcn_readfirstlane(t.rows), len = __builtin_amdgcn_readfirstlane(t.len);
 
     // The first keys are on their way before the rows.
     const int key0 = split * a.split_keys;
@@ -38,6 +50,15 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_fwd_kernel(TrainArgs a) {
     load_k(0);
     load_v(0);
     load_k(1);
+    if constexpr (LOCAL) {
+        local.list(a, s_local, u);
+        if (a.splits > 1 && hk == 0 && split == 0 && row0 == 0)
+            for (int i = tid; i * a.G * a.L_q < n_rows; i += 64 * WAVES) a.perm[t.first + i] = s_local.list[i];
+    }
+    auto place = [&](int r) {
+        if constexpr (LOCAL) return place_of(a, s_local.list, hk, r);
+        else return place_of(a, a.perm + t.first, hk, r);
+    };
     // The lane's row.
     const int r = row0 + wv * 32 + j;
     const bool live = r < n_rows;
@@ -45,7 +66,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_fwd_kernel(TrainArgs a) {
     uint32_t row, head;
     u32x4_t qf[TK];
     {
-        const Place at = place_of(a, first, hk, live ? r : 0);
+        const Place at = place(live ? r : 0);
         limit = live ? limit_of(a, at, len) : 0;
         row = (uint32_t)(at.cand * a.L_q + at.query);
         head = (uint32_t)at.head;
@@ -170,7 +191,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_fwd_kernel(TrainArgs a) {
     }
     const float sum = sum_halves(l);
     if (!live) return;
-    const Place at = place_of(a, first, hk, r);   // again, rather than kept
+    const Place at = place(r);   // again, rather than kept
     if (a.splits == 1) {
         const float by = sum > 0.f || sum != sum ? a.keep / sum : 0.f;   // a row that sees nothing is 0
         uint16_t *to = a.O + at.cand * a.o_cand + at.head * a.o_head + at.query * a.o_query + 8 * g;
@@ -228,18 +249,23 @@ __global__ void __launch_bounds__(256) train_fwd_join_kernel(TrainArgs a) {
         sum += sums[y][row];
     }
     const float by = sum > 0.f || sum != sum ? a.keep / sum : 0.f;
-    const Place p = place_of(a, t.first, hk, r);
+    const Place p = place_of(a, a.perm + t.first, hk, r);
     *reinterpret_cast<u32x2_t *>(a.O + p.cand * a.o_cand + p.head * a.o_head + p.query * a.o_query + 4 * x) =
         (u32x2_t){pack_bf16x2(o[0] * by, o[1] * by), pack_bf16x2(o[2] * by, o[3] * by)};
     if (x == 0) a.lse[((int64_t)p.cand * a.H_q + p.head) * a.L_q + p.query] = top * kLn2 + logf(sum);
 }
 
 template <int HD, int WAVES>
-hipError_t launch(const TrainArgs &a, hipStream_t s) {
+hipError_t launch(const TrainArgs &a, bool local, hipStream_t s) {
     const int64_t units = (int64_t)a.tiles * a.H_kv * a.splits;
-    const dim3 grid(blocks_of(units));
-    if (a.edge) hipLaunchKernelGGL((train_fwd_kernel<HD, WAVES, true>), grid, dim3(64 * WAVES), 0, s, a);
-    else hipLaunchKernelGGL((train_fwd_kernel<HD, WAVES, false>), grid, dim3(64 * WAVES), 0, s, a);
+    const dim3 grid(blocks_of(units) + local), block(64 * WAVES);   // one more for the rows of padding
+    if (local) {
+        if (a.edge) hipLaunchKernelGGL((train_fwd_kernel<HD, WAVES, true, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((train_fwd_kernel<HD, WAVES, false, true>), grid, block, 0, s, a);
+    } else {
+        if (a.edge) hipLaunchKernelGGL((train_fwd_kernel<HD, WAVES, true, false>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((train_fwd_kernel<HD, WAVES, false, false>), grid, block, 0, s, a);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     static_assert(kTileRows == 32 * WAVES, "the layout's tiles");
@@ -249,8 +275,8 @@ hipError_t launch(const TrainArgs &a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_train_forward(const TrainArgs &a, const TrainLayout &, int head_dim, hipStream_t s) {
-    return head_dim == 128 ? launch<128, kRowWaves>(a, s) : launch<64, kRowWaves>(a, s);
+hipError_t launch_train_forward(const TrainArgs &a, const TrainLayout &w, int head_dim, hipStream_t s) {
+    return head_dim == 128 ? launch<128, kRowWaves>(a, w.local, s) : launch<64, kRowWaves>(a, w.local, s);
 }
 
 }  // namespace ikbo

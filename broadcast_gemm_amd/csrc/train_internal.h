@@ -21,11 +21,13 @@ constexpr int keys_of(int head_dim) { return head_dim == 128 ? 256 : 128; }
 // Waves and rows of a block of the forward and of dQ.  Two blocks of 4 waves a CU: 70:1 with head 128, forward 154 us and dQ
 // 220, where one of 8 waves takes 180 and 253: its waves meet at every barrier.
 constexpr int kRowWaves = 4, kTileRows = 32 * kRowWaves;
+constexpr int kLocalUsers = 64, kLocalCands = 1024;   // calls up to which blocks find their places for themselves
 constexpr int kJoiners = 8;       // groups of lanes that add up the parts of a row
 
 // How the work is cut, and the byte offsets of the workspace's parts.  A user's rows of one shared head are its
 // candidates' queries of all heads of the group: slot * G * L_q + g * L_q + l, with the candidates in order.
 struct TrainLayout {
+    bool local;                        // every block finds its own place: no launch of the grouping
     int tiles;                         // tiles of rows per shared head, at most
     int splits, split_keys;            // parts of the keys, each a multiple of 64
     int chunk_rows;                    // rows to a block of dK and dV, at most

@@ -70,33 +70,12 @@ __device__ __forceinline__ int find(const int *at, int n, int x) {
     return lo;
 }
 
-__device__ void fill_padding(const TrainArgs &a, int head_dim, bool backward) {
-    const int n = a.H_q * a.L_q, lane = (int)threadIdx.x & 63;
-    const int w = ((int)blockIdx.x - 1) * (kThreads / 64) + ((int)threadIdx.x >> 6), waves = ((int)gridDim.x - 1) * (kThreads / 64);
-    for (int b0 = w * 64; b0 < a.B_c; b0 += waves * 64) {
-        const int u = b0 + lane < a.B_c ? a.map[b0 + lane] : 0;
-        uint64_t none = __ballot(u < 0 || u >= a.B_u);
-        while (none) {
-            const int b = b0 + __ffsll((unsigned long long)none) - 1;
-            none &= none - 1;
-            uint16_t *to = backward ? a.dQ + b * a.dq_cand : a.O + b * a.o_cand;
-            const int64_t head = backward ? a.dq_head : a.o_head, query = backward ? a.dq_query : a.o_query;
-            for (int i = lane; i < n * (head_dim / 8); i += 64) {
-                const int r = i / (head_dim / 8), h = r / a.L_q;
-                *reinterpret_cast<u32x4_t *>(to + h * head + (r - h * a.L_q) * query + 8 * (i % (head_dim / 8))) = (u32x4_t){0, 0, 0, 0};
-            }
-            if (!backward)
-                for (int i = lane; i < n; i += 64) a.lse[(int64_t)b * n + i] = neg_inf();
-        }
-    }
-}
-
 __global__ void __launch_bounds__(kThreads) train_prep_kernel(TrainArgs a, int waves, int steps, int head_dim, int backward) {
     extern __shared__ int sh[];
     __shared__ __align__(16) int s_scan[kThreads / 64];
     __shared__ int s_total[5];   // tiles, chunks, slots, notes, joins
     if (blockIdx.x > 0) {
-        fill_padding(a, head_dim, backward);
+        fill_padding(a, head_dim, backward, (int)blockIdx.x - 1, (int)gridDim.x - 1);
         return;
     }
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = tid >> 6, B = a.B_u, keys = B * steps;

@@ -155,6 +155,26 @@ def test_many_users_and_candidates():
     compare(x.run(), x.want(), "most users")
 
 
+@pytest.mark.parametrize("shape", [
+    # B_u, B_c, H_q, H_kv, L_q, L_kv, dim: around the sizes where blocks find their own places, with and without cut keys
+    (64, 1024, 1, 1, 4, 40, 64), (64, 1025, 1, 1, 1, 40, 64), (65, 1024, 1, 1, 1, 40, 64), (2, 1024, 4, 1, 1, 300, 64), (2, 1024, 4, 1, 1, 40, 128),
+    (1, 512, 1, 1, 1, 600, 64), (1, 513, 1, 1, 1, 600, 64), (1, 128, 4, 1, 1, 30, 128), (16, 512, 4, 1, 1, 520, 64), (16, 511, 4, 1, 1, 520, 128),
+    (16, 513, 4, 1, 1, 520, 128), (64, 1, 8, 1, 16, 1300, 128), (33, 1000, 2, 1, 1, 20, 64),
+    # and of many candidates, whose grouping takes several turns, and many rows of a user
+    (23, 9001, 1, 1, 2, 20, 64), (3, 2500, 2, 1, 1, 100, 128), (2, 1300, 2, 1, 2, 70, 64)])
+@pytest.mark.parametrize("dropout", [0.0, 0.2])
+def test_both_ways_of_grouping(shape, dropout):
+    log(f"grouping {shape} dropout={dropout}")
+    x = Inputs(sum(shape), *shape, causal=bool(dropout) or shape[1] % 2 == 1, dropout=dropout, padding=shape[1] // 7)
+    if shape[1] > 8:
+        x.mp[::9] = shape[0] // 2   # one user more often than the others
+    st = word()
+    got, again = x.run(st=st), x.run(st=st)
+    assert status(st) == bga.IKBO_OK
+    assert all(torch().equal(got[n], again[n]) for n in got)
+    compare(got, x.want(), f"{shape}")
+
+
 def test_strided_tensors():
     """Queries and gradients with tokens before heads, K and V out of one projection, K shared by all users, an
     expanded upstream gradient."""
@@ -250,6 +270,23 @@ def test_conditions_are_recorded():
     compare(got, x.want(), "map out of range")
 
 
+def test_conditions_of_many_candidates_are_recorded():
+    """As above, where the grouping is a launch of its own."""
+    x = Inputs(13, 70, 99, 2, 1, 2, 40, 64)
+    st = word()
+    x.lens[:] = 20
+    x.lens[69] = -1
+    got = x.run(st=st)
+    assert status(st) == bga.IKBO_ERR_PAGE_RANGE and status(st) == bga.IKBO_OK
+    x.lens[69] = 0
+    compare(got, x.want(), "clamped lengths")
+    x.mp[98] = 70
+    got = x.run(st=st)
+    assert status(st) == bga.IKBO_ERR_MAP_RANGE
+    x.mp[98] = -1
+    compare(got, x.want(), "map out of range")
+
+
 def test_no_candidates_and_padding_alone():
     t = torch()
     x = Inputs(14, 2, 3, 2, 1, 2, 40, 64)
@@ -280,7 +317,8 @@ def test_streams_and_replayed_graphs():
     """Two captured steps that share nothing but their inputs, replayed between eager work on two streams, with other
     numbers and lengths for every replay."""
     t = torch()
-    xs = [Inputs(16, 4, 50, 4, 2, 3, 200, 64, dropout=0.2), Inputs(17, 2, 31, 2, 2, 2, 900, 128, causal=True, dropout=0.1)]
+    xs = [Inputs(16, 4, 50, 4, 2, 3, 200, 64, dropout=0.2), Inputs(17, 2, 31, 2, 2, 2, 900, 128, causal=True, dropout=0.1),
+          Inputs(18, 70, 300, 2, 2, 2, 300, 64, dropout=0.1)]
     steps = []
     for x in xs:
         st, mp, how = word(), dev(x.mp), x.how()
