@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kMostSteps = 16, kBatch = 8;     // of the position; turns of a wave
+constexpr int kOrders = 32;                   // of the tiles' work
 
 // Exclusive prefix sums of v over the lanes of a wave; the totals in all.
 template <int N>
@@ -73,6 +74,7 @@ __device__ __forceinline__ int find(const int *at, int n, int x) {
 __global__ void __launch_bounds__(kThreads) train_prep_kernel(TrainArgs a, int waves, int steps, int head_dim, int backward) {
     extern __shared__ int sh[];
     __shared__ __align__(16) int s_scan[kThreads / 64];
+    __shared__ int s_orders[kOrders * kThreads / 64];
     __shared__ int s_total[5];   // tiles, chunks, slots, notes, joins
     if (blockIdx.x > 0) {
         fill_padding(a, head_dim, backward, (int)blockIdx.x - 1, (int)gridDim.x - 1);
@@ -203,13 +205,36 @@ __global__ void __launch_bounds__(kThreads) train_prep_kernel(TrainArgs a, int w
         a.perm[from + before] = b;
     });
     __syncthreads();
-    for (int t = tid; t < a.tiles; t += kThreads) {
-        TileEntry x{-1, 0, 0, 0, 0, 0, {0, 0}};
-        if (t < s_total[0]) {
-            const int u = find(t_at, B, t), row = (t - t_at[u]) * kTileRows;
-            x = TileEntry{u, row, offs[u], (offs[u + 1] - offs[u]) * GL, lens[u], n_at[u] + row / 64, {0, 0}};
+    const auto tile = [&](int t) {
+        if (t >= s_total[0]) return TileEntry{-1, 0, 0, 0, 0, 0, {0, 0}};
+        const int u = find(t_at, B, t), row = (t - t_at[u]) * kTileRows;
+        return TileEntry{u, row, offs[u], (offs[u + 1] - offs[u]) * GL, lens[u], n_at[u] + row / 64, {0, 0}};
+    };
+    if (a.tiles <= kThreads) {
+        // Those that see most come first, so that no long block starts when the others end (59 users, 4096 candidates with positions:
+        // forward 63 -> 47 us; 23 users, 8001 candidates: dQ 90 -> 68 us).  The order is a stable counting sort again; rows in the
+        // order of their positions are taken to see evenly less and less.  More tiles than threads fill the card several times.
+        const TileEntry x = tile(tid);
+        const float sees = x.user < 0 ? 0.f : a.positions ? (float)x.len * (float)(x.rows - x.row) / (float)x.rows : (float)x.len;
+        const int k = x.user < 0 ? kOrders - 1 : kOrders - 2 - min(kOrders - 2, (int)(sees * (float)(kOrders - 1) / (float)(a.L_kv + 1)));
+        uint64_t same = ~0ull;
+#pragma unroll
+        for (int bit = 1; bit < kOrders; bit <<= 1) {
+            const uint64_t m = __ballot(k & bit);
+            same &= k & bit ? m : ~m;
         }
-        a.tile[t] = x;
+        if (tid < kOrders * kThreads / 64) s_orders[tid] = 0;
+        __syncthreads();
+        if ((same & below) == 0) s_orders[k * (kThreads / 64) + wv] = __popcll(same);
+        __syncthreads();
+        int total;
+        const int n = tid < kOrders * kThreads / 64 ? s_orders[tid] : 0, before = scan_block(n, total, s_scan);
+        if (tid < kOrders * kThreads / 64) s_orders[tid] = before;
+        __syncthreads();
+        const int to = s_orders[k * (kThreads / 64) + wv] + __popcll(same & below);
+        if (to < a.tiles) a.tile[to] = x;
+    } else {
+        for (int t = tid; t < a.tiles; t += kThreads) a.tile[t] = tile(t);
     }
     for (int t = s_total[4] + tid; t < a.n_joins; t += kThreads) a.joins[t] = make_int4(0, 0, 0, 0);
     for (int t = tid; t < a.chunks; t += kThreads) {
