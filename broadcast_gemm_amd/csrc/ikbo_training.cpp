@@ -30,7 +30,7 @@ int check_shape(int B_u, int B_c, int H_q, int H_kv, int L_q, int L_kv, int head
         return IKBO_ERR_UNSUPPORTED;   // rows and keys are counted in 32 bits
     const TrainLayout w = train_layout(B_u, B_c, H_q, H_kv, L_q, L_kv, head_dim, true);
     // Threads of one launch are counted in 32 bits.
-    const int64_t most = std::max(((int64_t)w.tiles + 7) * w.splits, (int64_t)w.chunks * ((L_kv + keys_of(head_dim) - 1) / keys_of(head_dim))) * H_kv;
+    const int64_t most = std::max((int64_t)w.tiles * w.splits, (int64_t)w.chunks * ((L_kv + keys_of(head_dim) - 1) / keys_of(head_dim))) * H_kv;
     return most + 64 > kInt / kThreads ? IKBO_ERR_UNSUPPORTED : IKBO_OK;
 }
 

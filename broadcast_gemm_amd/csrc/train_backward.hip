@@ -26,10 +26,10 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dq_kernel(TrainArgs a) {
     constexpr int TK = HD / 16, DT = HD / 32, STAGE = Rows<HD>::matrix(64), ROWS = 32 * WAVES;
     __shared__ __align__(16) char lds[2][2][STAGE];
     __shared__ int s_most[WAVES], s_least[WAVES];
-    const int unit = unit_of((int)blockIdx.x, tile_units(a));
+    const int unit = unit_of((int)blockIdx.x, a.tiles * a.H_kv * a.splits);
     if (LOCAL && blockIdx.x == gridDim.x - 1) fill_padding(a, HD, true, 0, 1);
+    if (unit < 0) return;   // the whole block: no barrier has run
     const auto [tile, hk, split] = tile_unit(a, unit);
-    if (unit < 0 || tile >= a.tiles) return;   // the whole block: no barrier has run
     Local<64 * WAVES> local;
     __shared__ LocalLds s_local;
     TileEntry t;
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dkv_kernel(TrainArgs a) {
     const char *from_notes = reinterpret_cast<const char *>(a.notes + (int64_t)hk * a.n_notes + __builtin_amdgcn_readfirstlane(ch.note));
     auto load_notes = [&](int n) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) load_to_lds(from_notes + n * 3072 + 1024 * i, 16 * lane, lds_address(&notes[n % 3]) + 1024 * i);
+        for (int i = 0; i < 3; ++i) load_to_lds(from_notes + n * (int)sizeof(RowNotes) + 1024 * i, 16 * lane, lds_address(&notes[n % 3]) + 1024 * i);
     };
     auto load = [&](int st) {
         const RowNotes &x = notes[st % 3];
@@ -522,7 +522,7 @@ hipError_t launch(const TrainArgs &a, bool local, hipStream_t s) {
     static_assert(keys_of(HD) == 32 * KW, "the layout's chunks");
     hipError_t e;
     if (a.tiles > 0) {
-        const dim3 grid(blocks_of(tile_units(a)) + local), block(64 * WAVES);   // one more for the rows of padding
+        const dim3 grid(blocks_of((int64_t)a.tiles * a.H_kv * a.splits) + local), block(64 * WAVES);   // one more for the rows of padding
         if (local) {
             if (a.edge) hipLaunchKernelGGL((train_dq_kernel<HD, WAVES, true, true>), grid, block, 0, s, a);
             else hipLaunchKernelGGL((train_dq_kernel<HD, WAVES, false, true>), grid, block, 0, s, a);

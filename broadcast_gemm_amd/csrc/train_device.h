@@ -343,15 +343,14 @@ __device__ __forceinline__ int unit_of(int block, int n) {
 }
 // Blocks for n units.
 inline unsigned blocks_of(int64_t n) { return (unsigned)((n + 63) / 64 * 64); }
-// Units of tiles of rows: eight tiles of a shared head, the same of the next head, and so on; then the next eight, since
-// the grouping puts the tiles in the order of their work; then the next part of the keys.
+// Units of tiles of rows: eight tiles (or the last ones) of a shared head, the same of the next head, and so on; then the
+// next eight, since the grouping puts the tiles in the order of their work; then the next part of the keys.
 struct TileUnit {
     int tile, hk, split;
 };
-__device__ __host__ __forceinline__ int tile_units(const TrainArgs &a) { return (a.tiles + 7) / 8 * 8 * a.H_kv * a.splits; }
 __device__ __forceinline__ TileUnit tile_unit(const TrainArgs &a, int unit) {
-    const int eights = (a.tiles + 7) / 8, x = unit >> 3;
-    return TileUnit{x / a.H_kv % eights * 8 + (unit & 7), x % a.H_kv, x / a.H_kv / eights};
+    const int all = a.tiles * a.H_kv, x = unit % all, first = x / (8 * a.H_kv) * 8, n = min(8, a.tiles - first), y = x - first * a.H_kv;
+    return TileUnit{first + y % n, y / n, unit / all};
 }
 
 // Element quads 2 p and 2 p + 1 of a result column, rounded: 8 consecutive rows 16 p + 8 g .. of it for this lane.

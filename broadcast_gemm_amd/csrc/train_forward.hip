@@ -20,10 +20,10 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_fwd_kernel(TrainArgs a) {
     constexpr int TK = HD / 16, DT = HD / 32, STAGE = Rows<HD>::matrix(64), ROWS = 32 * WAVES;
     __shared__ __align__(16) char k_lds[2][STAGE], v_lds[2][STAGE];
     __shared__ int s_most[WAVES];
-    const int unit = unit_of((int)blockIdx.x, tile_units(a));
+    const int unit = unit_of((int)blockIdx.x, a.tiles * a.H_kv * a.splits);
     if (LOCAL && blockIdx.x == gridDim.x - 1) fill_padding(a, HD, false, 0, 1);
+    if (unit < 0) return;   // the whole block: no barrier has run
     const auto [tile, hk, split] = tile_unit(a, unit);
-    if (unit < 0 || tile >= a.tiles) return;   // the whole block: no barrier has run
     Local<64 * WAVES> local;
     __shared__ LocalLds s_local;
     TileEntry t;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(256) train_fwd_join_kernel(TrainArgs a) {
 
 template <int HD, int WAVES>
 hipError_t launch(const TrainArgs &a, bool local, hipStream_t s) {
-    const dim3 grid(blocks_of(tile_units(a)) + local), block(64 * WAVES);   // one more for the rows of padding
+    const dim3 grid(blocks_of((int64_t)a.tiles * a.H_kv * a.splits) + local), block(64 * WAVES);   // one more for the rows of padding
     if (local) {
         if (a.edge) hipLaunchKernelGGL((train_fwd_kernel<HD, WAVES, true, true>), grid, block, 0, s, a);
         else hipLaunchKernelGGL((train_fwd_kernel<HD, WAVES, false, true>), grid, block, 0, s, a);

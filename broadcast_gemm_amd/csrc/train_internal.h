@@ -16,7 +16,7 @@ int hip_fail(hipError_t e, const char *what);
 // Bits of the caller's status word, as in the cached histories.
 constexpr uint32_t kTrainStMap = 1u, kTrainStLens = 2u;
 
-// Keys to a block of dK and dV: 4 waves of 64 or 32.
+// Keys to a block of dK and dV: 8 waves or 4, of 32.
 constexpr int keys_of(int head_dim) { return head_dim == 128 ? 256 : 128; }
 // Waves and rows of a block of the forward and of dQ.  Two blocks of 4 waves a CU: 70:1 with head 128, forward 154 us and dQ
 // 220, where one of 8 waves takes 180 and 253: its waves meet at every barrier.
@@ -55,7 +55,7 @@ struct RowNotes {
     int most[2];                       // largest limit of each 32
     int unused[190];                   // whole KB
 };
-static_assert(sizeof(RowNotes) == 3072, "three loads of a wave");
+static_assert(sizeof(RowNotes) == 3 * 1024, "three loads of a wave");
 
 struct TrainArgs {
     const uint16_t *Q, *K, *V;

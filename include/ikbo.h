@@ -442,7 +442,8 @@ int ikbo_kv4_attention(const ikbo_kv4_attention_args *args, void *stream);
  * (multiples of 8, not negative; those of inputs may be 0) and contiguous heads, 16-byte aligned; lse [B_c][H_q][L_q] float32,
  * dense.  Outputs overlap nothing.  Scores, statistics and sums are float32; P and dS reach the matrix cores as bf16; outputs are rounded
  * once.  The same call gives the same bits.  scale = 0 means 1/sqrt(head_dim); negative, NaN and infinite scales are
- * INVALID_ARG.  head_dim 64 or 128, H_q a multiple of H_kv, 1 <= B_u <= IKBO_KV_MAX_USERS.
+ * INVALID_ARG.  head_dim 64 or 128, H_q a multiple of H_kv, 1 <= B_u <= IKBO_KV_MAX_USERS; tokens of K and of V at most
+ * 2^24 elements apart, 4 L_kv and 4 B_c L_q H_q below 2^31, and no more blocks than a launch holds, else UNSUPPORTED.
  * workspace: ikbo_attention_workspace bytes, 16-byte aligned, not shared with a call that may overlap; nothing in it has
  * to be kept between calls.
  */

@@ -63,7 +63,7 @@ COMMON = [
     (dict(lse=P + 2), ALIGNMENT), (dict(map=P + 1), ALIGNMENT), (dict(lens=P + 2), ALIGNMENT), (dict(positions=P + 2), ALIGNMENT),
     (dict(rng=P + 4), ALIGNMENT), (dict(workspace=P + 8), ALIGNMENT), (dict(status=0), INVALID), (dict(workspace=0), INVALID),
     (dict(workspace_bytes=255), INVALID), (dict(Q=0), INVALID), (dict(K=0), INVALID), (dict(V=0), INVALID), (dict(O=0), INVALID),
-    (dict(lse=0), INVALID), (dict(map=0), INVALID)]
+    (dict(lse=0), INVALID), (dict(map=0), INVALID), (dict(k_token=(1 << 24) + 8), UNSUPPORTED), (dict(v_token=(1 << 24) + 8), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("change, want", COMMON + [(dict(B_c=0, Q=0, O=0, map=0), OK)])
