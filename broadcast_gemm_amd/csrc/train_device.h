@@ -335,7 +335,9 @@ __device__ __forceinline__ void fill_padding(const TrainArgs &a, int head_dim, b
 }
 
 // Blocks go round the 8 dies in turn; runs of 8 (or 4) neighbouring units, which share what they read, go to one
-// die.  Whole eighths of the units to each die would leave the dies uneven where units differ.  Unit of this block among n, or -1.
+// die: 70:1 forward 155 -> 151 us, 10:1 dK and dV 77 -> 65 (dQ 46 -> 50).  Few units are dealt one by one, so that all dies
+// have some.  Whole eighths of the units to each die leave the dies uneven where units differ (70:1 dK and dV 462).  Unit
+// of this block among n, or -1.
 __device__ __forceinline__ int unit_of(int block, int n) {
     const int log_run = n >= 512 ? 3 : n >= 128 ? 2 : 0, i = block >> 3;
     const int at = ((((i >> log_run) << 3) + (block & 7)) << log_run) + (i & ((1 << log_run) - 1));

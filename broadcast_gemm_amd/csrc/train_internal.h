@@ -16,7 +16,8 @@ int hip_fail(hipError_t e, const char *what);
 // Bits of the caller's status word, as in the cached histories.
 constexpr uint32_t kTrainStMap = 1u, kTrainStLens = 2u;
 
-// Keys to a block of dK and dV: 8 waves or 4, of 32.
+// Keys to a block of dK and dV: 8 waves or 4, of 32.  Head 128: 8 waves share the rows' staging (259 us, 4 waves 270); head 64:
+// 4, two blocks of which stand on a CU (65 us, 8 waves 88; 26 users, 256 candidates of 33 queries, dropout).
 constexpr int keys_of(int head_dim) { return head_dim == 128 ? 256 : 128; }
 // Waves and rows of a block of the forward and of dQ.  Two blocks of 4 waves a CU: 70:1 with head 128, forward 154 us and dQ
 // 220, where one of 8 waves takes 180 and 253: its waves meet at every barrier.
