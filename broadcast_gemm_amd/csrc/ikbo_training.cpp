@@ -89,6 +89,8 @@ TrainArgs args_of(const ikbo_attention_args &a, const TrainLayout &w) {
     t.B_u = a.B_u; t.B_c = a.B_c; t.H_q = a.H_q; t.H_kv = a.H_kv; t.G = a.H_q / a.H_kv; t.L_q = a.L_q; t.L_kv = a.L_kv;
     t.splits = w.splits; t.split_keys = w.split_keys; t.tiles = w.tiles;
     t.chunk_rows = w.chunk_rows; t.chunks = w.chunks; t.slots = w.slots; t.n_joins = w.joins; t.n_notes = w.notes;
+    // Blocks for the rows of padding: one for each 256 KB of output (1024 threads; 256 in calls without the grouping).
+    t.pads = (int)std::clamp<int64_t>((int64_t)a.B_c * a.H_q * a.L_q * a.head_dim >> 17, 1, 64);
     t.scale = a.scale > 0.0f ? a.scale : 1.0f / std::sqrt((float)a.head_dim);
     t.scale_log2 = (float)(t.scale * 1.4426950408889634);
     t.edge = (uint32_t)steps(a.dropout, 256);

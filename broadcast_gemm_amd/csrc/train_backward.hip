@@ -10,7 +10,8 @@
 // dK and dV: a wave keeps 32 keys' K and V and their gradients in registers, and the block goes over a chunk of the
 // user's rows, staged in LDS 64 at a time: S = Q K^T, dP = dO V^T, dV^T += dO^T P, dK^T += Q^T dS.  Rows stand in the
 // results' rows here, so P and dS are the B operands as they stand.  The weights that stay are decided with the rows
-// in the lanes, as in the other kernels (one generator call for 16 tokens of a row), and the bits turned round (Turn).  Chunks of one user are joined by a third launch, in their order.
+// in the lanes, as in the other kernels (one generator call for 16 tokens of a row), and the bits turned round (Turn).
+// Chunks of one user are joined by a third launch, in their order.
 //
 // That is 7 products against the 5 that one pass needs; adding up dQ across key ranges instead would write and read 4
 // bytes an element for every range.  P and dS are rounded to bf16 for their products (half a step each, as the outputs); all
@@ -37,8 +38,14 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dq_kernel(TrainArgs a) {
     constexpr int TK = HD / 16, DT = HD / 32, STAGE = Rows<HD>::matrix(64), ROWS = 32 * WAVES;
     __shared__ __align__(16) char lds[2][2][STAGE];
     __shared__ int s_most[WAVES], s_least[WAVES];
+    if constexpr (LOCAL) {
+        const int pad = (int)blockIdx.x - (int)gridDim.x + a.pads;
+        if (pad >= 0) {   // the last blocks
+            fill_padding(a, HD, true, pad);
+            return;
+        }
+    }
     const int unit = unit_of((int)blockIdx.x, a.tiles * a.H_kv * a.splits);
-    if (LOCAL && blockIdx.x == gridDim.x - 1) fill_padding(a, HD, true, 0, 1);
     if (unit < 0) return;   // the whole block: no barrier has run
     const auto [tile, hk, split] = tile_unit(a, unit);
     Local<64 * WAVES> local;
@@ -534,7 +541,7 @@ hipError_t launch(const TrainArgs &a, bool local, hipStream_t s) {
     static_assert(keys_of(HD) == 32 * KW, "the layout's chunks");
     hipError_t e;
     if (a.tiles > 0) {
-        const dim3 grid(blocks_of((int64_t)a.tiles * a.H_kv * a.splits) + local), block(64 * WAVES);   // one more for the rows of padding
+        const dim3 grid(blocks_of((int64_t)a.tiles * a.H_kv * a.splits) + (local ? a.pads : 0)), block(64 * WAVES);   // some more for the rows of padding
         if (local) {
             if (a.edge) hipLaunchKernelGGL((train_dq_kernel<HD, WAVES, true, true>), grid, block, 0, s, a);
             else hipLaunchKernelGGL((train_dq_kernel<HD, WAVES, false, true>), grid, block, 0, s, a);

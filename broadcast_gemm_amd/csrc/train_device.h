@@ -313,10 +313,13 @@ struct Local {
     }
 };
 
-// O = 0 and lse = -inf, or dQ = 0, of candidates whose map entry is no user: block `block` of `blocks` of them.
-__device__ __forceinline__ void fill_padding(const TrainArgs &a, int head_dim, bool backward, int block, int blocks) {
-    const int n = a.H_q * a.L_q, lane = (int)threadIdx.x & 63, waves = (int)blockDim.x / 64;
-    for (int b0 = (block * waves + ((int)threadIdx.x >> 6)) * 64; b0 < a.B_c; b0 += blocks * waves * 64) {
+// O = 0 and lse = -inf, or dQ = 0, of candidates whose map entry is no user: block `block` of a.pads.  A wave looks at 64
+// candidates; where there are more waves than that, several share those of 64.
+__device__ __forceinline__ void fill_padding(const TrainArgs &a, int head_dim, bool backward, int block) {
+    const int n = a.H_q * a.L_q, waves = a.pads * (int)blockDim.x / 64, groups = max(1, (a.B_c + 63) / 64), share = max(1, waves / groups);
+    const int wave = block * (int)blockDim.x / 64 + ((int)threadIdx.x >> 6), lane = (int)threadIdx.x & 63, first = wave % share * 64 + lane, step = 64 * share;
+    if (wave >= waves / share * share) return;
+    for (int b0 = wave / share * 64; b0 < a.B_c; b0 += waves / share * 64) {
         const int u = b0 + lane < a.B_c ? a.map[b0 + lane] : 0;
         uint64_t none = __ballot(u < 0 || u >= a.B_u);
         while (none) {
@@ -324,12 +327,13 @@ __device__ __forceinline__ void fill_padding(const TrainArgs &a, int head_dim, b
             none &= none - 1;
             uint16_t *to = backward ? a.dQ + b * a.dq_cand : a.O + b * a.o_cand;
             const int64_t head = backward ? a.dq_head : a.o_head, query = backward ? a.dq_query : a.o_query;
-            for (int i = lane; i < n * (head_dim / 8); i += 64) {
-                const int r = i / (head_dim / 8), h = r / a.L_q;
-                *reinterpret_cast<u32x4_t *>(to + h * head + (r - h * a.L_q) * query + 8 * (i % (head_dim / 8))) = (u32x4_t){0, 0, 0, 0};
+            const int shift = head_dim == 128 ? 4 : 3;
+            for (int64_t i = first; i < (int64_t)n << shift; i += step) {
+                const int r = (int)(i >> shift), h = r / a.L_q;
+                *reinterpret_cast<u32x4_t *>(to + h * head + (r - h * a.L_q) * query + 8 * ((int)i & ((1 << shift) - 1))) = (u32x4_t){0, 0, 0, 0};
             }
             if (!backward)
-                for (int i = lane; i < n; i += 64) a.lse[(int64_t)b * n + i] = neg_inf();
+                for (int i = first; i < n; i += step) a.lse[(int64_t)b * n + i] = neg_inf();
         }
     }
 }

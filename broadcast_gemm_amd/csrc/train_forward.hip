@@ -10,9 +10,10 @@
 // taken (162 -> 149 us); a second set of waves for every other stage of keys loses (192), as blocks of 8 waves do (180).
 //
 // Measured: 15 users, 1024 candidates of 64 queries, 4 heads of 128, 777 to 1024 tokens (121 GFLOP): 149 us, 810 TFLOP/s,
-// where a library product of 8192^3 reaches 1378.  It is bound by what surrounds the
-// products: six vector instructions for a matrix one, 32 exponentials a lane and stage; LDS reads meet no conflict.  26 users, 256 candidates of 33 queries, 8 heads of 64, dropout (11.4 GFLOP): 35 us; at head 64 the weights
-// count double, and the generator's 28 wide products for 32 tokens come to them.
+// where a library product of 8192^3 reaches 1378.  It is bound by what surrounds the products: six vector instructions for a
+// matrix one, 32 exponentials a lane and stage; LDS reads meet no conflict.  26 users, 256 candidates of 33 queries, 8 heads
+// of 64, dropout (11.4 GFLOP): 35 us; at head 64 the weights count double, and the generator's 28 wide products for 32
+// tokens come to them.
 //
 // Few rows over long histories: the keys are cut into ranges, whose results a second launch joins (2 users of up to 32000
 // tokens, 48 candidates, 53 MB: 22 us and 6.5 to join; 614 us uncut).
@@ -28,8 +29,14 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_fwd_kernel(TrainArgs a) {
     constexpr int TK = HD / 16, DT = HD / 32, STAGE = Rows<HD>::matrix(64), ROWS = 32 * WAVES;
     __shared__ __align__(16) char k_lds[2][STAGE], v_lds[2][STAGE];
     __shared__ int s_most[WAVES];
+    if constexpr (LOCAL) {
+        const int pad = (int)blockIdx.x - (int)gridDim.x + a.pads;
+        if (pad >= 0) {   // the last blocks
+            fill_padding(a, HD, false, pad);
+            return;
+        }
+    }
     const int unit = unit_of((int)blockIdx.x, a.tiles * a.H_kv * a.splits);
-    if (LOCAL && blockIdx.x == gridDim.x - 1) fill_padding(a, HD, false, 0, 1);
     if (unit < 0) return;   // the whole block: no barrier has run
     const auto [tile, hk, split] = tile_unit(a, unit);
     Local<64 * WAVES> local;
@@ -264,7 +271,7 @@ __global__ void __launch_bounds__(256) train_fwd_join_kernel(TrainArgs a) {
 
 template <int HD, int WAVES>
 hipError_t launch(const TrainArgs &a, bool local, hipStream_t s) {
-    const dim3 grid(blocks_of((int64_t)a.tiles * a.H_kv * a.splits) + local), block(64 * WAVES);   // one more for the rows of padding
+    const dim3 grid(blocks_of((int64_t)a.tiles * a.H_kv * a.splits) + (local ? a.pads : 0)), block(64 * WAVES);   // some more for the rows of padding
     if (local) {
         if (a.edge) hipLaunchKernelGGL((train_fwd_kernel<HD, WAVES, true, true>), grid, block, 0, s, a);
         else hipLaunchKernelGGL((train_fwd_kernel<HD, WAVES, false, true>), grid, block, 0, s, a);

@@ -82,6 +82,7 @@ struct TrainArgs {
     float scale, scale_log2;
     uint32_t edge;                     // weights whose byte is below it are dropped
     float keep;                        // 256 / (256 - edge)
+    int pads;                          // blocks that fill the rows of padding
 };
 
 // What a launch of the grouping fills in for padding: O and lse, or dQ.

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads) train_prep_kernel(TrainArgs a, int w
     __shared__ int s_orders[kOrders * kThreads / 64];
     __shared__ int s_total[5];   // tiles, chunks, slots, notes, joins
     if (blockIdx.x > 0) {
-        fill_padding(a, head_dim, backward, (int)blockIdx.x - 1, (int)gridDim.x - 1);
+        fill_padding(a, head_dim, backward, (int)blockIdx.x - 1);
         return;
     }
     const int tid = (int)threadIdx.x, lane = tid & 63, wv = tid >> 6, B = a.B_u, keys = B * steps;
@@ -260,8 +260,7 @@ hipError_t launch_train_prep(const TrainArgs &a, bool backward, int head_dim, hi
     const int lds = 4 * (waves * a.B_u * steps + others_ints);
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(train_prep_kernel), hipFuncAttributeMaxDynamicSharedMemorySize, 4 * kInts);
     if (e != hipSuccess) return e;
-    const int others = std::min(64, (a.B_c + 1023) / 1024);
-    hipLaunchKernelGGL(train_prep_kernel, dim3(1 + others), dim3(kThreads), lds, s, a, waves, steps, head_dim, (int)backward);
+    hipLaunchKernelGGL(train_prep_kernel, dim3(1 + a.pads), dim3(kThreads), lds, s, a, waves, steps, head_dim, (int)backward);
     return hipGetLastError();
 }
 

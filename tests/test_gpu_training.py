@@ -175,6 +175,16 @@ def test_both_ways_of_grouping(shape, dropout):
     compare(got, x.want(), f"{shape}")
 
 
+@pytest.mark.parametrize("shape", [(3, 700, 6, 2, 4, 30, 64), (70, 1500, 2, 1, 8, 20, 128), (2, 65, 64, 64, 40, 10, 64)])
+def test_mostly_padding(shape):
+    """Nine of ten candidates are padding: their rows are shared by many waves."""
+    log(f"padding {shape}")
+    x = Inputs(21, *shape, padding=shape[1] * 9 // 10)
+    out = x.run()
+    compare(out, x.want(), f"{shape}")
+    assert not f64(out["O"])[x.mp < 0].any() and not f64(out["dQ"])[x.mp < 0].any()
+
+
 def test_strided_tensors():
     """Queries and gradients with tokens before heads, K and V out of one projection, K shared by all users, an
     expanded upstream gradient."""
