@@ -4,8 +4,12 @@
 // Block 0 groups with a stable counting sort: a wave takes a run of candidates, 64 to a turn.  The lanes with the same
 // key are found from ballots of the key's bits, whatever the map looks like.  Where queries have positions, the key is the
 // user and a step of the candidate's position in the history, as many steps as LDS has counts for: rows that see about
-// as many tokens then stand together, and their tiles end there (23 users, 8001 candidates: causal forward CAUSAL_FWD).  The other blocks look for
-// candidates whose map entry is no user, and write their O = 0 and lse = -inf, or dQ = 0.
+// as many tokens then stand together, and their tiles end there (23 users, 8001 candidates: the grouping 10 -> 13 us,
+// forward 80 -> 63, dQ 115 -> 89, dK and dV 122 -> 104).  The other blocks look for candidates whose map entry is no user,
+// and write their O = 0 and lse = -inf, or dQ = 0.
+//
+// It is bound by latency: one block, and a dozen steps that wait for one another.  1024 candidates of 15 users 8 us, 8001 of
+// 23 with positions 14.5, of which putting the tiles in order is 1.3.
 #include <algorithm>
 
 #include "train_device.h"
