@@ -50,7 +50,7 @@ int check(const ikbo_attention_args *a, bool backward) {
     const bool rows = a->B_c > 0;
     if (!a->status || !a->workspace || a->workspace_bytes < need || (a->dropout > 0 && !a->rng)) return IKBO_ERR_INVALID_ARG;
     if (rows && (!a->Q || !a->K || !a->V || !a->O || !a->lse || !a->map)) return IKBO_ERR_INVALID_ARG;
-    if (backward && (!a->dK || !a->dV || (rows && (!a->dO || !a->dQ)))) return IKBO_ERR_INVALID_ARG;
+    if (backward && (!a->K || !a->V || !a->dK || !a->dV || (rows && (!a->dO || !a->dQ)))) return IKBO_ERR_INVALID_ARG;
     for (const void *p : {a->Q, a->K, a->V, (const void *)a->O, (const void *)a->workspace})
         if (!aligned(p, 16)) return IKBO_ERR_ALIGNMENT;
     if (backward)

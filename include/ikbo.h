@@ -446,6 +446,7 @@ int ikbo_kv4_attention(const ikbo_kv4_attention_args *args, void *stream);
  * 2^24 elements apart, 4 L_kv and 4 B_c L_q H_q below 2^31, and no more blocks than a launch holds, else UNSUPPORTED.
  * workspace: ikbo_attention_workspace bytes, 16-byte aligned, not shared with a call that may overlap; nothing in it has
  * to be kept between calls.
+ * Without candidates the forward does nothing; the backward writes dK = dV = 0, and needs K and V but no tensor of the candidates.
  */
 typedef struct ikbo_attention_args {
     const void *Q, *K, *V;

@@ -80,6 +80,12 @@ def test_backward_refusals(L, change, want):
     assert L.ikbo_attention_backward(None, None) == INVALID
 
 
+@pytest.mark.parametrize("change", [dict(K=0), dict(V=0), dict(K=0, V=0)])
+def test_gradients_without_candidates_need_the_users_keys(L, change):
+    """dK and dV are written all the same, by a kernel that is given K and V."""
+    assert L.ikbo_attention_backward(ctypes.byref(fill(_AttentionArgs, **{**ATTEND, "B_c": 0, **change})), None) == INVALID
+
+
 @pytest.mark.parametrize("change, want", [
     (dict(n=-1), INVALID), (dict(n=0, x=0), OK), (dict(p=-0.1), INVALID), (dict(p=1.0), INVALID), (dict(p=math.nan), INVALID), (dict(p=1e-6), INVALID),
     (dict(dtype=2), INVALID), (dict(x=0), INVALID), (dict(y=0), INVALID), (dict(rng=0), INVALID), (dict(x=P + 1), ALIGNMENT),
