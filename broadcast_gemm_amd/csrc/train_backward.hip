@@ -301,6 +301,8 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dkv_kernel(TrainArgs a) {
         rnd.init(a.rng);
         turn.lane = lane;
     }
+    // Keys behind the history and users without candidates: zeros, and nothing is read.
+    int stages = range * KEYS < len ? __builtin_amdgcn_readfirstlane(ch.notes) : 0;
     u32x4_t kf[TK], vf[V_LDS ? 1 : TK];
     f32x16_t dk[DT], dv[DT];
     {
@@ -309,14 +311,14 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dkv_kernel(TrainArgs a) {
         const uint16_t *v = a.V + u * a.v_user + hk * a.v_head + t * a.v_token + 8 * g;
 #pragma unroll
         for (int s = 0; s < TK; ++s) {
-            kf[s] = t < len ? *reinterpret_cast<const u32x4_t *>(k + 16 * s) : (u32x4_t){0, 0, 0, 0};
-            if constexpr (!V_LDS) vf[s] = t < len ? *reinterpret_cast<const u32x4_t *>(v + 16 * s) : (u32x4_t){0, 0, 0, 0};
+            kf[s] = stages > 0 && t < len ? *reinterpret_cast<const u32x4_t *>(k + 16 * s) : (u32x4_t){0, 0, 0, 0};
+            if constexpr (!V_LDS) vf[s] = stages > 0 && t < len ? *reinterpret_cast<const u32x4_t *>(v + 16 * s) : (u32x4_t){0, 0, 0, 0};
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) dk[d] = dv[d] = (f32x16_t)(0.f);
     }
     const char *V = v_lds + Rows<HD>::matrix(32) * wv;
-    if constexpr (V_LDS) {   // each wave its own keys
+    if (V_LDS && stages > 0) {   // each wave its own keys
         const uint16_t *v = a.V + u * a.v_user + hk * a.v_head;
 #pragma unroll
         for (int i = 0; i < 32 * HD / 8 / 64; ++i) {
@@ -329,7 +331,6 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dkv_kernel(TrainArgs a) {
     Reader<HD> rd;
     rd.init(lane);
     const uint32_t lds0 = lds_address(lds);
-    int stages = range * KEYS < len ? __builtin_amdgcn_readfirstlane(ch.notes) : 0;   // keys behind the history: zeros
     const char *from_notes = reinterpret_cast<const char *>(a.notes + (int64_t)hk * a.n_notes + __builtin_amdgcn_readfirstlane(ch.note));
     auto load_notes = [&](int n) {
 #pragma unroll
@@ -362,10 +363,10 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dkv_kernel(TrainArgs a) {
         for (int w = 0; w < WAVES; ++w) stages = max(stages, s_stages[w]);
         stages = __builtin_amdgcn_readfirstlane(stages);
     }
+    if (wv == 0 && stages > 0) load_notes(0);
+    if (wv == 0 && stages > 1) load_notes(1);
+    landed();   // also where no stage is wanted: nothing may arrive after the block
     if (stages > 0) {
-        if (wv == 0) load_notes(0);
-        if (wv == 0 && stages > 1) load_notes(1);
-        landed();
         __syncthreads();
         load(0);
     }

@@ -185,6 +185,24 @@ def test_mostly_padding(shape):
     assert not f64(out["O"])[x.mp < 0].any() and not f64(out["dQ"])[x.mp < 0].any()
 
 
+@pytest.mark.parametrize("users", [9, 70])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_keys_that_no_query_sees(users, dim):
+    """Users without candidates, ranges of keys behind every position and behind histories stand between others: zeros, and
+    nothing of the former is read."""
+    x = Inputs(users + dim, users, 80, 2, 1, 2, 700, dim, causal=True, padding=5, empty_users=True)
+    x.positions[:] = x.positions % 230
+    x.lens[1] = 700
+    k, v = x.k.cuda(), x.v.cuda()
+    none = ~np.isin(np.arange(users), x.mp)
+    k[none], v[none] = float("nan"), float("inf")
+    log(f"keys without rows: {users} users, head {dim}")
+    got = x.run(k=k, v=v)
+    compare(got, x.want(), f"{users} users, head {dim}")
+    for n in ("dK", "dV"):
+        assert none.sum() > 3 and not f64(got[n])[none].any() and not f64(got[n])[:, :, 230:].any()
+
+
 def test_strided_tensors():
     """Queries and gradients with tokens before heads, K and V out of one projection, K shared by all users, an
     expanded upstream gradient."""
