@@ -135,6 +135,7 @@ TrainLayout train_layout(int B_u, int B_c, int H_q, int H_kv, int L_q, int L_kv,
         const int64_t ranges = (L_kv + keys_of(head_dim) - 1) / keys_of(head_dim), at_once = kCus * 256 / keys_of(head_dim), work = rows * H_kv * ranges, whole = (int64_t)B_u * H_kv * ranges;
         int64_t each = std::max<int64_t>(work / (2 * at_once), 256);
         if (whole >= at_once * 3 / 4) each = std::max(each, rows * 5 / 4 / B_u);
+        each = std::min(each, rows + 1);   // more is the same, and passes 32 bits
         w.chunk_rows = w.local ? 2048 : (int)((each + 63) / 64 * 64);   // all rows of any user
         w.chunks = w.local ? B_u : (int)(rows / w.chunk_rows + B_u);
         w.slots = rows > w.chunk_rows ? (int)(2 * rows / w.chunk_rows + 1) : 0;   // n > 1 chunks of a user are more than n / 2 full ones

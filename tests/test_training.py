@@ -104,6 +104,13 @@ def test_workspace(L):
         assert f(*shape, 1) < 4 * shape[1] * shape[2] * shape[4] + (1 << 30), shape
 
 
+@pytest.mark.parametrize("B_c, L_kv, dim", [(1 << 26, 1 << 22, 64), (1 << 26, (1 << 22) - 1000, 64), (1 << 26, 3 << 21, 64), (1 << 26, 1 << 23, 64),
+                                            (1 << 26, 1 << 24, 128), (1 << 28, 1 << 24, 64), (45_000_000, 50_000, 64)])
+def test_workspace_of_many_rows_over_many_keys(L, B_c, L_kv, dim):
+    """One user's rows are not cut however many keys there are: 4 bytes of order, a quarter of a table entry and 48 bytes of notes a row."""
+    assert 52 * B_c < L.ikbo_attention_workspace(1, B_c, 1, 1, 1, L_kv, dim, 1) < 53 * B_c
+
+
 def test_generator_gives_the_published_numbers():
     """Known answers of Philox4x32 for a counter and key of zeros, with 7 rounds and 10."""
     assert [hex(x) for x in ref.philox(np.zeros(4, np.uint64), 0)] == ["0x5f6fb709", "0xd893f64", "0x4f121f81", "0x4f730a48"]
