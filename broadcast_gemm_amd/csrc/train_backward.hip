@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) train_dkv_kernel(TrainArgs a) {
     const char *from_notes = reinterpret_cast<const char *>(a.notes + (int64_t)hk * a.n_notes + __builtin_amdgcn_readfirstlane(ch.note));
     auto load_notes = [&](int n) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) load_to_lds(from_notes + n * (int)sizeof(RowNotes) + 1024 * i, 16 * lane, lds_address(&notes[n % 3]) + 1024 * i);
+        for (int i = 0; i < 3; ++i) load_to_lds(from_notes + (int64_t)n * (int)sizeof(RowNotes) + 1024 * i, 16 * lane, lds_address(&notes[n % 3]) + 1024 * i);
     };
     auto load = [&](int st) {
         const RowNotes &x = notes[st % 3];

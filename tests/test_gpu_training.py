@@ -241,6 +241,36 @@ def test_wide_offsets():
     compare(x.run(do=far(x.do)), want, "far gradients")
 
 
+def test_rows_of_one_user_whose_notes_pass_2_to_31_bytes():
+    """45 million candidates of one user, each of which sees the first of 50000 tokens: one chunk of rows, 48 bytes of notes each.
+    O is that token's V and the weights are 1, so dV is the sum of dO there, and dQ and dK are zero."""
+    t = torch()
+    n, dim = 45_000_000, 64
+    log("45 million rows")
+    bf = dict(dtype=t.bfloat16, device="cuda")
+    k, v = t.randn(1, 1, 50_000, dim, **bf), t.randn(1, 1, 50_000, dim, **bf)
+    q = t.randn(1, 1, 1, dim, **bf).expand(n, -1, -1, -1)
+    lse = (q[0, 0, 0].double() @ k[0, 0, 0].double() / 8).float().expand(n, 1, 1).contiguous()
+    do = t.zeros(n, 1, 1, dim, **bf)
+    far = [0, 1, n // 2, 43_000_000, 44_739_264, n - 65, n - 2, n - 1]    # 2^31 bytes of notes end with row 44739242
+    do[far] = t.randn(len(far), 1, 1, dim, **bf)
+    mp, positions, st = t.zeros(n, dtype=t.int32, device="cuda"), t.zeros(n, 1, dtype=t.int32, device="cuda"), word()
+    dQ, dK, dV = T().attention_backward(do, q, k, v, v[:, :, :1].expand(n, -1, -1, -1), lse, mp, st, positions=positions)
+    t.cuda.synchronize()
+    assert status(st) == bga.IKBO_OK
+    rows, size = f64(do[far]).reshape(len(far), dim), np.abs(f64(v[0, 0, 0]))
+    # A score is a float32 sum of dim products, and so is the lse given: each weight is off by their rounding, and by half a step of bf16.
+    w = 2 * (dim + 4) * ref.U24 * float((q[0, 0, 0].double() * k[0, 0, 0].double()).abs().sum()) / 8 + 2.0 ** -20
+    want, off = rows.sum(0), np.abs(rows).sum(0) * (ref.B8 + w)
+    assert (np.abs(f64(dV[0, 0, 0]) - want) <= off + ref.B8 * (np.abs(want) + off)).all()
+    assert not dV[0, 0, 1:].any()
+    # dS = P (dP - D), where D is the row's one P dP: off by P's error and twice that of dP, a float32 sum of dim products.
+    ds = (np.abs(rows) @ size) * (2 * w + 2 * (dim + 4) * ref.U24)
+    assert (np.abs(f64(dK[0, 0, 0])) <= ds.sum() / 8 * np.abs(f64(q[0, 0, 0])) * 1.01 + 1e-30).all() and not dK[0, 0, 1:].any()
+    assert float(dQ[far].abs().max()) <= ds.max() / 8 * float(k[0, 0, 0].abs().max()) * 1.01
+    assert not dQ[500::1000].any()
+
+
 def test_what_is_masked_is_not_read():
     """NaN and infinity behind the histories, in the rows of padding and in the gradients of queries that see nothing."""
     t = torch()
