@@ -24,7 +24,7 @@ angle with the same factor, the same kernel.
 
 Target attention trains through ``IkboAttention``, with dropout of its weights, and ``IkboDropout`` drops activations;
 ``IkboLce`` takes a ``dropout`` of its output.  Their masks are never stored: the backward forms them again from the
-module's counter (``training``).
+call's (seed, offset) (``training``), which is torch's to give, or the module's if it has a seed.
 
     attend = IkboAttention(dropout=0.1).cuda()
     O = attend(Q, K, V, map, lens=lens)              # Q, K, V may require grad; dK, dV at the user batch
@@ -158,12 +158,27 @@ class IkboRope(torch.nn.Module):
         return RopeFunction.apply(q, k, positions, self.freq, self.layout, self.factor)
 
 
+# Which run of autograd's engine this thread is in, -1 outside of backward passes.
+_in_backward = getattr(torch._C, "_current_graph_task_id", None) or (lambda: -1)
+
+
 class _Counter(torch.nn.Module):
-    """A module with random numbers of its own: ``rng`` (seed, offset), whose offset moves on with every call that uses them,
-    on the device, so that replays of a captured step draw new ones.  It is saved with the module's state."""
+    """A module with random numbers.
+
+    Without a seed every call takes its (seed, offset) from torch's generator of the device, on the device.  They are then
+    what torch's own dropout would have: set by ``torch.manual_seed``, new in every replay of a captured step, and the same
+    when ``torch.utils.checkpoint`` runs a forward pass again, since it restores that generator.
+
+    With a seed they are the module's own: ``rng`` (seed, offset), whose offset moves on with every call that uses them, on
+    the device, so that replays of a captured step draw new ones; it is saved with the module's state (modules without a seed
+    have it too, for states of either kind).  Nothing moves it back for a forward pass that is run again, which would
+    give gradients of another mask than the output's: within a backward pass such a module raises an error."""
+
+    _counted = True
 
     def __init__(self, seed):
         super().__init__()
+        self._counted = seed is not None
         if seed is None:   # from torch's generator: other modules have others
             seed = int(torch.randint(0, 1 << 62, ()))
         self.register_buffer("rng", torch.tensor([seed, 0], dtype=torch.int64))
@@ -172,6 +187,15 @@ class _Counter(torch.nn.Module):
         rng = self.rng.clone()
         self.rng[1:].add_(1)
         return rng
+
+    def _numbers(self, device):
+        """(seed, offset) of one call."""
+        if not self._counted:
+            return torch.randint(0, 1 << 62, (2,), device=device)
+        if _in_backward() != -1:
+            raise RuntimeError("a module with a seed of its own cannot repeat its random numbers in a forward pass that is run again for the "
+                               "backward (activation checkpointing); leave seed=None there")
+        return self._draw()
 
 
 def _probability(p: float, of: int) -> float:
@@ -206,7 +230,7 @@ class IkboDropout(_Counter):
 
     def forward(self, x, residual=None):
         if self.training and self.p:
-            return DropoutFunction.apply(x, residual, self.p, self._draw())
+            return DropoutFunction.apply(x, residual, self.p, self._numbers(x.device))
         return x if residual is None else residual + x
 
 
@@ -256,7 +280,7 @@ class IkboAttention(_Counter):
     def forward(self, Q, K, V, mp, lens=None, positions=None):
         i32 = [None if t is None else t.to(torch.int32).contiguous() for t in (mp, lens, positions)]
         drop = self.dropout if self.training else 0.0
-        return AttentionFunction.apply(Q, K, V, *i32, self.scale, drop, self._draw() if drop else None, self.status)
+        return AttentionFunction.apply(Q, K, V, *i32, self.scale, drop, self._numbers(Q.device) if drop else None, self.status)
 
     def check(self, stream=None) -> int:
         return history.kv_status(self.status, stream)

@@ -626,3 +626,64 @@ def test_a_captured_training_step_draws_new_numbers():
         assert t.equal(O, O2) and all(t.equal(a, b) for a, b in zip(grads, want))
         seen.append(O.clone())
     assert not t.equal(seen[0], seen[1]) and not t.equal(seen[1], seen[2])
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_gradients_under_activation_checkpointing(reentrant):
+    """Two layers of attention, dropout and the LCE, whose forward runs again in the backward: the same outputs and gradients as without,
+    from the same state of torch's generator."""
+    t = torch()
+    from torch.utils.checkpoint import checkpoint
+    from broadcast_gemm_amd.autograd import IkboAttention, IkboDropout, IkboLce
+    x = Inputs(23, 3, 12, 4, 2, 8, 60, 64, padding=2)
+    attend, drop, lce = IkboAttention(dropout=0.2).cuda(), IkboDropout(0.25).cuda(), IkboLce(10, 32, 32, 64, dropout=0.1).cuda()
+    mp, lens = dev(x.mp), dev(x.lens)
+    users = mp.clamp(min=0)
+    U, dY = t.randn(3, 10, 64, device="cuda").to(t.bfloat16), x.do.cuda()
+    log(f"checkpointing, reentrant={reentrant}")
+
+    def layer(q, k, v):
+        y = drop(attend(q, k, v, mp, lens=lens), q)
+        return lce(U, y.reshape(12, 32, 64), users).view(12, 4, 8, 64)
+
+    def step(call):
+        t.manual_seed(31)
+        leaves = [y.cuda().requires_grad_() for y in (x.q, x.k, x.v)]
+        lce.W_u.grad = lce.W_c.grad = None
+        Y = call(call(*leaves), *leaves[1:])
+        Y.backward(dY)
+        return [Y.detach()] + [y.grad for y in leaves + [lce.W_u, lce.W_c]]
+
+    want = step(layer)
+    got = step(lambda *a: checkpoint(layer, *a, use_reentrant=reentrant))
+    t.cuda.synchronize()
+    assert attend.check() == bga.IKBO_OK
+    assert all(t.equal(a, b) for a, b in zip(got, want))
+    assert not t.equal(layer(*(y.cuda() for y in (x.q, x.k, x.v))), layer(*(y.cuda() for y in (x.q, x.k, x.v))))
+    lce._plans.close()
+
+
+def test_a_captured_step_takes_numbers_from_torch():
+    """Every replay has another mask, and its gradient the same mask as its output."""
+    t = torch()
+    from broadcast_gemm_amd.autograd import IkboDropout
+    drop = IkboDropout(0.5).cuda()
+    x, dy = t.ones(4099, device="cuda").requires_grad_(), t.full((4099,), 3.0, device="cuda")
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        t.autograd.grad(drop(x), x, dy)
+    t.cuda.current_stream().wait_stream(side)
+    t.cuda.synchronize()
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        y = drop(x)
+        dx, = t.autograd.grad(y, x, dy)
+    seen = []
+    for _ in range(4):
+        g.replay()
+        t.cuda.synchronize()
+        assert set(y.unique().tolist()) == {0.0, 2.0} and t.equal(dx, 3 * y)
+        seen.append(y.detach().clone())
+        seen.append(drop(x).detach())   # eager calls between the replays
+    assert all(not t.equal(a, b) for i, a in enumerate(seen) for b in seen[:i])

@@ -173,6 +173,26 @@ def test_modules_refuse_probabilities_and_keep_their_counters():
     assert IkboLce(8, 8, 4, 32).drop is None and IkboLce(8, 8, 4, 32, dropout=0.1).drop.p == 0.1
 
 
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_a_forward_pass_that_is_run_again_draws_the_same_numbers(reentrant):
+    from torch.utils.checkpoint import checkpoint
+    drop, seeded, drawn = IkboDropout(0.5), IkboDropout(0.5, seed=3), []
+
+    def layer(module, x):
+        drawn.append(module._numbers(x.device).tolist())
+        return x * x
+
+    x = torch.ones(3, requires_grad=True)
+    y = checkpoint(layer, drop, x, use_reentrant=reentrant) + checkpoint(layer, drop, 2 * x, use_reentrant=reentrant)
+    y.sum().backward()
+    assert len(drawn) == 4 and drawn[0] != drawn[1] and sorted(drawn[:2]) == sorted(drawn[2:])
+    # A counter of the module's own would have moved on: refused, in the second pass.
+    y = checkpoint(layer, seeded, x, use_reentrant=reentrant).sum()
+    with pytest.raises(RuntimeError, match="seed"):
+        y.backward()
+    assert drawn[4:] == [[3, 0]] and seeded.rng.tolist() == [3, 1]
+
+
 def test_dropout_in_evaluation_is_the_sum():
     x, r = torch.randn(5), torch.randn(5)
     d = IkboDropout(0.5).eval()
