@@ -262,6 +262,11 @@ def _rows(t):
     return t if whole and all(s % 8 == 0 for s, n in zip(t.stride()[:3], t.shape) if n > 1) else t.clone(memory_format=torch.contiguous_format)
 
 
+def _int32(t):
+    """t in 32 bits; what does not fit becomes the nearest that does, which is as far outside (a wrapped one might be a user)."""
+    return (t.clamp(-1 << 31, (1 << 31) - 1) if t.dtype == torch.int64 else t).to(torch.int32).contiguous()
+
+
 class IkboAttention(_Counter):
     """Target attention with gradients: Q [B_c, H_q, L_q, head_dim] over the K, V [B_u, H_kv, L_kv, head_dim] of the candidates'
     users, bf16.
@@ -278,7 +283,7 @@ class IkboAttention(_Counter):
         self.register_buffer("status", torch.zeros(1, dtype=torch.int32), persistent=False)
 
     def forward(self, Q, K, V, mp, lens=None, positions=None):
-        i32 = [None if t is None else t.to(torch.int32).contiguous() for t in (mp, lens, positions)]
+        i32 = [None if t is None else _int32(t) for t in (mp, lens, positions)]
         drop = self.dropout if self.training else 0.0
         return AttentionFunction.apply(Q, K, V, *i32, self.scale, drop, self._numbers(Q.device) if drop else None, self.status)
 

@@ -663,6 +663,29 @@ def test_gradients_under_activation_checkpointing(reentrant):
     lce._plans.close()
 
 
+def test_module_with_numbers_beyond_32_bits():
+    """Positions without a bound, and users and lengths that 32 bits would wrap into others, are what they are."""
+    t = torch()
+    from broadcast_gemm_amd.autograd import IkboAttention
+    x = Inputs(24, 3, 10, 2, 1, 2, 50, 64)
+    x.lens[:] = 50, 20, 50
+    attend, q, k, v = IkboAttention().cuda(), x.q.cuda(), x.k.cuda(), x.v.cuda()
+    mp, lens = dev(x.mp).long(), dev(x.lens).long()
+    log("64-bit numbers")
+    want = attend(q, k, v, mp, lens=lens)
+    assert attend.check() == bga.IKBO_OK
+    last = t.iinfo(t.int64).max
+    assert t.equal(attend(q, k, v, mp, lens=lens, positions=t.full((10, 2), last, device="cuda")), want)
+    assert not attend(q, k, v, mp, lens=lens, positions=t.full((10, 2), -last, device="cuda")).any()
+    assert attend.check() == bga.IKBO_OK
+    far = mp.clone()
+    far[3] += 1 << 32
+    got = attend(q, k, v, far, lens=lens)
+    assert attend.check() == bga.IKBO_ERR_MAP_RANGE and not got[3].any() and t.equal(got[:3], want[:3]) and t.equal(got[4:], want[4:])
+    lens[0] += 1 << 32
+    assert t.equal(attend(q, k, v, mp, lens=lens), want) and attend.check() == bga.IKBO_ERR_PAGE_RANGE
+
+
 def test_a_captured_step_takes_numbers_from_torch():
     """Every replay has another mask, and its gradient the same mask as its output."""
     t = torch()

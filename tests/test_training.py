@@ -206,3 +206,10 @@ def test_tensors_on_the_host_are_refused():
         training.attention(x, x, x, torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError):
         training.dropout(x, 0.1, torch.zeros(2, dtype=torch.int64))
+
+
+def test_numbers_of_64_bits_are_not_wrapped():
+    from broadcast_gemm_amd.autograd import _int32
+    t = torch.tensor([[-1 << 63, -(1 << 32) - 1, -1], [1 << 32, (1 << 63) - 1, 7]])
+    assert _int32(t).tolist() == [[-1 << 31, -1 << 31, -1], [(1 << 31) - 1, (1 << 31) - 1, 7]] and _int32(t.t()).is_contiguous()
+    assert _int32(t.to(torch.int32)).dtype == torch.int32 and _int32(torch.tensor([3, 250], dtype=torch.uint8)).tolist() == [3, 250]
