@@ -222,16 +222,21 @@ class DropoutFunction(torch.autograd.Function):
 class IkboDropout(_Counter):
     """x with ``p`` of its elements dropped and the others divided by 1 - p, added to ``residual`` if that is given.
 
-    bf16 or float32 on the GPU; p in whole 65536ths (the nearest).  In evaluation nothing is dropped."""
+    bf16 or float32 on the GPU; p in whole 65536ths (the nearest).  In evaluation nothing is dropped.  A residual of x's shape
+    and type is added in the same kernel and the sum rounded once; any other that can be added to x is added to what the
+    dropout rounded."""
 
     def __init__(self, p: float, seed=None):
         super().__init__(seed)
         self.p = _probability(p, 65536)
 
     def forward(self, x, residual=None):
-        if self.training and self.p:
-            return DropoutFunction.apply(x, residual, self.p, self._numbers(x.device))
-        return x if residual is None else residual + x
+        if not (self.training and self.p):
+            return x if residual is None else residual + x
+        rng = self._numbers(x.device)
+        if residual is None or (torch.is_tensor(residual) and residual.shape == x.shape and residual.dtype == x.dtype):
+            return DropoutFunction.apply(x, residual, self.p, rng)
+        return residual + DropoutFunction.apply(x, None, self.p, rng)
 
 
 class AttentionFunction(torch.autograd.Function):

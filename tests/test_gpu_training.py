@@ -663,6 +663,31 @@ def test_gradients_under_activation_checkpointing(reentrant):
     lce._plans.close()
 
 
+@pytest.mark.parametrize("kind", ["row", "float32", "wider", "number"])
+def test_residuals_that_are_not_like_the_activations(kind):
+    """What evaluation adds, training adds too: of another shape or type, with gradients in the residual's shape."""
+    t = torch()
+    from broadcast_gemm_amd.autograd import IkboDropout
+    g = t.Generator(device="cuda").manual_seed(2)
+    x = t.randn(6, 35, generator=g, device="cuda").to(t.bfloat16).requires_grad_()
+    shape = dict(row=(35,), float32=(6, 35), wider=(3, 6, 35), number=())[kind]
+    r = t.randn(shape, generator=g, device="cuda").to(t.float32 if kind == "float32" else t.bfloat16).requires_grad_()
+    r = 0.5 if kind == "number" else r
+    drop = IkboDropout(0.25, seed=4).cuda()
+    log(f"residual {kind}")
+    y = drop(x, r)
+    kept = T().dropout(x.detach(), 0.25, t.tensor([4, 0], device="cuda"))
+    assert t.equal(y, r + kept)
+    dy = t.randn(y.shape, generator=g, device="cuda").to(y.dtype)
+    y.backward(dy)
+    dx = dy.sum(0) if kind == "wider" else dy.to(x.dtype)
+    assert t.equal(x.grad, T().dropout(dx, 0.25, t.tensor([4, 0], device="cuda")))
+    if kind != "number":
+        assert t.equal(r.grad, dy.sum(0) if kind == "row" else dy)
+    z = drop.eval()(x, r)
+    assert z.shape == y.shape and z.dtype == y.dtype
+
+
 def test_module_with_numbers_beyond_32_bits():
     """Positions without a bound, and users and lengths that 32 bits would wrap into others, are what they are."""
     t = torch()
