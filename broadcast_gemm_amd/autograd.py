@@ -171,8 +171,9 @@ class _Counter(torch.nn.Module):
 
     With a seed they are the module's own: ``rng`` (seed, offset), whose offset moves on with every call that uses them, on
     the device, so that replays of a captured step draw new ones; it is saved with the module's state (modules without a seed
-    have it too, for states of either kind).  Nothing moves it back for a forward pass that is run again, which would
-    give gradients of another mask than the output's: within a backward pass such a module raises an error."""
+    have it too, for states of either kind).  A copy of the module, and ranks whose buffers a wrapper keeps alike, draw the same
+    ones.  Nothing moves it back for a forward pass that is run again, which would give gradients of another mask than the
+    output's: within a backward pass such a module raises an error."""
 
     _counted = True
 
@@ -285,7 +286,15 @@ class IkboAttention(_Counter):
     def __init__(self, dropout: float = 0.0, scale: float = 0.0, seed=None):
         super().__init__(seed)
         self.dropout, self.scale = _probability(dropout, 256), float(scale)
-        self.register_buffer("status", torch.zeros(1, dtype=torch.int32), persistent=False)
+        # Not a buffer: wrappers that give all ranks the first one's buffers would write over what was recorded.
+        self.status = torch.zeros(1, dtype=torch.int32)
+
+    def _apply(self, fn, *args, **kwargs):
+        super()._apply(fn, *args, **kwargs)
+        device, old = fn(torch.empty(0, dtype=torch.int32, device=self.status.device)).device, self.status
+        if device != old.device:   # moved alone, and not cast
+            self.status = torch.zeros(1, dtype=torch.int32, device=device) if old.is_meta else old.to(device)
+        return self
 
     def forward(self, Q, K, V, mp, lens=None, positions=None):
         i32 = [None if t is None else _int32(t) for t in (mp, lens, positions)]

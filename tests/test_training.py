@@ -213,3 +213,16 @@ def test_numbers_of_64_bits_are_not_wrapped():
     t = torch.tensor([[-1 << 63, -(1 << 32) - 1, -1], [1 << 32, (1 << 63) - 1, 7]])
     assert _int32(t).tolist() == [[-1 << 31, -1 << 31, -1], [(1 << 31) - 1, (1 << 31) - 1, 7]] and _int32(t.t()).is_contiguous()
     assert _int32(t.to(torch.int32)).dtype == torch.int32 and _int32(torch.tensor([3, 250], dtype=torch.uint8)).tolist() == [3, 250]
+
+
+def test_status_is_the_modules_own():
+    """It moves with the module and is neither cast, saved, nor among the buffers that a wrapper broadcasts between ranks."""
+    import copy
+    m = torch.nn.Sequential(IkboAttention(dropout=0.1), torch.nn.Linear(2, 2))
+    assert set(dict(m.named_buffers())) == {"0.rng"} and "0.status" not in m.state_dict()
+    m[0].status[0] = 2
+    assert m.bfloat16().double()[0].status.tolist() == [2] and m[0].status.dtype == torch.int32
+    other = copy.deepcopy(m)
+    other[0].status.zero_()
+    assert m[0].status.tolist() == [2]
+    assert m.to("meta")[0].status.is_meta and m.to_empty(device="cpu")[0].status.tolist() == [0]
