@@ -663,6 +663,41 @@ def test_gradients_under_activation_checkpointing(reentrant):
     lce._plans.close()
 
 
+@pytest.mark.parametrize("shape", [(3, 12, 10, 32, 8, 64), (15, 200, 40, 64, 96, 160), (1, 1, 8, 8, 5, 128)])
+def test_lce_with_dropout(shape):
+    """Output and gradients are those of the LCE without dropout and of the dropout, one behind the other, with the same numbers."""
+    t = torch()
+    from broadcast_gemm_amd.autograd import IkboLce
+    B_u, B_c, K_u, K_c, M, D = shape
+    g = t.Generator(device="cuda").manual_seed(3)
+    U, C, dY = (t.randn(*s, generator=g, device="cuda").to(t.bfloat16) for s in ((B_u, K_u, D), (B_c, K_c, D), (B_c, M, D)))
+    mp = t.randint(0, B_u, (B_c,), generator=g, device="cuda")
+    lce = IkboLce(K_u, K_c, M, D, dropout=0.1).cuda()
+    log(f"LCE with dropout {shape}")
+
+    def step(dY):
+        for y in (U, C, lce.W_u, lce.W_c):
+            y.grad = None
+            y.requires_grad_()
+        Y = lce(U, C, mp)
+        Y.backward(dY)
+        return Y.detach(), [y.grad for y in (U, C, lce.W_u, lce.W_c)]
+
+    t.manual_seed(17)
+    Y, grads = step(dY)
+    t.manual_seed(17)
+    rng = t.randint(0, 1 << 62, (2,), device="cuda")         # what the call took
+    lce.eval()
+    plain, want = step(T().dropout(dY, 0.1, rng))
+    kept = ref.elements_kept(Y.numel(), 0.1, rng.tolist()).reshape(Y.shape)
+    assert 0 < kept.mean() < 1 and not f64(Y)[~kept].any()
+    # The factor and the product round in float32, and then bf16 does.
+    exact = np.where(kept, f64(plain) / (1 - round(65536 * 0.1) / 65536), 0.0)
+    assert (np.abs(f64(Y) - exact) <= np.abs(exact) * (ref.B8 + 3 * ref.U24)).all()
+    assert all(t.equal(a, b) and a.any() for a, b in zip(grads, want))
+    lce._plans.close()
+
+
 @pytest.mark.parametrize("kind", ["row", "float32", "wider", "number"])
 def test_residuals_that_are_not_like_the_activations(kind):
     """What evaluation adds, training adds too: of another shape or type, with gradients in the residual's shape."""
