@@ -17,8 +17,8 @@
 // bytes an element for every range.  P and dS are rounded to bf16 for their products (half a step each, as the outputs); all
 // sums are float32.
 //
-// Measured, with the batch of the forward (15 users, 1024 candidates of 64 queries, 4 heads of 128): dQ 211 us, dK and dV
-// 253, which is 860 and 954 TFLOP/s of their own products (3 and 4 of them).  Both stand two waves to a SIMD with all 256
+// Measured, with the batch of the forward (15 users, 1024 candidates of 64 queries, 4 heads of 128): dQ 211 to 214 us, dK
+// and dV 253 to 257, by the card: 850 and 945 TFLOP/s of their own products (3 and 4 of them).  Both stand two waves to a SIMD with nearly all 256
 // registers, and are bound by that: a wave's products wait for its own exponentials and LDS reads (256 bytes a cycle, no
 // conflicts), and only one other wave fills the time.  What made the difference: V in LDS for dK and dV, for two waves on
 // a SIMD instead of one (921 -> 407 us); no spilled register in the loop, as a reload waits for all loads of the next

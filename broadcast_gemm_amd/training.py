@@ -57,7 +57,7 @@ def attention_backward(dO, Q, K, V, O, lse, mp, status, lens=None, positions=Non
     """(dQ, dK, dV) of the attention above for the upstream gradient dO (``ikbo_attention_backward``).
 
     The other arguments are those of the forward, O and lse its results.  dK and dV are summed over the user's candidates,
-    their queries and the heads that share a head; users without candidates and tokens behind a history get zeros."""
+    their queries and the heads that share a head; users without candidates and tokens behind a history get zeros.  All three are computed, whichever are wanted."""
     return _status_of(_run(_device(Q), stream, _training().attention_backward, dO, Q, K, V, O, lse, mp, status, lens, positions, scale,
                            dropout, rng), "ikbo_attention_backward")
 
