@@ -299,7 +299,9 @@ class IkboAttention(_Counter):
     def forward(self, Q, K, V, mp, lens=None, positions=None):
         i32 = [None if t is None else _int32(t) for t in (mp, lens, positions)]
         drop = self.dropout if self.training else 0.0
-        return AttentionFunction.apply(Q, K, V, *i32, self.scale, drop, self._numbers(Q.device) if drop else None, self.status)
+        # A replica on another device (torch.nn.DataParallel) has the original's word, which only buffers would follow.
+        status = self.status.to(Q.device) if getattr(self, "_is_replica", False) else self.status
+        return AttentionFunction.apply(Q, K, V, *i32, self.scale, drop, self._numbers(Q.device) if drop else None, status)
 
     def check(self, stream=None) -> int:
         return history.kv_status(self.status, stream)

@@ -746,6 +746,17 @@ def test_module_with_numbers_beyond_32_bits():
     assert t.equal(attend(q, k, v, mp, lens=lens), want) and attend.check() == bga.IKBO_ERR_PAGE_RANGE
 
 
+def test_a_replica_on_another_device_than_its_original():
+    """As torch.nn.DataParallel makes them: a status word that has not followed is copied; a module that was never moved is refused."""
+    from broadcast_gemm_amd.autograd import IkboAttention
+    x = Inputs(25, 2, 5, 2, 1, 2, 40, 64, ragged=False)
+    here, there = IkboAttention().cuda(), IkboAttention()
+    args = x.q.cuda(), x.k.cuda(), x.v.cuda(), dev(x.mp)
+    assert torch().equal(there._replicate_for_data_parallel()(*args), here(*args))
+    with pytest.raises(ValueError):
+        there(*args)
+
+
 def test_a_captured_step_takes_numbers_from_torch():
     """Every replay has another mask, and its gradient the same mask as its output."""
     t = torch()
